@@ -9,9 +9,12 @@ Raw entry points (same names and argument order as the C ABI, pointers as
 ints):  ``fa_fwd``, ``fa_fwd_fp8``, ``fa_bwd``, ``fa_bwd_workspace_size``, the three phases
 of ``fa_bwd`` (``fa_bwd_preprocess``, ``fa_bwd_dkdv``, ``fa_bwd_dq_convert``),
 the split-KV decode forward (``fa_fwd_splitkv``,
-``fa_fwd_splitkv_workspace_size``), ``fa_get_device_status``,
-``fa_status_string``.
-Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`.
+``fa_fwd_splitkv_workspace_size``), the norm and rotation of queries and keys
+(``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
+``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``),
+``fa_get_device_status``, ``fa_status_string``.
+Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`,
+:func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`.
 """
 
 from __future__ import annotations
@@ -24,9 +27,11 @@ __all__ = [
     "fa_fwd_dropout", "fa_bwd_dropout",
     "fa_bwd_preprocess", "fa_bwd_dkdv", "fa_bwd_dq_convert", "fa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES",
     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "decode_forward",
+    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
+    "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "paged_append",
     "fa_get_device_status", "fa_status_string", "forward", "backward", "EXPORTED_SYMBOLS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_WORKSPACE", "FA_ERR_CUDA",
-    "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INTERNAL",
+    "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INTERNAL", "FA_ERR_DEVICE_INDEX",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
@@ -38,11 +43,13 @@ FA_ERR_WORKSPACE = 3
 FA_ERR_CUDA = 4
 FA_ERR_DEVICE_TIMEOUT = 5
 FA_ERR_INTERNAL = 6
+FA_ERR_DEVICE_INDEX = 7
 
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_fp8", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_deterministic", "fa_fwd_dropout",
                     "fa_bwd_dropout", "fa_bwd_preprocess",
                     "fa_bwd_dkdv",
                     "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size",
+                    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
                     "fa_get_device_status", "fa_status_string")
 
 # Size of the library-owned scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES).
@@ -95,6 +102,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_splitkv.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, sz, vp]
     lib.fa_fwd_splitkv_workspace_size.restype = sz
     lib.fa_fwd_splitkv_workspace_size.argtypes = [i, i, i, i, i, i]
+    ll = ctypes.c_longlong
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope.argtypes = [vp] * 4 + [i] * 5 + [ll] * 6 + [i, vp, vp, i, f, vp, i, i, i, vp, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 8 + [i] * 5 + [ll] * 12 + [i, vp, vp, i, f, vp, i, i, i, vp, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_paged_append.restype = i
+    lib.fa_paged_append.argtypes = [vp] * 9 + [i] * 8 + [ll] * 12 + [i, vp, vp, i, f, vp, i, i, i, vp]
     lib.fa_get_device_status.restype = i
     lib.fa_get_device_status.argtypes = [vp]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -164,6 +180,40 @@ def fa_fwd_splitkv(q, k, v, o, lse, B, H, Nq, Nk, d, scale, causal, num_splits, 
 
 def fa_fwd_splitkv_workspace_size(B, H, Nq, Nk, d, num_splits) -> int:
     return load_library().fa_fwd_splitkv_workspace_size(B, H, Nq, Nk, d, num_splits)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, B, Hq, Hk, N, d, q_stride_b, q_stride_h, q_stride_n, k_stride_b, k_stride_h,
+                    k_stride_n, norm, q_weight, k_weight, weights_f32, eps, rope, rope_len, rope_dim, interleaved,
+                    positions, stream) -> int:
+    return load_library().fa_qk_norm_rope(q, k, q_out, k_out, B, Hq, Hk, N, d, q_stride_b, q_stride_h, q_stride_n,
+                                          k_stride_b, k_stride_h, k_stride_n, norm, q_weight, k_weight, weights_f32,
+                                          eps, rope, rope_len, rope_dim, interleaved, positions, stream)
+
+
+def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, B, Hq, Hk, N, d, q_stride_b, q_stride_h,
+                        q_stride_n, k_stride_b, k_stride_h, k_stride_n, dq_stride_b, dq_stride_h, dq_stride_n,
+                        dk_stride_b, dk_stride_h, dk_stride_n, norm, q_weight, k_weight, weights_f32, eps, rope,
+                        rope_len, rope_dim, interleaved, positions, workspace, workspace_bytes, stream) -> int:
+    return load_library().fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, B, Hq, Hk, N, d,
+                                              q_stride_b, q_stride_h, q_stride_n, k_stride_b, k_stride_h, k_stride_n,
+                                              dq_stride_b, dq_stride_h, dq_stride_n, dk_stride_b, dk_stride_h,
+                                              dk_stride_n, norm, q_weight, k_weight, weights_f32, eps, rope, rope_len,
+                                              rope_dim, interleaved, positions, workspace, workspace_bytes, stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
+    return load_library().fa_qk_norm_rope_bwd_workspace_size(d)
+
+
+def fa_paged_append(q, k, v, q_out, k_pages, v_pages, page_table, cu_seqlens, kv_lens, T, S, Hq, Hk, d, num_pages,
+                    page_size, max_pages, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
+                    kp_stride_p, kp_stride_h, kp_stride_r, vp_stride_p, vp_stride_h, vp_stride_r, norm, q_weight,
+                    k_weight, weights_f32, eps, rope, rope_len, rope_dim, interleaved, stream) -> int:
+    return load_library().fa_paged_append(q, k, v, q_out, k_pages, v_pages, page_table, cu_seqlens, kv_lens, T, S, Hq,
+                                          Hk, d, num_pages, page_size, max_pages, q_stride_t, q_stride_h, k_stride_t,
+                                          k_stride_h, v_stride_t, v_stride_h, kp_stride_p, kp_stride_h, kp_stride_r,
+                                          vp_stride_p, vp_stride_h, vp_stride_r, norm, q_weight, k_weight,
+                                          weights_f32, eps, rope, rope_len, rope_dim, interleaved, stream)
 
 
 def fa_get_device_status(stream) -> int:
@@ -287,3 +337,194 @@ def decode_forward(q, k, v, scale=None, causal=True, num_splits=0, out=None, lse
     if st != FA_OK:
         raise FaError(st, "fa_fwd_splitkv")
     return o, l
+
+
+# ------------------------------------------------ norm, rotation and paged cache ----
+def _strided(t, name, shape, dtype):
+    """A CUDA tensor of this type and shape (None: any size) whose last dimension is contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t
+
+
+def _steps(t, dims):
+    """Strides of ``dims``; where a size is below 2 the stride means nothing and any valid one will do."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else t.shape[-1] for i in dims)
+
+
+class _On:
+    """Run on the tensors' device and on ``stream`` (None: that device's current one): what a helper allocates inside
+    belongs to that stream."""
+
+    def __init__(self, device, stream, *tensors):
+        import torch
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"every tensor must be on {device}, got one on {t.device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        self.guards = []
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
+        elif device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+
+    def __enter__(self):
+        import torch
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved):
+    """The shared trailing arguments of the norm-and-rotation calls, checked."""
+    import torch
+    wt = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if wt is not None and w.dtype != wt:
+            raise ValueError("q_weight and k_weight must have one type")
+        wt = w.dtype if w.dtype in (torch.float32, torch.bfloat16) else torch.bfloat16
+        _check(w, name, (d,), wt)
+    rope_len = rope_dim = 0
+    if rope is not None:
+        _strided(rope, "rope", (None, None), torch.float32)
+        _check(rope, "rope", rope.shape, torch.float32)
+        rope_len, rope_dim = rope.shape
+    return (int(bool(norm)), _ptr(q_weight), _ptr(k_weight), int(wt == torch.float32), float(eps), _ptr(rope),
+            rope_len, rope_dim, int(bool(interleaved)))
+
+
+def rope_table(length, rope_dim, base=10000.0, device="cuda"):
+    """Rotation table ``[length, rope_dim]`` fp32 of the angles ``p * base ** (-2 i / rope_dim)``: row p holds the
+    ``rope_dim / 2`` cosines, then the sines.  Angles are formed in fp64 (in fp32 they lose bits at far positions).
+    A program makes it once; any table of that layout (scaled frequencies, say) serves as well."""
+    import torch
+    if length < 1 or rope_dim < 2 or rope_dim % 2:
+        raise ValueError("length must be >= 1 and rope_dim a positive even number")
+    i = torch.arange(rope_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * float(base) ** (-2.0 * i / rope_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6, interleaved=False,
+                 norm=True, out=None, stream=None):
+    """Norm of queries and keys for each head, then rotation: ``q [B, Hq, N, d]``, ``k [B, Hk, N, d]`` bf16 of any
+    strides (``x.transpose(1, 2)`` of a token-major projection, a slice of a wider row) -> contiguous
+    ``(q_out, k_out)``, what :func:`forward` takes.  ``rope`` is a :func:`rope_table` (None: no rotation),
+    ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only."""
+    import torch
+    bf16 = torch.bfloat16
+    _strided(q, "q", (None, None, None, None), bf16)
+    B, Hq, N, d = q.shape
+    _strided(k, "k", (B, None, N, d), bf16)
+    Hk = k.shape[1]
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
+    if positions is not None:
+        _check(positions, "positions", (B, N), torch.int32)
+    with _On(q.device, stream, k, q_weight, k_weight, rope, positions, *(out or ())) as s:
+        q_out, k_out = out if out is not None else (torch.empty((B, h, N, d), dtype=bf16, device=q.device)
+                                                    for h in (Hq, Hk))
+        _check(q_out, "q_out", (B, Hq, N, d), bf16)
+        _check(k_out, "k_out", (B, Hk, N, d), bf16)
+        st = fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d,
+                             *_steps(q, (0, 1, 2)), *_steps(k, (0, 1, 2)), *args, _ptr(positions), s)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
+                          interleaved=False, norm=True, grads=None, weight_grads=True, workspace=None, stream=None):
+    """Gradients ``(dq, dk, dq_weight, dk_weight)`` of :func:`qk_norm_rope` from those of its outputs
+    (:func:`backward`'s ``dq, dk``).  ``dq, dk`` have q's and k's shapes, token-major in memory
+    (``[B, N, H, d]``) unless ``grads=(dq, dk)`` gives tensors of any strides.  The weights' gradients are
+    fp32 ``[d]`` (None with ``norm=False`` or ``weight_grads=False``)."""
+    import torch
+    bf16 = torch.bfloat16
+    _strided(q, "q", (None, None, None, None), bf16)
+    B, Hq, N, d = q.shape
+    _strided(k, "k", (B, None, N, d), bf16)
+    Hk = k.shape[1]
+    _check(dq_out, "dq_out", (B, Hq, N, d), bf16)
+    _check(dk_out, "dk_out", (B, Hk, N, d), bf16)
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
+    if positions is not None:
+        _check(positions, "positions", (B, N), torch.int32)
+    with _On(q.device, stream, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace,
+             *(grads or ())) as s:
+        if grads is None:
+            grads = tuple(torch.empty((B, N, h, d), dtype=bf16, device=q.device).transpose(1, 2) for h in (Hq, Hk))
+        dq, dk = grads
+        _strided(dq, "dq", (B, Hq, N, d), bf16)
+        _strided(dk, "dk", (B, Hk, N, d), bf16)
+        dqw = dkw = None
+        if norm and weight_grads:
+            dqw, dkw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(fa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        st = fa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
+                                 dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, Hq, Hk, N, d, *_steps(q, (0, 1, 2)),
+                                 *_steps(k, (0, 1, 2)), *_steps(dq, (0, 1, 2)), *_steps(dk, (0, 1, 2)), *args,
+                                 _ptr(positions), _ptr(workspace), wbytes, s)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
+def _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d):
+    """Checks of the paged cache's tensors: ``(S, num_pages, page_size, max_pages, strides)``."""
+    import torch
+    _strided(k_pages, "k_pages", (None, Hk, None, d), torch.bfloat16)
+    _strided(v_pages, "v_pages", k_pages.shape, torch.bfloat16)
+    _strided(page_table, "page_table", (None, None), torch.int32)
+    S = page_table.shape[0]
+    _check(page_table, "page_table", page_table.shape, torch.int32)
+    _check(cu_seqlens, "cu_seqlens", (S + 1,), torch.int32)
+    _check(kv_lens, "kv_lens", (S,), torch.int32)
+    steps = _steps(k_pages, (0, 1, 2)) + _steps(v_pages, (0, 1, 2))
+    return S, k_pages.shape[0], k_pages.shape[2], page_table.shape[1], steps
+
+
+def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight=None, k_weight=None, rope=None,
+                 eps=1e-6, interleaved=False, norm=True, out=None, stream=None):
+    """Norm and rotate the new tokens' ``q [T, Hq, d]`` and ``k [T, Hk, d]`` at their positions, write keys and values
+    into the cache ``k_pages, v_pages [num_pages, Hk, page_size, d]`` (any strides: a token-major pool is a
+    ``transpose(1, 2)`` view), and return the queries ``[T, Hq, d]`` for :func:`paged_forward`.
+    ``page_table [S, max_pages]``, ``cu_seqlens [S + 1]`` and ``kv_lens [S]`` (new tokens included) are int32 on
+    the device.  ``rope=None, norm=False`` caches k and v as they are."""
+    import torch
+    bf16 = torch.bfloat16
+    _strided(q, "q", (None, None, None), bf16)
+    T, Hq, d = q.shape
+    _strided(k, "k", (T, None, d), bf16)
+    Hk = k.shape[1]
+    _strided(v, "v", (T, Hk, d), bf16)
+    S, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d)
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
+    with _On(q.device, stream, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight, k_weight, rope,
+             out) as s:
+        q_out = torch.empty((T, Hq, d), dtype=bf16, device=q.device) if out is None else out
+        _check(q_out, "out", (T, Hq, d), bf16)
+        st = fa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+                             v_pages.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(), T,
+                             S, Hq, Hk, d, num_pages, page_size, max_pages, *_steps(q, (0, 1)), *_steps(k, (0, 1)),
+                             *_steps(v, (0, 1)), *steps, *args, s)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_append")
+    return q_out

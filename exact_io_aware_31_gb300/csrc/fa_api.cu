@@ -12,6 +12,7 @@
 #include "../../include/fa.h"
 #include "fa_common.cuh"
 #include "fa_context.h"
+#include "fa_host.h"
 #include "fa_kernels.h"
 
 namespace fa {
@@ -24,14 +25,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// Facts about the current device plus the status word's address in the
-// current context.
-struct DeviceInfo {
-  int sms = 0;
-  bool sm103 = false;
-  int* status = nullptr;  // device address of g_device_status in the current context
-};
-
 struct DeviceProps {
   bool ready = false;
   int sms = 0;
@@ -42,6 +35,10 @@ std::mutex g_mu;
 DeviceProps g_dev[kMaxDevices];
 PerContextAddress g_status_addr;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return g_encode; }
 
 // Device properties are resolved once per device; the status word's address
 // once per context (a device address is only valid in the context that gave
@@ -89,6 +86,8 @@ int device_info(DeviceInfo* out) {
   return FA_OK;
 }
 
+namespace {
+
 // [B*H, N, d] bf16 viewed as a 3-D tensor; box_rows-row x 64-column boxes
 // (128 unless given), 128-byte swizzle (the layout the tcgen05 descriptors
 // expect).
@@ -129,8 +128,6 @@ int make_map_e4m3(CUtensorMap* m, const void* base, int BH, int N, int d) {
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int check_sizes(int B, int H, int N, int d, float scale, int causal) {
   if (B < 1 || H < 1 || N < 1) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
@@ -141,18 +138,6 @@ int check_sizes(int B, int H, int N, int d, float scale, int causal) {
   if (bh * npad * (d > 0 ? d : 1) >= (1ll << 31)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   return FA_OK;
-}
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// scale * log2(e), its magnitude floored at 1e-30 so that a masked score
-// (-inf) times |c2| stays -inf when scale == 0.  For finite scores |s| < 1e8
-// the floor changes 2^(s * c2) by less than one fp32 ulp of 1, so scale == 0
-// still gives exact uniform attention.  The sign is kept: the tensor-core
-// kernels compute S negated for a negative scale and use |c2| after it.
-float log2_scale(float scale) {
-  const float c2 = scale * 1.4426950408889634f;
-  return std::fabs(c2) > 1e-30f ? c2 : std::copysign(1e-30f, c2);
 }
 
 struct WorkspaceLayout {
@@ -599,6 +584,8 @@ extern "C" const char* fa_status_string(int status) {
       return "FA_ERR_DEVICE_TIMEOUT: a kernel gave up on a bounded wait";
     case FA_ERR_INTERNAL:
       return "FA_ERR_INTERNAL: a kernel found an internal layout assumption violated";
+    case FA_ERR_DEVICE_INDEX:
+      return "FA_ERR_DEVICE_INDEX: a position, page or length lies outside its table";
     default:
       return "unknown fa status";
   }

@@ -61,7 +61,8 @@ typedef enum {
   FA_ERR_WORKSPACE = 3,       /* workspace missing or smaller than required */
   FA_ERR_CUDA = 4,            /* a CUDA runtime/driver call or launch failed */
   FA_ERR_DEVICE_TIMEOUT = 5,  /* a kernel gave up on a bounded wait */
-  FA_ERR_INTERNAL = 6         /* a kernel found an internal layout assumption violated */
+  FA_ERR_INTERNAL = 6,        /* a kernel found an internal layout assumption violated */
+  FA_ERR_DEVICE_INDEX = 7     /* a kernel met a position, page or length outside its table */
 } fa_status_t;
 
 /*
@@ -228,6 +229,117 @@ int fa_bwd_dq_convert(void* dq, int B, int H, int N, int d, float scale, const v
                       size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Norm of queries and keys for each head with the position rotation in the
+ * same pass: from a projection's output to the operands fa_fwd reads, in one
+ * launch.  For a head row x at position p, with r = 1 / sqrt(mean(x^2) + eps):
+ *
+ *     y = w * x * r                                (norm = 1; y = x for norm = 0)
+ *     z_a = y_a c - y_b s,  z_b = y_b c + y_a s    for each pair (a, b) of columns
+ *
+ * The pairs cover columns [0, rope_dim): (i, i + rope_dim / 2), or
+ * (2i, 2i + 1) with interleaved = 1; c and s are the i-th cosine and sine of
+ * the rotation table's row p.  The other columns pass through.  Arithmetic is
+ * fp32, rounded once to bf16.
+ *
+ *   q, k      in   bf16 [B, Hq, N, d] and [B, Hk, N, d] of any strides: element
+ *                  (b, h, n, c) at b*stride_b + h*stride_h + n*stride_n + c.
+ *                  Strides are in elements, >= 0 and multiples of 8 (a
+ *                  token-major projection is stride_n = its row, stride_h = d).
+ *   q_out, k_out   out  contiguous [B, Hq, N, d], [B, Hk, N, d] bf16
+ *   q_weight, k_weight  in  [d] norm weights shared by the heads, bf16
+ *                  (weights_f32 = 0) or fp32 (1); NULL means ones
+ *   eps       finite, >= 0
+ *   rope      in   [rope_len, rope_dim] fp32: row p holds the rope_dim / 2
+ *                  cosines, then the sines, of position p's angles.  NULL
+ *                  with rope_dim = 0 (no rotation).
+ *   rope_dim  multiple of 16, 0 <= rope_dim <= d
+ *   positions in   [B, N] int32, or NULL for 0 .. N-1 (then N <= rope_len)
+ *
+ * A position outside [0, rope_len) gives a zero row (and a zero gradient row)
+ * and records FA_ERR_DEVICE_INDEX in the device status word.  Head counts may
+ * differ (grouped key heads).  Sizes are not limited to 2^31 elements here;
+ * B*N < 2^31.
+ */
+int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int Hq, int Hk, int N, int d,
+                    long long q_stride_b, long long q_stride_h, long long q_stride_n, long long k_stride_b,
+                    long long k_stride_h, long long k_stride_n, int norm, const void* q_weight, const void* k_weight,
+                    int weights_f32, float eps, const float* rope, int rope_len, int rope_dim, int interleaved,
+                    const int* positions, cudaStream_t stream);
+
+/*
+ * Gradients of fa_qk_norm_rope: from dq_out, dk_out (fa_bwd's dq and dk) to
+ * those of q, k and the weights.  q, k and the arguments after them mean the
+ * same as in the forward; 1 / rms is formed again from q and k.
+ *
+ *   dq_out, dk_out  in  contiguous [B, Hq, N, d], [B, Hk, N, d] bf16
+ *   dq, dk     out  bf16, of strides of their own (as q and k; distinct
+ *                   elements must not overlap, so a stride is >= d wherever its
+ *                   size is above 1)
+ *   dq_weight, dk_weight  out  [d] fp32, summed over all rows in a fixed order
+ *                   (the same bits on every run); NULL where not wanted;
+ *                   both must be NULL with norm = 0
+ *   workspace  fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned;
+ *              may be NULL when no weight gradient is wanted
+ *
+ * One launch, or two with weight gradients.
+ */
+int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq, void* dk,
+                        float* dq_weight, float* dk_weight, int B, int Hq, int Hk, int N, int d,
+                        long long q_stride_b, long long q_stride_h, long long q_stride_n, long long k_stride_b,
+                        long long k_stride_h, long long k_stride_n, long long dq_stride_b, long long dq_stride_h,
+                        long long dq_stride_n, long long dk_stride_b, long long dk_stride_h, long long dk_stride_n,
+                        int norm, const void* q_weight, const void* k_weight, int weights_f32, float eps,
+                        const float* rope, int rope_len, int rope_dim, int interleaved, const int* positions,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of fa_qk_norm_rope_bwd with weight gradients; 0 for an invalid d. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * Paged key/value cache
+ * ---------------------
+ *  A cache is a pool of num_pages pages of page_size keys each, for all Hk key
+ *  heads: element (page, h, row, c) of k_pages at page*stride_p + h*stride_h +
+ *  row*stride_r + c (v_pages likewise, with strides of its own).  Strides are
+ *  in elements, multiples of 8, > 0; both head-major ([pages, Hk, page_size, d])
+ *  and token-major ([pages, page_size, Hk, d]) pools are covered.  page_size is
+ *  a power of two, 16 to 65536.
+ *  page_table [S, max_pages] int32 (contiguous): key j of sequence s is row
+ *  j mod page_size of page page_table[s][j / page_size].  Entries behind a
+ *  sequence's end are not read.  Sequences may share pages that they only read.
+ *  The T new tokens of a step lie one after the other in ragged rows: sequence
+ *  s has rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 (cu_seqlens [S+1] int32,
+ *  not decreasing; rows behind cu_seqlens[S] are left as they are).
+ *  kv_lens [S] int32: keys of each sequence, its new tokens included, so new
+ *  token i of sequence s has position kv_lens[s] - q_len[s] + i.  A sequence
+ *  may have no new token and a length of zero.
+ *  All of these live on the device, so one captured graph serves every step of
+ *  the same T and S.  T = 0 or S = 0 does nothing.
+ *
+ * fa_paged_append: the pass of fa_qk_norm_rope on the T new tokens at their
+ * positions, queries to q_out, keys and values (as they are) into the cache.
+ * One launch.
+ *
+ *   q, k, v   in   bf16 [T, Hq, d], [T, Hk, d], [T, Hk, d]: element (t, h, c) at
+ *                  t*stride_t + h*stride_h + c (multiples of 8, >= 0)
+ *   q_out     out  contiguous [T, Hq, d] bf16
+ *   others    as in fa_qk_norm_rope (norm = 0 and rope_dim = 0 make a plain copy)
+ *
+ * A token with no position in [0, min(rope_len, max_pages*page_size)) gets a
+ * zero q_out row and is not cached; one whose page lies outside the pool is
+ * not cached; each records FA_ERR_DEVICE_INDEX.  Two tokens of one call must
+ * not share a slot (then either may win).
+ */
+int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_pages, void* v_pages,
+                    const int* page_table, const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq, int Hk,
+                    int d, int num_pages, int page_size, int max_pages, long long q_stride_t, long long q_stride_h,
+                    long long k_stride_t, long long k_stride_h, long long v_stride_t, long long v_stride_h,
+                    long long kp_stride_p, long long kp_stride_h, long long kp_stride_r, long long vp_stride_p,
+                    long long vp_stride_h, long long vp_stride_r, int norm, const void* q_weight,
+                    const void* k_weight, int weights_f32, float eps, const float* rope, int rope_len, int rope_dim,
+                    int interleaved, cudaStream_t stream);
+
+/*
  * Size of the library-owned scratch fa_bwd_noalloc uses: 64 MiB, held on every
  * GPU that loads the library until the process exits.
  */
@@ -269,7 +381,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device: FA_OK, or FA_ERR_DEVICE_TIMEOUT if any kernel of this
  * library gave up on a bounded wait since the last call (FA_ERR_INTERNAL for
- * a violated layout assumption); FA_ERR_CUDA if the
+ * a violated layout assumption, FA_ERR_DEVICE_INDEX for a position, page or
+ * length outside its table); FA_ERR_CUDA if the
  * synchronisation itself failed.
  */
 int fa_get_device_status(cudaStream_t stream);

@@ -11,10 +11,11 @@ of ``fa_bwd`` (``fa_bwd_preprocess``, ``fa_bwd_dkdv``, ``fa_bwd_dq_convert``),
 the split-KV decode forward (``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_size``), the norm and rotation of queries and keys
 (``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
-``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``),
+``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``, ``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``),
 ``fa_get_device_status``, ``fa_status_string``.
 Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`,
-:func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`.
+:func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`,
+:func:`paged_forward`.
 """
 
 from __future__ import annotations
@@ -28,7 +29,8 @@ __all__ = [
     "fa_bwd_preprocess", "fa_bwd_dkdv", "fa_bwd_dq_convert", "fa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES",
     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "decode_forward",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
-    "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "paged_append",
+    "fa_fwd_paged", "fa_fwd_paged_workspace_size",
+    "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "paged_append", "paged_forward",
     "fa_get_device_status", "fa_status_string", "forward", "backward", "EXPORTED_SYMBOLS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_WORKSPACE", "FA_ERR_CUDA",
     "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INTERNAL", "FA_ERR_DEVICE_INDEX",
@@ -50,6 +52,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_fp8", "fa_bwd", "fa_bwd_workspace_size", "
                     "fa_bwd_dkdv",
                     "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size",
                     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
+                    "fa_fwd_paged", "fa_fwd_paged_workspace_size",
                     "fa_get_device_status", "fa_status_string")
 
 # Size of the library-owned scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES).
@@ -111,6 +114,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
     lib.fa_paged_append.restype = i
     lib.fa_paged_append.argtypes = [vp] * 9 + [i] * 8 + [ll] * 12 + [i, vp, vp, i, f, vp, i, i, i, vp]
+    lib.fa_fwd_paged.restype = i
+    lib.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [ll] * 8 + [f, i, i, vp, sz, vp]
+    lib.fa_fwd_paged_workspace_size.restype = sz
+    lib.fa_fwd_paged_workspace_size.argtypes = [i]
     lib.fa_get_device_status.restype = i
     lib.fa_get_device_status.argtypes = [vp]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -214,6 +221,19 @@ def fa_paged_append(q, k, v, q_out, k_pages, v_pages, page_table, cu_seqlens, kv
                                           k_stride_h, v_stride_t, v_stride_h, kp_stride_p, kp_stride_h, kp_stride_r,
                                           vp_stride_p, vp_stride_h, vp_stride_r, norm, q_weight, k_weight,
                                           weights_f32, eps, rope, rope_len, rope_dim, interleaved, stream)
+
+
+def fa_fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, T, S, Hq, Hk, d, num_pages, page_size,
+                 max_pages, q_stride_t, q_stride_h, kp_stride_p, kp_stride_h, kp_stride_r, vp_stride_p, vp_stride_h,
+                 vp_stride_r, scale, causal, max_q, workspace, workspace_bytes, stream) -> int:
+    return load_library().fa_fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, T, S, Hq, Hk, d,
+                                       num_pages, page_size, max_pages, q_stride_t, q_stride_h, kp_stride_p,
+                                       kp_stride_h, kp_stride_r, vp_stride_p, vp_stride_h, vp_stride_r, scale, causal,
+                                       max_q, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_workspace_size(d) -> int:
+    return load_library().fa_fwd_paged_workspace_size(d)
 
 
 def fa_get_device_status(stream) -> int:
@@ -528,3 +548,32 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
     if st != FA_OK:
         raise FaError(st, "fa_paged_append")
     return q_out
+
+
+def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,
+                  lse=None, workspace=None, stream=None):
+    """Attention of the new tokens ``q [T, Hq, d]`` (any strides) over the paged cache that :func:`paged_append` wrote;
+    returns ``(o [T, Hq, d], lse [T, Hq])``.  ``max_q`` is the longest chunk of the step (0: not known; a hint that
+    selects the kernel variant)."""
+    import torch
+    bf16 = torch.bfloat16
+    _strided(q, "q", (None, None, None), bf16)
+    T, Hq, d = q.shape
+    Hk = k_pages.shape[1] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4 else None
+    S, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d)
+    if scale is None:
+        scale = d ** -0.5
+    with _On(q.device, stream, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out, lse, workspace) as s:
+        o = torch.empty((T, Hq, d), dtype=bf16, device=q.device) if out is None else out
+        l = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+        _check(o, "out", (T, Hq, d), bf16)
+        _check(l, "lse", (T, Hq), torch.float32)
+        if workspace is None:
+            workspace = torch.empty(fa_fwd_paged_workspace_size(d), dtype=torch.uint8, device=q.device)
+        st = fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), l.data_ptr(),
+                          page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(), T, S, Hq, Hk, d, num_pages,
+                          page_size, max_pages, *_steps(q, (0, 1)), *steps, float(scale), int(bool(causal)),
+                          int(max_q), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_paged")
+    return o, l

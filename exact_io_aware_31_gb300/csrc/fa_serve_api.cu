@@ -11,6 +11,7 @@
 #include "../../include/fa.h"
 #include "fa_host.h"
 #include "fa_norm_rope.cuh"
+#include "fa_paged.cuh"
 
 namespace fa {
 namespace {
@@ -225,4 +226,126 @@ extern "C" int fa_paged_append(const void* q, const void* k, const void* v, void
   a.page_size = page_size;
   a.max_pages = max_pages;
   return cuda_status(launch_paged_append(a, stream));
+}
+
+namespace fa {
+namespace {
+
+struct PagedWorkspace {
+  size_t ml, o, total;
+};
+
+PagedWorkspace paged_workspace(int sms, int d) {
+  const size_t rows = (size_t)sms * 2 * kPagedRows;
+  PagedWorkspace w;
+  w.ml = round256((size_t)sms * kPagedHdr * sizeof(int));
+  w.o = w.ml + round256(rows * 2 * sizeof(float));
+  w.total = w.o + round256(rows * d * sizeof(float));
+  return w;
+}
+
+// A pool [pages, Hk, page_size, d] of any strides: boxes of 64 columns by the
+// rows of a page, at most a key tile's 128 (128-byte swizzle).
+int make_pool_map(CUtensorMap* m, const void* base, int pages, int Hk, int page_size, int d, long long sp,
+                  long long sh, long long sr) {
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)Hk, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)sr * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)(page_size < 128 ? page_size : 128), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// Queries [T, Hk, G, d]: boxes of 64 columns x one key head's G heads x `tokens`.
+int make_ragged_map(CUtensorMap* m, const void* base, int T, int Hk, int G, int d, int tokens, long long st,
+                    long long sh) {
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)Hk, (cuuint64_t)T};
+  cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)sh * G * 2, (cuuint64_t)st * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)tokens};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" size_t fa_fwd_paged_workspace_size(int d) {
+  if (d != 64 && d != 128) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev) != FA_OK) return 0;
+  return paged_workspace(dev.sms, d).total;
+}
+
+extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                            const int* page_table, const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq,
+                            int Hk, int d, int num_pages, int page_size, int max_pages, long long q_stride_t,
+                            long long q_stride_h, long long kp_stride_p, long long kp_stride_h, long long kp_stride_r,
+                            long long vp_stride_p, long long vp_stride_h, long long vp_stride_r, float scale,
+                            int causal, int max_q, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (T < 0 || S < 0 || T >= (1 << 30) || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_q < 0 || !flag(causal) ||
+      !std::isfinite(scale))
+    return FA_ERR_INVALID_ARG;
+  if (Hq >= (1 << 15)) return FA_ERR_INVALID_ARG;
+  const int G = Hq / Hk;
+  if ((d != 64 && d != 128) || G > 128) return FA_ERR_UNSUPPORTED;
+  if (T == 0 || S == 0) return FA_OK;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
+  for (long long st : {q_stride_t, q_stride_h})  // written into a tensor map: positive
+    if (st < d || st % 8 != 0 || st >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  const long long sp[2] = {kp_stride_p, vp_stride_p}, sh[2] = {kp_stride_h, vp_stride_h},
+                  sr[2] = {kp_stride_r, vp_stride_r};
+  int st = check_cache(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d, num_pages, page_size, max_pages, sp,
+                       sh, sr);
+  if (st != FA_OK) return st;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != FA_OK) return st;
+  const PagedWorkspace w = paged_workspace(dev.sms, d);
+  if (workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+  PagedLaunch a = {};
+  a.d = d;
+  a.grid = dev.sms;
+  // Rows a sequence brings to one key head: over a tile of 128, the two-tile
+  // kernel.  Where they fit 64, the tiles hold no more than 64 rows and two of
+  // them fit the one-tile kernel's query buffer (the next unit's is loaded
+  // while this one runs).
+  const long long rows = (long long)(max_q > 0 ? max_q : T) * G;
+  const int tokens = 128 / G;
+  a.wide = rows > tokens * G;
+  const bool two = !a.wide && G <= 64 && rows <= 64 / G * G;
+  PagedParams& p = a.p;
+  p.tile_tokens = two ? 64 / G : tokens;
+  p.q_bufs = two ? 2 : 1;
+  p.o = o;
+  p.lse = lse;
+  p.page_table = page_table;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.T = T;
+  p.S = S;
+  p.Hk = Hk;
+  p.G = G;
+  p.num_pages = num_pages;
+  p.page_log2 = 0;
+  while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  p.max_pages = max_pages;
+  p.causal = causal;
+  p.c2 = log2_scale(scale);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.hdr = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  p.status = dev.status;
+  if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||
+      make_pool_map(&a.tm_k, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0]) ||
+      make_pool_map(&a.tm_v, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1]))
+    return FA_ERR_CUDA;
+  return cuda_status(launch_paged(a, stream));
 }

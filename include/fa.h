@@ -340,6 +340,48 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
                     int interleaved, cudaStream_t stream);
 
 /*
+ * Attention of the T new tokens of a step over the paged cache (their keys and
+ * values appended before): a single token a sequence, a few, or chunks of a
+ * prompt, in any mix; grouped key heads (query head h reads key head
+ * h / (Hq / Hk)).
+ *
+ *   q         in   bf16 [T, Hq, d]: element (t, h, c) at t*stride_t + h*stride_h
+ *                  + c (multiples of 8, >= d)
+ *   o         out  contiguous [T, Hq, d] bf16
+ *   lse       out  contiguous [T, Hq] fp32, natural-log logsumexp of each row;
+ *                  may be NULL
+ *   causal    key j is visible to new token i of sequence s iff j < kv_lens[s]
+ *             and, with causal = 1, j <= kv_lens[s] - q_len[s] + i
+ *   max_q     the longest q_len, or 0 if it is not known: it selects the kernel
+ *             variant; any value gives the same results up to rounding
+ *   workspace fa_fwd_paged_workspace_size(d) bytes, 256-byte aligned; its
+ *             contents on entry do not matter.  Calls that may overlap (other
+ *             streams, two captured graphs) need one each, and a captured
+ *             graph's must live as long as the graph.
+ *
+ * A row that sees no key is zero with lse = -infinity.  What a page holds
+ * behind its sequence's end does not matter (NaN included).  Keys of a page
+ * outside the pool count as zeros with zero values, lengths outside their
+ * range are cut to it; both record FA_ERR_DEVICE_INDEX.  Two launches.  Results
+ * are the same bits on every run.
+ * Hq must be a multiple of Hk with Hq / Hk <= 128 (FA_ERR_UNSUPPORTED above);
+ * T < 2^30.
+ */
+int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse, const int* page_table,
+                 const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq, int Hk, int d, int num_pages,
+                 int page_size, int max_pages, long long q_stride_t, long long q_stride_h, long long kp_stride_p,
+                 long long kp_stride_h, long long kp_stride_r, long long vp_stride_p, long long vp_stride_h,
+                 long long vp_stride_r, float scale, int causal, int max_q, void* workspace, size_t workspace_bytes,
+                 cudaStream_t stream);
+
+/*
+ * Workspace bytes of fa_fwd_paged on the current device: the partial outputs of
+ * the units of work that its CTAs share.  0 for an invalid d or without an
+ * sm_103 device.
+ */
+size_t fa_fwd_paged_workspace_size(int d);
+
+/*
  * Size of the library-owned scratch fa_bwd_noalloc uses: 64 MiB, held on every
  * GPU that loads the library until the process exits.
  */

@@ -101,3 +101,20 @@ def test_rope_table_layout():
     for bad in ((0, 4), (5, 3), (5, 0)):
         with pytest.raises(ValueError):
             fa.rope_table(*bad, device="cpu")
+
+
+FWD_PAGED = dict(q=A, k_pages=A, v_pages=A, o=A, lse=A, **CACHE, T=5, S=2, Hq=4, Hk=2, d=64, num_pages=8, page_size=16,
+                 max_pages=4, q_stride_t=256, q_stride_h=64, **{n: v for n, v in APPEND.items() if n[1:9] == "p_stride"},
+                 scale=0.1, causal=1, max_q=0, workspace=A, workspace_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", POOL + [
+    (dict(d=96), UNSUPPORTED), (dict(Hq=0), INVALID), (dict(Hk=0), INVALID), (dict(Hq=5), INVALID),
+    (dict(Hq=258), UNSUPPORTED), (dict(Hq=1 << 15, Hk=1 << 14), INVALID), (dict(T=1 << 30), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(causal=2), INVALID), (dict(max_q=-1), INVALID), (dict(q=A + 8), INVALID),
+    (dict(o=None), INVALID), (dict(lse=A + 2), INVALID), (dict(q_stride_t=0), INVALID), (dict(q_stride_h=68), INVALID),
+    (dict(q_stride_t=1 << 31), INVALID), (dict(workspace=None), WORKSPACE), (dict(workspace=A + 64), WORKSPACE),
+    (dict(T=0), fa.FA_OK), (dict(S=0, q=None, o=None, workspace=None), fa.FA_OK),
+])
+def test_paged_forward_refusals(kw, code):
+    assert fa.fa_fwd_paged(**(FWD_PAGED | kw)) == code

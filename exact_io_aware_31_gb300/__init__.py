@@ -360,73 +360,82 @@ def decode_forward(q, k, v, scale=None, causal=True, num_splits=0, out=None, lse
 
 
 # ------------------------------------------------ norm, rotation and paged cache ----
-def _strided(t, name, shape, dtype):
-    """A CUDA tensor of this type and shape (None: any size) whose last dimension is contiguous."""
+# A decode step makes several of these calls a layer, each of a few microseconds
+# on the GPU: the helpers below look at each tensor once and call the library
+# directly.
+def _refuse(t, name, shape, dtype, device):
+    """The error of a tensor that is not a CUDA tensor of this type and shape on device ``device``."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
+    raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} with a contiguous last dimension, got {t.dtype} "
+                     f"{tuple(t.shape)}, strides {t.stride()}")
 
 
-def _steps(t, dims):
-    """Strides of ``dims``; where a size is below 2 the stride means nothing and any valid one will do."""
-    return tuple(t.stride(i) if t.shape[i] > 1 else t.shape[-1] for i in dims)
+def _dims(t, name, n):
+    """Shape of a tensor of n dimensions on a CUDA device, and the device's index."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != n:
+        raise ValueError(f"{name} must be a CUDA tensor of {n} dimensions")
+    return t.shape, t.get_device()
 
 
-class _On:
-    """Run on the tensors' device and on ``stream`` (None: that device's current one): what a helper allocates inside
-    belongs to that stream."""
+def _rows(t, name, shape, dtype, device):
+    """Check rows of any layout; their strides without the last.  Where a size is 1 a stride means nothing, and any
+    valid one will do."""
+    st = t.stride()
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or st[-1] != 1:
+        _refuse(t, name, shape, dtype, device)
+    if 1 in shape:
+        return [s if n > 1 else shape[-1] for s, n in zip(st[:-1], shape[:-1])]
+    return st[:-1]
 
-    def __init__(self, device, stream, *tensors):
+
+def _flat(t, name, shape, dtype, device):
+    """Check a contiguous tensor (None passes); its address."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _on_stream(fn):
+    """The helper run on its tensors' device and, where ``stream`` is given, on that stream: what it allocates belongs
+    to the stream that uses it."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if stream is None:
+            import torch
+            if not isinstance(first, torch.Tensor) or not first.is_cuda:
+                raise ValueError(f"{fn.__name__} takes CUDA tensors")
+            if first.get_device() == torch.cuda.current_device():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(first.get_device()):
+                return fn(first, *args, **kw)
         import torch
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"every tensor must be on {device}, got one on {t.device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        self.guards = []
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
-        elif device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
+        if not isinstance(first, torch.Tensor) or first.device != stream.device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the first tensor is not")
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
 
-    def __enter__(self):
-        import torch
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+    return call
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved):
+def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, device):
     """The shared trailing arguments of the norm-and-rotation calls, checked."""
     import torch
-    wt = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if wt is not None and w.dtype != wt:
-            raise ValueError("q_weight and k_weight must have one type")
-        wt = w.dtype if w.dtype in (torch.float32, torch.bfloat16) else torch.bfloat16
-        _check(w, name, (d,), wt)
-    rope_len = rope_dim = 0
-    if rope is not None:
-        _strided(rope, "rope", (None, None), torch.float32)
-        _check(rope, "rope", rope.shape, torch.float32)
-        rope_len, rope_dim = rope.shape
-    return (int(bool(norm)), _ptr(q_weight), _ptr(k_weight), int(wt == torch.float32), float(eps), _ptr(rope),
-            rope_len, rope_dim, int(bool(interleaved)))
+    first = q_weight if q_weight is not None else k_weight
+    wt = torch.float32 if first is not None and first.dtype == torch.float32 else torch.bfloat16
+    qw, kw = _flat(q_weight, "q_weight", (d,), wt, device), _flat(k_weight, "k_weight", (d,), wt, device)
+    rope_len, rope_dim = (0, 0) if rope is None else _dims(rope, "rope", 2)[0]
+    return (1 if norm else 0, qw, kw, 1 if wt == torch.float32 else 0, eps,
+            _flat(rope, "rope", (rope_len, rope_dim), torch.float32, device), rope_len, rope_dim,
+            1 if interleaved else 0)
 
 
 def rope_table(length, rope_dim, base=10000.0, device="cuda"):
@@ -441,139 +450,146 @@ def rope_table(length, rope_dim, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+@_on_stream
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6, interleaved=False,
-                 norm=True, out=None, stream=None):
+                 norm=True, out=None):
     """Norm of queries and keys for each head, then rotation: ``q [B, Hq, N, d]``, ``k [B, Hk, N, d]`` bf16 of any
     strides (``x.transpose(1, 2)`` of a token-major projection, a slice of a wider row) -> contiguous
     ``(q_out, k_out)``, what :func:`forward` takes.  ``rope`` is a :func:`rope_table` (None: no rotation),
-    ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only."""
+    ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only.  ``stream`` (keyword): a stream
+    to run on instead of the current one."""
     import torch
     bf16 = torch.bfloat16
-    _strided(q, "q", (None, None, None, None), bf16)
-    B, Hq, N, d = q.shape
-    _strided(k, "k", (B, None, N, d), bf16)
-    Hk = k.shape[1]
-    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
-    if positions is not None:
-        _check(positions, "positions", (B, N), torch.int32)
-    with _On(q.device, stream, k, q_weight, k_weight, rope, positions, *(out or ())) as s:
-        q_out, k_out = out if out is not None else (torch.empty((B, h, N, d), dtype=bf16, device=q.device)
-                                                    for h in (Hq, Hk))
-        _check(q_out, "q_out", (B, Hq, N, d), bf16)
-        _check(k_out, "k_out", (B, Hk, N, d), bf16)
-        st = fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d,
-                             *_steps(q, (0, 1, 2)), *_steps(k, (0, 1, 2)), *args, _ptr(positions), s)
+    (B, Hq, N, d), dev = _dims(q, "q", 4)
+    Hk = _dims(k, "k", 4)[0][1]
+    sq, sk = _rows(q, "q", (B, Hq, N, d), bf16, dev), _rows(k, "k", (B, Hk, N, d), bf16, dev)
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
+    pos = _flat(positions, "positions", (B, N), torch.int32, dev)
+    if out is None:
+        q_out, k_out = (torch.empty((B, h, N, d), dtype=bf16, device=q.device) for h in (Hq, Hk))
+    else:
+        q_out, k_out = out
+        _flat(q_out, "q_out", (B, Hq, N, d), bf16, dev)
+        _flat(k_out, "k_out", (B, Hk, N, d), bf16, dev)
+    st = load_library().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N,
+                                        d, *sq, *sk, *args, pos, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_qk_norm_rope")
     return q_out, k_out
 
 
+@_on_stream
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
-                          interleaved=False, norm=True, grads=None, weight_grads=True, workspace=None, stream=None):
+                          interleaved=False, norm=True, grads=None, weight_grads=True, workspace=None):
     """Gradients ``(dq, dk, dq_weight, dk_weight)`` of :func:`qk_norm_rope` from those of its outputs
     (:func:`backward`'s ``dq, dk``).  ``dq, dk`` have q's and k's shapes, token-major in memory
     (``[B, N, H, d]``) unless ``grads=(dq, dk)`` gives tensors of any strides.  The weights' gradients are
     fp32 ``[d]`` (None with ``norm=False`` or ``weight_grads=False``)."""
     import torch
+    (B, Hq, N, d), dev = _dims(q, "q", 4)
+    Hk = _dims(k, "k", 4)[0][1]
     bf16 = torch.bfloat16
-    _strided(q, "q", (None, None, None, None), bf16)
-    B, Hq, N, d = q.shape
-    _strided(k, "k", (B, None, N, d), bf16)
-    Hk = k.shape[1]
-    _check(dq_out, "dq_out", (B, Hq, N, d), bf16)
-    _check(dk_out, "dk_out", (B, Hk, N, d), bf16)
-    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
-    if positions is not None:
-        _check(positions, "positions", (B, N), torch.int32)
-    with _On(q.device, stream, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace,
-             *(grads or ())) as s:
-        if grads is None:
-            grads = tuple(torch.empty((B, N, h, d), dtype=bf16, device=q.device).transpose(1, 2) for h in (Hq, Hk))
+    sq, sk = _rows(q, "q", (B, Hq, N, d), bf16, dev), _rows(k, "k", (B, Hk, N, d), bf16, dev)
+    dqo = _flat(dq_out, "dq_out", (B, Hq, N, d), bf16, dev)
+    dko = _flat(dk_out, "dk_out", (B, Hk, N, d), bf16, dev)
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
+    pos = _flat(positions, "positions", (B, N), torch.int32, dev)
+    if grads is None:
+        dq, dk = (torch.empty_strided((B, h, N, d), (N * h * d, d, h * d, 1), dtype=bf16, device=q.device)
+                  for h in (Hq, Hk))
+        sdq, sdk = (N * Hq * d, d, Hq * d), (N * Hk * d, d, Hk * d)
+    else:
         dq, dk = grads
-        _strided(dq, "dq", (B, Hq, N, d), bf16)
-        _strided(dk, "dk", (B, Hk, N, d), bf16)
-        dqw = dkw = None
-        if norm and weight_grads:
-            dqw, dkw = torch.empty((2, d), dtype=torch.float32, device=q.device)
-            if workspace is None:
-                workspace = torch.empty(fa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
-        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        st = fa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), dq.data_ptr(),
-                                 dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, Hq, Hk, N, d, *_steps(q, (0, 1, 2)),
-                                 *_steps(k, (0, 1, 2)), *_steps(dq, (0, 1, 2)), *_steps(dk, (0, 1, 2)), *args,
-                                 _ptr(positions), _ptr(workspace), wbytes, s)
+        sdq, sdk = _rows(dq, "dq", (B, Hq, N, d), bf16, dev), _rows(dk, "dk", (B, Hk, N, d), bf16, dev)
+    dqw = dkw = None
+    if norm and weight_grads:
+        dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in "qk")
+        if workspace is None:
+            workspace = torch.empty(fa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+    ws, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    st = load_library().fa_qk_norm_rope_bwd(dqo, dko, q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                            None if dqw is None else dqw.data_ptr(),
+                                            None if dkw is None else dkw.data_ptr(), B, Hq, Hk, N, d, *sq, *sk, *sdq,
+                                            *sdk, *args, pos, ws, wbytes, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
 
 
-def _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d):
-    """Checks of the paged cache's tensors: ``(S, num_pages, page_size, max_pages, strides)``."""
+def _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, d, device):
+    """Checks of the paged cache's tensors: their addresses, ``(S, Hk, num_pages, page_size, max_pages)``, strides."""
     import torch
-    _strided(k_pages, "k_pages", (None, Hk, None, d), torch.bfloat16)
-    _strided(v_pages, "v_pages", k_pages.shape, torch.bfloat16)
-    _strided(page_table, "page_table", (None, None), torch.int32)
-    S = page_table.shape[0]
-    _check(page_table, "page_table", page_table.shape, torch.int32)
-    _check(cu_seqlens, "cu_seqlens", (S + 1,), torch.int32)
-    _check(kv_lens, "kv_lens", (S,), torch.int32)
-    steps = _steps(k_pages, (0, 1, 2)) + _steps(v_pages, (0, 1, 2))
-    return S, k_pages.shape[0], k_pages.shape[2], page_table.shape[1], steps
+    bf16, i32 = torch.bfloat16, torch.int32
+    (num_pages, Hk, page_size, _), _ = _dims(k_pages, "k_pages", 4)
+    shape = (num_pages, Hk, page_size, d)
+    steps = (*_rows(k_pages, "k_pages", shape, bf16, device), *_rows(v_pages, "v_pages", shape, bf16, device))
+    (S, max_pages), _ = _dims(page_table, "page_table", 2)
+    addresses = (_flat(page_table, "page_table", (S, max_pages), i32, device),
+                 _flat(cu_seqlens, "cu_seqlens", (S + 1,), i32, device), _flat(kv_lens, "kv_lens", (S,), i32, device))
+    return addresses, S, Hk, num_pages, page_size, max_pages, steps
 
 
+@_on_stream
 def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight=None, k_weight=None, rope=None,
-                 eps=1e-6, interleaved=False, norm=True, out=None, stream=None):
+                 eps=1e-6, interleaved=False, norm=True, out=None):
     """Norm and rotate the new tokens' ``q [T, Hq, d]`` and ``k [T, Hk, d]`` at their positions, write keys and values
     into the cache ``k_pages, v_pages [num_pages, Hk, page_size, d]`` (any strides: a token-major pool is a
     ``transpose(1, 2)`` view), and return the queries ``[T, Hq, d]`` for :func:`paged_forward`.
     ``page_table [S, max_pages]``, ``cu_seqlens [S + 1]`` and ``kv_lens [S]`` (new tokens included) are int32 on
-    the device.  ``rope=None, norm=False`` caches k and v as they are."""
+    the device.  ``rope=None, norm=False`` caches k and v as they are.  ``stream`` (keyword): a stream to run on
+    instead of the current one."""
     import torch
     bf16 = torch.bfloat16
-    _strided(q, "q", (None, None, None), bf16)
-    T, Hq, d = q.shape
-    _strided(k, "k", (T, None, d), bf16)
-    Hk = k.shape[1]
-    _strided(v, "v", (T, Hk, d), bf16)
-    S, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d)
-    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved)
-    with _On(q.device, stream, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight, k_weight, rope,
-             out) as s:
-        q_out = torch.empty((T, Hq, d), dtype=bf16, device=q.device) if out is None else out
-        _check(q_out, "out", (T, Hq, d), bf16)
-        st = fa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
-                             v_pages.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(), T,
-                             S, Hq, Hk, d, num_pages, page_size, max_pages, *_steps(q, (0, 1)), *_steps(k, (0, 1)),
-                             *_steps(v, (0, 1)), *steps, *args, s)
+    (T, Hq, d), dev = _dims(q, "q", 3)
+    meta, S, Hk, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+                                                                      d, dev)
+    sq, sk, sv = (_rows(q, "q", (T, Hq, d), bf16, dev), _rows(k, "k", (T, Hk, d), bf16, dev),
+                  _rows(v, "v", (T, Hk, d), bf16, dev))
+    args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
+    else:
+        _flat(out, "out", (T, Hq, d), bf16, dev)
+    st = load_library().fa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), k_pages.data_ptr(),
+                                        v_pages.data_ptr(), *meta, T, S, Hq, Hk, d, num_pages, page_size, max_pages,
+                                        *sq, *sk, *sv, *steps, *args, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_paged_append")
-    return q_out
+    return out
 
 
+_paged_workspace = {}  # (device, d) -> bytes
+
+
+@_on_stream
 def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,
-                  lse=None, workspace=None, stream=None):
+                  lse=None, workspace=None):
     """Attention of the new tokens ``q [T, Hq, d]`` (any strides) over the paged cache that :func:`paged_append` wrote;
     returns ``(o [T, Hq, d], lse [T, Hq])``.  ``max_q`` is the longest chunk of the step (0: not known; a hint that
-    selects the kernel variant)."""
+    selects the kernel variant).  ``stream`` (keyword): a stream to run on instead of the current one."""
     import torch
     bf16 = torch.bfloat16
-    _strided(q, "q", (None, None, None), bf16)
-    T, Hq, d = q.shape
-    Hk = k_pages.shape[1] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4 else None
-    S, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d)
-    if scale is None:
-        scale = d ** -0.5
-    with _On(q.device, stream, k_pages, v_pages, page_table, cu_seqlens, kv_lens, out, lse, workspace) as s:
-        o = torch.empty((T, Hq, d), dtype=bf16, device=q.device) if out is None else out
-        l = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        _check(o, "out", (T, Hq, d), bf16)
-        _check(l, "lse", (T, Hq), torch.float32)
-        if workspace is None:
-            workspace = torch.empty(fa_fwd_paged_workspace_size(d), dtype=torch.uint8, device=q.device)
-        st = fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), l.data_ptr(),
-                          page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(), T, S, Hq, Hk, d, num_pages,
-                          page_size, max_pages, *_steps(q, (0, 1)), *steps, float(scale), int(bool(causal)),
-                          int(max_q), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    (T, Hq, d), dev = _dims(q, "q", 3)
+    meta, S, Hk, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+                                                                      d, dev)
+    sq = _rows(q, "q", (T, Hq, d), bf16, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
+    else:
+        _flat(out, "out", (T, Hq, d), bf16, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _flat(lse, "lse", (T, Hq), torch.float32, dev)
+    if workspace is None:
+        need = _paged_workspace.get((dev, d))
+        if need is None:
+            need = _paged_workspace[dev, d] = fa_fwd_paged_workspace_size(d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = load_library().fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                     lse.data_ptr(), *meta, T, S, Hq, Hk, d, num_pages, page_size, max_pages, *sq,
+                                     *steps, d ** -0.5 if scale is None else scale, 1 if causal else 0, max_q,
+                                     workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged")
-    return o, l
+    return out, lse

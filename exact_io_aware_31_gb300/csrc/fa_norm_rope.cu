@@ -14,14 +14,17 @@
 // bound by device memory, so each element is read once and written once, 16
 // bytes a thread.  d / 8 lanes share a row (a thread holds 8 neighbouring
 // columns; the sum of squares and a split rotation's partner columns come by
-// shuffle), a warp takes 32 / (d / 8) rows at once and kSteps such steps per
-// item: an item is one token's run of up to kSteps * rows heads, so that the
-// token's cosines and sines are loaded once for all of them and four 16-byte
-// loads a thread are in flight.  The input may be any strided view (a slice
-// of the projection's output); the output is the contiguous [B, H, N, d] that
-// the attention kernels read, so the transposition costs no pass of its own.
-// Everything between load and store is fp32; the one rounding is the stored
-// bf16 (the weights' gradient stays fp32).
+// shuffle), a warp takes 32 / (d / 8) rows at once and STEPS such steps: a
+// chunk of one token's heads, so that the token's cosines and sines are loaded
+// once for all of them.  A CTA keeps one chunk and walks the tokens, its warps
+// on neighbouring ones: weights, pointers and the kind of rotation cost nothing
+// a token, and a token's rows are loaded before the last one's are computed.
+// (One token a warp spent 160 instructions on 512 bytes of input and was bound
+// by their issue, 93 us for the case below; so paired fp32 arithmetic as well.)
+// The input may be any strided view (a slice of the projection's output); the
+// output is the contiguous [B, H, N, d] that the attention kernels read, so the
+// transposition costs no pass of its own.  Everything between load and store is
+// fp32; the one rounding is the stored bf16 (the weights' gradient stays fp32).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,42 +32,73 @@
 #include "fa_norm_rope.cuh"
 #include "sm103_ptx.cuh"
 
+#ifndef NRF
+#define NRF 4
+#endif
+#ifndef NRT
+#define NRT 8
+#endif
+#ifndef NRB
+#define NRB 2
+#endif
+#ifndef NRS
+#define NRS 4
+#endif
+#ifndef NRW
+#define NRW 8
+#endif
+#ifndef NRV
+#define NRV 2048
+#endif
 namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSteps = 4;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(v[i] << 16);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-  }
+// A thread's 8 columns of a row as four pairs (one instruction for two elements).
+using Row = uint64_t[4];
+
+__device__ __forceinline__ uint64_t unpack2(uint32_t v) {
+  return f2_pack(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void unpack8(const uint4& u, Row& x) {
+  x[0] = unpack2(u.x), x[1] = unpack2(u.y), x[2] = unpack2(u.z), x[3] = unpack2(u.w);
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ uint4 pack8(const Row& x) {
+  return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+}
+
+__device__ __forceinline__ void load8(const float* p, Row& x) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  x[0] = f2_pack(a.x, a.y), x[1] = f2_pack(a.z, a.w), x[2] = f2_pack(b.x, b.y), x[3] = f2_pack(b.z, b.w);
 }
 
-__device__ __forceinline__ void load_weights(const NormRopeParams& p, int which, int l, float (&w)[8]) {
+// Weights of the 8 columns of lane l of a row.
+__device__ __forceinline__ void load_weights(const NormRopeParams& p, int which, int l, Row& w) {
   const void* src = p.w[which];
   if (src == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    for (int i = 0; i < 4; ++i) w[i] = f2_pack(1.f, 1.f);
   } else if (p.weights_f32) {
     load8(static_cast<const float*>(src) + 8 * l, w);
   } else {
     unpack8(__ldg(static_cast<const uint4*>(src) + l), w);
   }
+}
+
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
 }
 
 template <int LPR>
@@ -74,238 +108,327 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// The cosines and sines of this lane's 8 columns (lane l of a row), and how
-// the row turns.  Split pairs (i, i + dr / 2): lanes l and l + dr / 16 hold
-// partner columns and the same angles.  Neighbouring pairs: four angles a lane.
-struct Turn {
-  float c[8], s[8];  // interleaved: the first four
-  int mode;          // 0: columns pass, 1: split pairs, first half, 2: second half, 3: neighbouring pairs
-  int hl;            // lanes between split partners
+// Where a lane stands in its row.  The rotation is z = y * c + other * s:
+// `other` is the partner column's element (dr / 16 lanes away for split pairs
+// (i, i + dr / 2), the neighbour within the pair for (2i, 2i + 1): INTER), and
+// s carries a sign.  Columns that pass have c = 1, s = 0 and an `other` of zero.
+template <int D, bool INTER>
+struct Lane {
+  int l;         // of the row's D / 8
+  int partner;   // the lane that holds the partner columns
+  int angle;     // its first angle
+  bool turned, first;
+  __device__ __forceinline__ Lane(const NormRopeParams& p, int lane) {
+    const int hl = p.dr / 16;
+    l = lane % (D / 8);
+    turned = 8 * l < p.dr;
+    first = l < hl;
+    partner = INTER || !turned ? l : first ? l + hl : l - hl;
+    angle = INTER ? 4 * l : 8 * (first ? l : l - hl);
+  }
 };
 
-__device__ __forceinline__ void load_turn(const NormRopeParams& p, int pos, int l, Turn& t) {
-  const int half = p.dr / 2;
-  t.hl = p.dr / 16;
-  t.mode = 0;
-  if (8 * l >= p.dr) return;
-  const float* row = p.rope + (size_t)pos * p.dr;
-  if (p.interleaved) {
-    t.mode = 3;
-    const float4 a = __ldg(reinterpret_cast<const float4*>(row) + l);
-    const float4 b = __ldg(reinterpret_cast<const float4*>(row + half) + l);
-    t.c[0] = a.x, t.c[1] = a.y, t.c[2] = a.z, t.c[3] = a.w;
-    t.s[0] = b.x, t.s[1] = b.y, t.s[2] = b.z, t.s[3] = b.w;
-  } else {
-    t.mode = l < t.hl ? 1 : 2;
-    const int at = 8 * (l < t.hl ? l : l - t.hl);
-    load8(row + at, t.c);
-    load8(row + half + at, t.s);
-  }
-}
+constexpr uint64_t kSign2 = 0x8000000080000000ull;
 
-// Rotate the row's 8 columns of this lane by the angle (BACK: by minus the
-// angle).  Every lane of the warp calls it.
-template <bool BACK>
-__device__ __forceinline__ void turn_row(const NormRopeParams& p, const Turn& t, float (&y)[8]) {
-  if (p.dr == 0) return;
-  if (p.interleaved) {
-    if (t.mode == 3) {
+// Cosines and sines of the 8 columns at a table row, without sign.
+template <int D, bool INTER>
+__device__ __forceinline__ void load_angles(const NormRopeParams& p, const Lane<D, INTER>& ln, int pos, Row& c,
+                                            Row& s) {
+  if (!ln.turned) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = BACK ? -t.s[i] : t.s[i];
-        const float a = y[2 * i], b = y[2 * i + 1];
-        y[2 * i] = a * t.c[i] - b * s;
-        y[2 * i + 1] = b * t.c[i] + a * s;
-      }
-    }
+    for (int i = 0; i < 4; ++i) c[i] = f2_pack(1.f, 1.f), s[i] = 0;
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int src = t.mode == 1 ? lane + t.hl : t.mode == 2 ? lane - t.hl : lane;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float other = __shfl_sync(0xffffffffu, y[i], src);
-    if (t.mode != 0) {
-      const float s = (t.mode == 1) != BACK ? -t.s[i] : t.s[i];
-      y[i] = y[i] * t.c[i] + other * s;
-    }
+  const float* row = p.rope + (size_t)pos * p.dr + ln.angle;
+  const float* sines = row + p.dr / 2;
+  if constexpr (INTER) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(row)), b = __ldg(reinterpret_cast<const float4*>(sines));
+    c[0] = f2_pack(a.x, a.x), c[1] = f2_pack(a.y, a.y), c[2] = f2_pack(a.z, a.z), c[3] = f2_pack(a.w, a.w);
+    s[0] = f2_pack(b.x, b.x), s[1] = f2_pack(b.y, b.y), s[2] = f2_pack(b.z, b.z), s[3] = f2_pack(b.w, b.w);
+  } else {
+    load8(row, c);
+    load8(sines, s);
   }
 }
 
-// One item: a token's heads [h0, h0 + kSteps * 32 / LPR) of one tensor.
-template <int D>
-struct Item {
-  static constexpr int LPR = D / 8;          // lanes a row
-  static constexpr int RPW = 32 / LPR;       // rows a warp and step
-  static constexpr int kRows = RPW * kSteps; // heads an item
+// What the sines are multiplied with: the sign of z_a = y_a c - y_b s, z_b = y_b c + y_a s
+// (BACK: the other one) times `w`, the partner columns' weights.
+template <int D, bool INTER, bool BACK>
+__device__ __forceinline__ void signed_row(const Lane<D, INTER>& ln, Row& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] ^= INTER ? (BACK ? 0x8000000000000000ull : 0x80000000ull) : ln.first != BACK ? kSign2 : 0;
+}
+
+// The partner columns of 8 bf16 columns (every lane of the warp calls it).
+template <int D, bool INTER>
+__device__ __forceinline__ uint4 partner_of(const NormRopeParams& p, const Lane<D, INTER>& ln, const uint4& v) {
+  uint4 o;
+  if constexpr (INTER) {
+    o = make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032), __byte_perm(v.z, 0, 0x1032),
+                   __byte_perm(v.w, 0, 0x1032));
+  } else {
+    o.x = __shfl_sync(0xffffffffu, v.x, ln.partner, D / 8);
+    o.y = __shfl_sync(0xffffffffu, v.y, ln.partner, D / 8);
+    o.z = __shfl_sync(0xffffffffu, v.z, ln.partner, D / 8);
+    o.w = __shfl_sync(0xffffffffu, v.w, ln.partner, D / 8);
+  }
+  if (p.dr < D && !ln.turned) o = make_uint4(0, 0, 0, 0);
+  return o;
+}
+
+// The norm's weights folded into the rotation, z = r (x c + other s): c is
+// multiplied with the columns' weights, s with its sign and the partner columns'.
+template <int D, bool INTER>
+struct Factors {
+  Row w, o;
+  __device__ __forceinline__ void load(const NormRopeParams& p, const Lane<D, INTER>& ln, int which) {
+    if (p.norm) {
+      load_weights(p, which, ln.l, w);
+      load_weights(p, which, ln.partner, o);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = (o[i] << 32) | (o[i] >> 32);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = o[i] = f2_pack(1.f, 1.f);
+    }
+    signed_row<D, INTER, false>(ln, o);
+  }
+  __device__ __forceinline__ void fold(Row& c, Row& s) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f2_mul(c[i], w[i]), s[i] = f2_mul(s[i], o[i]);
+  }
 };
 
-// ----------------------------------------------------------------- forward ---
-template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeLaunch a) {
-  using I = Item<D>;
-  const int lane = threadIdx.x & 31, l = lane % I::LPR, sub = lane / I::LPR;
-  const int cq = (a.H[0] + I::kRows - 1) / I::kRows, ck = (a.H[1] + I::kRows - 1) / I::kRows;
-  const long long item = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
-  const long long token = item / (cq + ck);
-  if (token >= (long long)a.B * a.N) return;
-  const int chunk = (int)(item - token * (cq + ck));
-  const int which = chunk >= cq;
-  const int h0 = (which ? chunk - cq : chunk) * I::kRows, H = a.H[which];
-  const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-  const HeadRows in = a.in[which];
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + b * in.sb + n * in.sn + 8 * l;
-  uint4 raw[kSteps];
+// 1 / rms of STEPS = 4 rows at once.  The lanes of a row exchange halves of the
+// four sums instead of all of them: after two rounds each lane goes on with one
+// row's, so the reduction and the root are done once, not four times.
+template <int D, int STEPS>
+__device__ __forceinline__ void inverse_rms(const uint4 (&raw)[STEPS], int l, float eps, float (&r)[STEPS]) {
+  static_assert(STEPS == 4, "four rows");
+  float v[4];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * I::RPW + sub;
-    raw[i] = h < H ? __ldg(reinterpret_cast<const uint4*>(src + h * in.sh)) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) {
+    Row x;
+    unpack8(raw[i], x);
+    uint64_t ss = f2_mul(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) ss = f2_fma(x[e], x[e], ss);
+    v[i] = pair_sum(ss);
   }
-  const int pos = a.positions ? __ldg(a.positions + token) : n;
-  const bool bad = a.p.dr > 0 && (pos < 0 || pos >= a.p.rope_len);
-  Turn t;
-  load_turn(a.p, bad ? 0 : pos, l, t);
-  float w[8];
-  load_weights(a.p, which, l, w);
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out[which]) + (((size_t)b * H) * a.N + n) * D + 8 * l;
+  const bool b0 = l & 1, b1 = l & 2;
+  const float t0 = (b0 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2], 1);
+  const float t1 = (b0 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b0 ? v[1] : v[3], 1);
+  float u = (b1 ? t1 : t0) + __shfl_xor_sync(0xffffffffu, b1 ? t0 : t1, 2);  // row 2 b0 + b1
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * I::RPW + sub;
-    float y[8];
-    unpack8(raw[i], y);
-    if (a.p.norm) {
-      float ss = 0.f;
+  for (int off = 4; off < D / 8; off *= 2) u += __shfl_xor_sync(0xffffffffu, u, off);
+  u = rsqrtf(u * (1.f / D) + eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      const float r = rsqrtf(row_sum<I::LPR>(ss) * (1.f / D) + a.p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
-    }
-    turn_row<false>(a.p, t, y);
-    if (h < H)
-      *reinterpret_cast<uint4*>(dst + (size_t)h * a.N * D) = bad ? make_uint4(0, 0, 0, 0) : pack8(y);
-  }
-  if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+  for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, u, (i >> 1) | ((i & 1) << 1), D / 8);
 }
 
-// ---------------------------------------------------------------- backward ---
-// A warp walks the items with a grid stride and keeps the weights' gradients
-// of its 8 columns in registers (queries and keys apart); a CTA adds up its
-// warps and writes one row of partial sums, and a second kernel adds those in
-// a fixed order: no atomics, the same bits on every run.
-template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeLaunch a) {
-  using I = Item<D>;
-  const int lane = threadIdx.x & 31, l = lane % I::LPR, sub = lane / I::LPR;
-  const int cq = (a.H[0] + I::kRows - 1) / I::kRows, ck = (a.H[1] + I::kRows - 1) / I::kRows;
-  const long long items = (long long)a.B * a.N * (cq + ck);
-  float dw[2][8];
+// A row's 8 columns of this lane, turned and scaled (c and s folded).
+template <int D, bool INTER>
+__device__ __forceinline__ uint4 turn_row(const NormRopeParams& p, const Lane<D, INTER>& ln, const Row& c, const Row& s,
+                                          const uint4& raw, float r) {
+  Row x, o;
+  unpack8(raw, x);
+  unpack8(partner_of<D, INTER>(p, ln, raw), o);
+  const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-  for (long long item = (long long)blockIdx.x * kWarps + threadIdx.x / 32; item < items;
-       item += (long long)gridDim.x * kWarps) {
-    const long long token = item / (cq + ck);
-    const int chunk = (int)(item - token * (cq + ck));
-    const int which = chunk >= cq;
-    const int h0 = (which ? chunk - cq : chunk) * I::kRows, H = a.H[which];
-    const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-    const HeadRows in = a.in[which], dx = a.dx[which];
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + b * in.sb + n * in.sn + 8 * l;
-    const __nv_bfloat16* dsrc =
-        static_cast<const __nv_bfloat16*>(a.dout[which]) + (((size_t)b * H) * a.N + n) * D + 8 * l;
-    uint4 raw[kSteps], draw[kSteps];
+  for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2_fma(o[i], s[i], f2_mul(x[i], c[i])), r2);
+  return pack8(x);
+}
+
+// A chunk: up to kRows heads of one token.
+template <int D, int STEPS>
+struct Chunk {
+  static constexpr int LPR = D / 8;           // lanes a row
+  static constexpr int RPW = 32 / LPR;        // rows a warp and step
+  static constexpr int kRows = RPW * STEPS;   // heads a chunk
+  __host__ __device__ static int of(int H) { return (H + kRows - 1) / kRows; }
+};
+constexpr int kFwdSteps = 4;
+constexpr int kBwdSteps = NRS;
+static_assert(2 * ((kNormRopeMaxHeads + Chunk<128, kBwdSteps>::kRows - 1) / Chunk<128, kBwdSteps>::kRows) <=
+              kNormRopeMaxCtas);
+
+// ----------------------------------------------------------------- forward ---
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, NRF) norm_rope_kernel(const NormRopeLaunch a) {
+  using I = Chunk<D, kFwdSteps>;
+  const int lane = threadIdx.x & 31, sub = lane / I::LPR;
+  const Lane<D, INTER> ln(a.p, lane);
+  const unsigned cq = I::of(a.H[0]);
+  const unsigned group = a.by_chunks.div(blockIdx.x), chunk = blockIdx.x - group * a.by_chunks.d;
+  const int which = chunk >= cq, H = a.H[which];
+  const int h0 = (which ? chunk - cq : chunk) * I::kRows + sub;  // this lane's first head
+  const HeadRows in = a.in[which];
+  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(in.p) + h0 * in.sh + 8 * ln.l;
+  const long long hop = in.sh * I::RPW;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out[which]) + (size_t)h0 * a.N * D + 8 * ln.l;
+  const size_t out_hop = (size_t)a.N * D * I::RPW;
+  Factors<D, INTER> f;
+  f.load(a.p, ln, which);
+  unsigned token = group * a.walk * kWarps + threadIdx.x / 32;
+#pragma unroll 1
+  for (int k = 0; k < a.walk; ++k, token += kWarps) {
+    if (token >= (unsigned)a.B * a.N) return;
+    const unsigned b = a.by_n.div(token), n = token - b * a.N;
+    const __nv_bfloat16* src = base + b * in.sb + n * in.sn;
+    uint4 raw[kFwdSteps];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int h = h0 + i * I::RPW + sub;
-      raw[i] = h < H && a.p.norm ? __ldg(reinterpret_cast<const uint4*>(src + h * in.sh)) : make_uint4(0, 0, 0, 0);
-      draw[i] = h < H ? __ldg(reinterpret_cast<const uint4*>(dsrc + (size_t)h * a.N * D)) : make_uint4(0, 0, 0, 0);
-    }
-    const int pos = a.positions ? __ldg(a.positions + token) : n;
+    for (int i = 0; i < kFwdSteps; ++i, src += hop)
+      raw[i] = h0 + i * I::RPW < H ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    const int pos = a.positions ? __ldg(a.positions + token) : (int)n;
     const bool bad = a.p.dr > 0 && (pos < 0 || pos >= a.p.rope_len);
-    Turn t;
-    load_turn(a.p, bad ? 0 : pos, l, t);
-    float w[8];
-    load_weights(a.p, which, l, w);
-    __nv_bfloat16* dst =
-        static_cast<__nv_bfloat16*>(const_cast<void*>(dx.p)) + b * dx.sb + n * dx.sn + 8 * l;
+    Row c, s;
+    load_angles<D, INTER>(a.p, ln, bad ? 0 : pos, c, s);
+    f.fold(c, s);
+    float r[kFwdSteps];
+    if (a.p.norm) inverse_rms<D, kFwdSteps>(raw, ln.l, a.p.eps, r);
+    __nv_bfloat16* dst = out + ((size_t)b * H * a.N + n) * D;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int h = h0 + i * I::RPW + sub;
-      float g[8];
-      unpack8(draw[i], g);
-      turn_row<true>(a.p, t, g);
-      if (a.p.norm) {
-        float x[8];
-        unpack8(raw[i], x);
-        float ss = 0.f, sg = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(x[e], x[e], ss);
-          sg = fmaf(x[e] * w[e], g[e], sg);
-        }
-#pragma unroll
-        for (int off = I::LPR / 2; off > 0; off /= 2) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          sg += __shfl_xor_sync(0xffffffffu, sg, off);
-        }
-        const float r = rsqrtf(ss * (1.f / D) + a.p.eps);
-        const float k = sg * (1.f / D) * r * r;  // mean(g x r) r, per unit of x
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xr = x[e] * r;
-          if (!bad) {  // a row without a position has no gradient
-            if (which)
-              dw[1][e] = fmaf(g[e], xr, dw[1][e]);
-            else
-              dw[0][e] = fmaf(g[e], xr, dw[0][e]);
-          }
-          g[e] = r * (g[e] * w[e] - x[e] * k);
-        }
-      }
-      if (h < H) *reinterpret_cast<uint4*>(dst + h * dx.sh) = bad ? make_uint4(0, 0, 0, 0) : pack8(g);
+    for (int i = 0; i < kFwdSteps; ++i, dst += out_hop) {
+      const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
+      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
     }
     if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
   }
-  if (a.partial == nullptr) return;
-  // rows of the warp, then the warps of the CTA
-  __shared__ float acc[kWarps][2][D];
+}
+
+// ---------------------------------------------------------------- backward ---
+// The weights' gradients of a thread's 8 columns stay in registers over all its
+// tokens; a CTA adds up its warps and writes one row of partial sums, and a
+// second kernel adds those in a fixed order: no atomics, the same bits on every
+// run.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, NRB) norm_rope_bwd_kernel(const NormRopeLaunch a) {
+  using I = Chunk<D, kBwdSteps>;
+  const int lane = threadIdx.x & 31, sub = lane / I::LPR;
+  const Lane<D, INTER> ln(a.p, lane);
+  const unsigned cq = I::of(a.H[0]);
+  const unsigned group = a.by_chunks.div(blockIdx.x), chunk = blockIdx.x - group * a.by_chunks.d;
+  const int which = chunk >= cq, H = a.H[which];
+  const int h0 = (which ? chunk - cq : chunk) * I::kRows + sub;
+  const HeadRows in = a.in[which], dx = a.dx[which];
+  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(in.p) + h0 * in.sh + 8 * ln.l;
+  const __nv_bfloat16* dbase = static_cast<const __nv_bfloat16*>(a.dout[which]) + (size_t)h0 * a.N * D + 8 * ln.l;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(const_cast<void*>(dx.p)) + h0 * dx.sh + 8 * ln.l;
+  const long long hop = in.sh * I::RPW, out_hop = dx.sh * I::RPW;
+  const size_t dhop = (size_t)a.N * D * I::RPW;
+  Row w, dw = {0, 0, 0, 0};
+  load_weights(a.p, which, ln.l, w);
+  unsigned token = group * a.walk * kWarps + threadIdx.x / 32;
+#pragma unroll 1
+  for (int k = 0; k < a.walk && token < (unsigned)a.B * a.N; ++k, token += kWarps) {
+    const unsigned b = a.by_n.div(token), n = token - b * a.N;
+    const __nv_bfloat16* src = base + b * in.sb + n * in.sn;
+    const __nv_bfloat16* dsrc = dbase + ((size_t)b * H * a.N + n) * D;
+    uint4 raw[kBwdSteps], dz[kBwdSteps];
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float v = dw[q][e];
-#pragma unroll
-      for (int off = I::LPR; off < 32; off *= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
-      if (sub == 0) acc[threadIdx.x / 32][q][8 * l + e] = v;
+    for (int i = 0; i < kBwdSteps; ++i, src += hop, dsrc += dhop) {
+      const bool row = h0 + i * I::RPW < H;
+      raw[i] = row && a.p.norm ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      dz[i] = row ? __ldg(reinterpret_cast<const uint4*>(dsrc)) : make_uint4(0, 0, 0, 0);
     }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-    float v = 0.f;
+    const int pos = a.positions ? __ldg(a.positions + token) : (int)n;
+    const bool bad = a.p.dr > 0 && (pos < 0 || pos >= a.p.rope_len);
+    Row c, s;
+    load_angles<D, INTER>(a.p, ln, bad ? 0 : pos, c, s);
+    signed_row<D, INTER, true>(ln, s);
+    __nv_bfloat16* dst = out + b * dx.sb + n * dx.sn;
 #pragma unroll
-    for (int wp = 0; wp < kWarps; ++wp) v += acc[wp][c / D][c % D];
-    a.partial[(size_t)blockIdx.x * 2 * D + c] = v;
+    for (int i = 0; i < kBwdSteps; ++i, dst += out_hop) {
+      Row g, o;
+      unpack8(dz[i], g);
+      unpack8(partner_of<D, INTER>(a.p, ln, dz[i]), o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = f2_fma(o[e], s[e], f2_mul(g[e], c[e]));  // dy
+      if (a.p.norm) {
+        Row x, gw;
+        unpack8(raw[i], x);
+        uint64_t ss2 = 0, sg2 = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          gw[e] = f2_mul(g[e], w[e]);
+          ss2 = f2_fma(x[e], x[e], ss2);
+          sg2 = f2_fma(x[e], gw[e], sg2);
+        }
+        float ss = pair_sum(ss2), sg = pair_sum(sg2);
+        // both sums at once: even lanes go on with one, odd lanes with the other
+        const bool odd = lane & 1;
+        float v = (odd ? sg : ss) + __shfl_xor_sync(0xffffffffu, odd ? ss : sg, 1);
+#pragma unroll
+        for (int off = I::LPR / 2; off > 1; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+        const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+        ss = odd ? u : v;
+        sg = odd ? v : u;
+        const float r = rsqrtf(ss * (1.f / D) + a.p.eps);
+        const float kk = -sg * (1.f / D) * r * r * r;  // -mean(g x r) r^2, per unit of x
+        const float rw = bad ? 0.f : r;               // a row without a position has no gradient
+        const uint64_t r2 = f2_pack(r, r), k2 = f2_pack(kk, kk), rw2 = f2_pack(rw, rw);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dw[e] = f2_fma(g[e], f2_mul(x[e], rw2), dw[e]);
+          g[e] = f2_fma(x[e], k2, f2_mul(gw[e], r2));
+        }
+      }
+      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : pack8(g);
+    }
+    if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+  }
+  if (a.partial != nullptr) {
+    // rows of the warp, then the warps of the CTA
+    __shared__ float acc[kWarps][D];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      f2_unpack(dw[e], lo, hi);
+#pragma unroll
+      for (int off = I::LPR; off < 32; off *= 2) {
+        lo += __shfl_xor_sync(0xffffffffu, lo, off);
+        hi += __shfl_xor_sync(0xffffffffu, hi, off);
+      }
+      if (sub == 0) acc[threadIdx.x / 32][8 * ln.l + 2 * e] = lo, acc[threadIdx.x / 32][8 * ln.l + 2 * e + 1] = hi;
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float v = 0.f;
+#pragma unroll
+      for (int wp = 0; wp < kWarps; ++wp) v += acc[wp][threadIdx.x];
+      a.partial[(size_t)blockIdx.x * D + threadIdx.x] = v;
+    }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Adds the rows of partial sums: one block per 32 columns, 32 threads a column.
+// Adds the rows of partial sums, those of the queries' chunks and those of the
+// keys' (row r belongs to chunk r mod `chunks`): 8 columns a block, 128 threads
+// a column.
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ partial, int rows, int d,
-                                                            float* dqw, float* dkw) {
+                                                            int cq, int chunks, float* dqw, float* dkw) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float acc[32][33];
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + x;  // of 2 d columns
+  __shared__ float acc[32][8];
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8;
+  const int col = blockIdx.x * 8 + x, which = blockIdx.y;
+  const int first = which ? cq : 0, width = which ? chunks - cq : cq;
+  const int count = rows / chunks * width;
   float v = 0.f;
-  for (int r = y; r < rows; r += 32) v += partial[(size_t)r * 2 * d + col];
-  acc[y][x] = v;
-  __syncthreads();
-  float u = acc[x][y];  // warp y adds column y
+#pragma unroll 4
+  for (int i = y; i < count; i += 128) v += partial[(size_t)(i / width * chunks + first + i % width) * d + col];
 #pragma unroll
-  for (int off = 16; off > 0; off /= 2) u += __shfl_xor_sync(0xffffffffu, u, off);
-  const int c = blockIdx.x * 32 + y;
-  if (x == 0) {
-    float* out = c < d ? dqw : dkw;
-    if (out) out[c < d ? c : c - d] = u;
+  for (int off = 8; off < 32; off *= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (threadIdx.x % 32 < 8) acc[threadIdx.x / 32][x] = v;
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float u = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u += acc[i][x];
+    float* out = which ? dkw : dqw;
+    if (out) out[col] = u;
   }
 }
 
@@ -332,107 +455,108 @@ __device__ __forceinline__ int find_sequence(const int* cu, int S, int t) {
 // one without a slot (in front of position 0, behind the page table or the
 // rotation table, or in a page outside the pool) is not cached, and its query
 // row is zero where it has no position.
-template <int D>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendLaunch a) {
-  using I = Item<D>;
-  const int lane = threadIdx.x & 31, l = lane % I::LPR, sub = lane / I::LPR;
-  const int cq = (a.Hq + I::kRows - 1) / I::kRows, ck = (a.Hk + I::kRows - 1) / I::kRows;
-  const long long item = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
-  const long long tok = item / (cq + 2 * ck);
-  if (tok >= a.T) return;
-  const int t = (int)tok;
-  const int chunk = (int)(item - tok * (cq + 2 * ck));
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendLaunch a) {
+  using I = Chunk<D, kFwdSteps>;
+  const int lane = threadIdx.x & 31, sub = lane / I::LPR;
+  const Lane<D, INTER> ln(a.p, lane);
+  const unsigned cq = I::of(a.Hq), ck = I::of(a.Hk);
+  const unsigned group = a.by_chunks.div(blockIdx.x), chunk = blockIdx.x - group * a.by_chunks.d;
+  const unsigned token = group * kWarps + threadIdx.x / 32;
+  if (token >= (unsigned)a.T) return;
+  const int t = (int)token;
   const int which = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;  // queries, keys, values
-  const int h0 = (chunk - (which == 0 ? 0 : which == 1 ? cq : cq + ck)) * I::kRows;
+  const int h0 = (chunk - (which == 0 ? 0 : which == 1 ? cq : cq + ck)) * I::kRows + sub;
   const int H = which ? a.Hk : a.Hq;
   const HeadRows in = a.in[which];
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + t * in.sn + 8 * l;
-  uint4 raw[kSteps];
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + t * in.sn + h0 * in.sh + 8 * ln.l;
+  const long long in_hop = in.sh * I::RPW;
+  uint4 raw[kFwdSteps];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * I::RPW + sub;
-    raw[i] = h < H ? __ldg(reinterpret_cast<const uint4*>(src + h * in.sh)) : make_uint4(0, 0, 0, 0);
-  }
-  const int s = find_sequence(a.cu_seqlens, a.S, t);
-  if (s < 0 || s >= a.S) return;  // a row of no sequence: left as it was
-  const long long pos = (long long)__ldg(a.kv_lens + s) - __ldg(a.cu_seqlens + s + 1) + t;
-  const bool bad = pos < 0 || pos >= (long long)a.max_pages * a.page_size || (a.p.dr > 0 && pos >= a.p.rope_len);
+  for (int i = 0; i < kFwdSteps; ++i, src += in_hop)
+    raw[i] = h0 + i * I::RPW < H ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+  const int sq = find_sequence(a.cu_seqlens, a.S, t);
+  if (sq < 0 || sq >= a.S) return;  // a row of no sequence: left as it was
+  const long long pos = (long long)__ldg(a.kv_lens + sq) - __ldg(a.cu_seqlens + sq + 1) + t;
+  const int cap = a.max_pages << a.page_log2;
+  const bool bad = pos < 0 || pos >= cap || (a.p.dr > 0 && pos >= a.p.rope_len);
+  const int at = bad ? 0 : (int)pos;
   __nv_bfloat16* dst = nullptr;
   long long step = 0;
   bool lost = bad;  // no place to write
   if (which == 0) {
-    dst = static_cast<__nv_bfloat16*>(a.q_out) + (size_t)t * a.Hq * D + 8 * l;
+    dst = static_cast<__nv_bfloat16*>(a.q_out) + (size_t)t * a.Hq * D + 8 * ln.l;
     step = D;
     lost = false;
   } else if (!bad) {
-    const int page = __ldg(a.page_table + (size_t)s * a.max_pages + pos / a.page_size);
+    const int page = __ldg(a.page_table + (size_t)sq * a.max_pages + (at >> a.page_log2));
     lost = page < 0 || page >= a.num_pages;
     if (!lost) {
       const int kv = which - 1;
-      dst = static_cast<__nv_bfloat16*>(a.pages[kv]) + page * a.page_sp[kv] + (pos % a.page_size) * a.page_sr[kv] +
-            8 * l;
+      dst = static_cast<__nv_bfloat16*>(a.pages[kv]) + page * a.page_sp[kv] +
+            (at & ((1 << a.page_log2) - 1)) * a.page_sr[kv] + 8 * ln.l;
       step = a.page_sh[kv];
     }
   }
   if ((bad || lost) && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
   if (lost) return;
+  dst += h0 * step;
+  step *= I::RPW;
   if (which == 2) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int h = h0 + i * I::RPW + sub;
-      if (h < H) *reinterpret_cast<uint4*>(dst + h * step) = raw[i];
-    }
+    for (int i = 0; i < kFwdSteps; ++i, dst += step)
+      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = raw[i];
     return;
   }
-  Turn tn;
-  load_turn(a.p, bad ? 0 : (int)pos, l, tn);
-  float w[8];
-  load_weights(a.p, which, l, w);
+  Row c, s;
+  load_angles<D, INTER>(a.p, ln, at, c, s);
+  Factors<D, INTER> f;
+  f.load(a.p, ln, which);
+  f.fold(c, s);
+  float r[kFwdSteps];
+  if (a.p.norm) inverse_rms<D, kFwdSteps>(raw, ln.l, a.p.eps, r);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * I::RPW + sub;
-    float y[8];
-    unpack8(raw[i], y);
-    if (a.p.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      const float r = rsqrtf(row_sum<I::LPR>(ss) * (1.f / D) + a.p.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
-    }
-    turn_row<false>(a.p, tn, y);
-    if (h < H) *reinterpret_cast<uint4*>(dst + h * step) = bad ? make_uint4(0, 0, 0, 0) : pack8(y);
+  for (int i = 0; i < kFwdSteps; ++i, dst += step) {
+    const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
+    if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
   }
 }
 
-template <int D>
-long long item_blocks(long long tokens, int chunks) {
-  return (tokens * chunks + kWarps - 1) / kWarps;
+unsigned token_groups(long long tokens) { return (unsigned)((tokens + kWarps - 1) / kWarps); }
+
+// Tokens a warp of the forward walks: several, as long as the device still gets
+// eight CTAs for each it holds.
+int forward_walk(unsigned groups, int chunks, int sms) {
+  int walk = 1;
+  while (walk < NRW && (long long)groups * chunks >= 2ll * walk * NRT * NRF * sms) walk *= 2;
+  return walk;
 }
 
-template <int D>
-int chunks_of(int H) {
-  return (H + Item<D>::kRows - 1) / Item<D>::kRows;
-}
-
-template <int D>
-cudaError_t launch_norm_rope_t(const NormRopeLaunch& a, cudaStream_t stream) {
-  const long long blocks = item_blocks<D>((long long)a.B * a.N, chunks_of<D>(a.H[0]) + chunks_of<D>(a.H[1]));
-  norm_rope_kernel<D><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+template <int D, bool INTER>
+cudaError_t launch_norm_rope_t(NormRopeLaunch a, cudaStream_t stream) {
+  using I = Chunk<D, kFwdSteps>;
+  const unsigned chunks = I::of(a.H[0]) + I::of(a.H[1]), groups = token_groups((long long)a.B * a.N);
+  a.walk = forward_walk(groups, chunks, a.sms);
+  a.by_n = FastDiv(a.N);
+  a.by_chunks = FastDiv(chunks);
+  norm_rope_kernel<D, INTER><<<(groups + a.walk - 1) / a.walk * chunks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_norm_rope_bwd_t(const NormRopeLaunch& a, cudaStream_t stream) {
-  const long long blocks = item_blocks<D>((long long)a.B * a.N, chunks_of<D>(a.H[0]) + chunks_of<D>(a.H[1]));
-  const long long most = 4ll * a.sms < kNormRopeMaxCtas ? 4ll * a.sms : kNormRopeMaxCtas;
-  const int grid = (int)(blocks < most ? blocks : most);
-  norm_rope_bwd_kernel<D><<<grid, kThreads, 0, stream>>>(a);
+template <int D, bool INTER>
+cudaError_t launch_norm_rope_bwd_t(NormRopeLaunch a, cudaStream_t stream) {
+  using I = Chunk<D, kBwdSteps>;
+  const unsigned cq = I::of(a.H[0]), chunks = cq + I::of(a.H[1]), groups = token_groups((long long)a.B * a.N);
+  const unsigned runs = NRV / chunks;  // of tokens, at most: a row of partial sums for each
+  a.walk = (groups + runs - 1) / runs;
+  a.by_n = FastDiv(a.N);
+  a.by_chunks = FastDiv(chunks);
+  const int grid = (groups + a.walk - 1) / a.walk * chunks;
+  norm_rope_bwd_kernel<D, INTER><<<grid, kThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.partial == nullptr) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32);
+  cfg.gridDim = dim3(D / 8, 2);
   cfg.blockDim = dim3(1024);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -440,29 +564,37 @@ cudaError_t launch_norm_rope_bwd_t(const NormRopeLaunch& a, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), grid, D, a.dw[0],
-                            a.dw[1]);
+  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), grid, D, (int)cq,
+                            (int)chunks, a.dw[0], a.dw[1]);
 }
 
-template <int D>
-cudaError_t launch_paged_append_t(const AppendLaunch& a, cudaStream_t stream) {
-  const long long blocks = item_blocks<D>(a.T, chunks_of<D>(a.Hq) + 2 * chunks_of<D>(a.Hk));
-  paged_append_kernel<D><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+template <int D, bool INTER>
+cudaError_t launch_paged_append_t(AppendLaunch a, cudaStream_t stream) {
+  using I = Chunk<D, kFwdSteps>;
+  a.by_chunks = FastDiv(I::of(a.Hq) + 2 * I::of(a.Hk));
+  paged_append_kernel<D, INTER><<<token_groups(a.T) * a.by_chunks.d, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream) {
-  return a.p.d == 64 ? launch_norm_rope_t<64>(a, stream) : launch_norm_rope_t<128>(a, stream);
+  if (a.p.d == 64)
+    return a.p.interleaved ? launch_norm_rope_t<64, true>(a, stream) : launch_norm_rope_t<64, false>(a, stream);
+  return a.p.interleaved ? launch_norm_rope_t<128, true>(a, stream) : launch_norm_rope_t<128, false>(a, stream);
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& a, cudaStream_t stream) {
-  return a.p.d == 64 ? launch_norm_rope_bwd_t<64>(a, stream) : launch_norm_rope_bwd_t<128>(a, stream);
+  if (a.p.d == 64)
+    return a.p.interleaved ? launch_norm_rope_bwd_t<64, true>(a, stream) : launch_norm_rope_bwd_t<64, false>(a, stream);
+  return a.p.interleaved ? launch_norm_rope_bwd_t<128, true>(a, stream)
+                         : launch_norm_rope_bwd_t<128, false>(a, stream);
 }
 
 cudaError_t launch_paged_append(const AppendLaunch& a, cudaStream_t stream) {
-  return a.p.d == 64 ? launch_paged_append_t<64>(a, stream) : launch_paged_append_t<128>(a, stream);
+  if (a.p.d == 64)
+    return a.p.interleaved ? launch_paged_append_t<64, true>(a, stream) : launch_paged_append_t<64, false>(a, stream);
+  return a.p.interleaved ? launch_paged_append_t<128, true>(a, stream) : launch_paged_append_t<128, false>(a, stream);
 }
 
 }  // namespace fa

@@ -13,6 +13,20 @@ struct HeadRows {
   long long sb, sn, sh;
 };
 
+// Division of n < 2^31 by a fixed d: q = (mulhi(n, m) + n) >> l with
+// l = ceil(log2 d), m = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery).
+struct FastDiv {
+  unsigned m, l, d;
+  FastDiv() = default;
+  explicit FastDiv(unsigned d_) : m(0), l(0), d(d_) {
+    while ((1ull << l) < d) ++l;
+    m = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, m) + n) >> l; }
+#endif
+};
+
 struct NormRopeParams {
   int d, dr;               // head dimension; rotated columns (0: no rotation)
   int interleaved;         // pairs (2i, 2i + 1) instead of (i, i + dr / 2)
@@ -32,11 +46,13 @@ struct NormRopeLaunch {
   int H[2];
   int B, N;
   const int* positions;    // [B, N] or null (n)
+  int walk;                // tokens a warp takes
+  FastDiv by_n, by_chunks;
   // backward: dout is what `out` was, dx is strided
   const void* dout[2];
   HeadRows dx[2];
   float* dw[2];            // [d] fp32 or null
-  float* partial;          // [grid, 2, d] fp32
+  float* partial;          // [grid, d] fp32
   int sms;
 };
 
@@ -49,11 +65,15 @@ struct AppendLaunch {
   const int* page_table;   // [S, max_pages]
   const int* cu_seqlens;   // [S + 1]
   const int* kv_lens;      // [S]
-  int T, S, Hq, Hk, num_pages, page_size, max_pages;
+  int T, S, Hq, Hk, num_pages, page_log2, max_pages;
+  FastDiv by_chunks;
 };
 
-// CTAs of the backward kernel at most (the rows of its partial sums).
-constexpr int kNormRopeMaxCtas = 1024;
+// Heads of a tensor at most, and CTAs of the backward kernel (the rows of its
+// partial sums): it takes one for every chunk of at least four heads, and
+// multiples of that up to three an SM.
+constexpr int kNormRopeMaxHeads = 2048;
+constexpr int kNormRopeMaxCtas = 2048;
 
 cudaError_t launch_norm_rope(const NormRopeLaunch& a, cudaStream_t stream);
 cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& a, cudaStream_t stream);

@@ -57,8 +57,8 @@ int check_norm_rope(NormRopeParams* p, int d, int norm, const void* qw, const vo
 }
 
 bool sizes_ok(int B, int Hq, long long Hk, int N) {
-  // 2^15 heads and 2^31 tokens keep the launch grid below its limit
-  return B >= 1 && N >= 1 && Hq >= 1 && Hk >= 1 && Hq < (1 << 15) && Hk < (1 << 15) &&
+  // (the last bound keeps the launch grid below its limit)
+  return B >= 1 && N >= 1 && Hq >= 1 && Hk >= 1 && Hq <= kNormRopeMaxHeads && Hk <= 2 * kNormRopeMaxHeads &&
          (long long)B * N <= INT_MAX && (long long)B * N * (Hq + Hk) < (1ll << 34);
 }
 
@@ -73,7 +73,7 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
                                const void* q_weight, const void* k_weight, int weights_f32, float eps,
                                const float* rope, int rope_len, int rope_dim, int interleaved, const int* positions,
                                cudaStream_t stream) {
-  if (!sizes_ok(B, Hq, Hk, N)) return FA_ERR_INVALID_ARG;
+  if (!sizes_ok(B, Hq, Hk, N) || Hk > kNormRopeMaxHeads) return FA_ERR_INVALID_ARG;
   NormRopeLaunch a = {};
   int st = check_norm_rope(&a.p, d, norm, q_weight, k_weight, weights_f32, eps, rope, rope_len, rope_dim, interleaved,
                            positions ? 0 : N);
@@ -95,12 +95,13 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
   a.B = B;
   a.N = N;
   a.positions = positions;
+  a.sms = dev.sms;
   return cuda_status(launch_norm_rope(a, stream));
 }
 
 extern "C" size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
-  return (size_t)kNormRopeMaxCtas * 2 * d * sizeof(float);
+  return (size_t)kNormRopeMaxCtas * d * sizeof(float);
 }
 
 extern "C" int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, void* dq,
@@ -113,7 +114,7 @@ extern "C" int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const
                                    const float* rope, int rope_len, int rope_dim, int interleaved,
                                    const int* positions, void* workspace, size_t workspace_bytes,
                                    cudaStream_t stream) {
-  if (!sizes_ok(B, Hq, Hk, N)) return FA_ERR_INVALID_ARG;
+  if (!sizes_ok(B, Hq, Hk, N) || Hk > kNormRopeMaxHeads) return FA_ERR_INVALID_ARG;
   NormRopeLaunch a = {};
   int st = check_norm_rope(&a.p, d, norm, q_weight, k_weight, weights_f32, eps, rope, rope_len, rope_dim, interleaved,
                            positions ? 0 : N);
@@ -223,7 +224,7 @@ extern "C" int fa_paged_append(const void* q, const void* k, const void* v, void
   a.Hq = Hq;
   a.Hk = Hk;
   a.num_pages = num_pages;
-  a.page_size = page_size;
+  while ((1 << a.page_log2) < page_size) ++a.page_log2;
   a.max_pages = max_pages;
   return cuda_status(launch_paged_append(a, stream));
 }

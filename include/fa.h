@@ -257,8 +257,8 @@ int fa_bwd_dq_convert(void* dq, int B, int H, int N, int d, float scale, const v
  *
  * A position outside [0, rope_len) gives a zero row (and a zero gradient row)
  * and records FA_ERR_DEVICE_INDEX in the device status word.  Head counts may
- * differ (grouped key heads).  Sizes are not limited to 2^31 elements here;
- * B*N < 2^31.
+ * differ (grouped key heads), up to 2048 each.  Tensors are not limited to 2^31
+ * elements here; B*N < 2^31 and B*N*(Hq+Hk) < 2^34.
  */
 int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int Hq, int Hk, int N, int d,
                     long long q_stride_b, long long q_stride_h, long long q_stride_n, long long k_stride_b,

@@ -16,11 +16,12 @@
 // columns; the sum of squares and a split rotation's partner columns come by
 // shuffle), a warp takes 32 / (d / 8) rows at once and STEPS such steps: a
 // chunk of one token's heads, so that the token's cosines and sines are loaded
-// once for all of them.  A CTA keeps one chunk and walks the tokens, its warps
-// on neighbouring ones: weights, pointers and the kind of rotation cost nothing
-// a token, and a token's rows are loaded before the last one's are computed.
-// (One token a warp spent 160 instructions on 512 bytes of input and was bound
-// by their issue, 93 us for the case below; so paired fp32 arithmetic as well.)
+// once for all of them.  A CTA takes one chunk of neighbouring tokens (its
+// warps one after the other, each a few), the CTAs of a token's chunks are
+// neighbours, so its table row comes from the caches after the first.  Many
+// short CTAs: a grid of resident ones that walk all tokens measured 91 to 111
+// us, with loads in flight through registers or cp.async, against 85 (0.54 GB,
+// 79 us at the copy rate).
 // The input may be any strided view (a slice of the projection's output); the
 // output is the contiguous [B, H, N, d] that the attention kernels read, so the
 // transposition costs no pass of its own.  Everything between load and store is
@@ -32,24 +33,6 @@
 #include "fa_norm_rope.cuh"
 #include "sm103_ptx.cuh"
 
-#ifndef NRF
-#define NRF 4
-#endif
-#ifndef NRT
-#define NRT 8
-#endif
-#ifndef NRB
-#define NRB 2
-#endif
-#ifndef NRS
-#define NRS 4
-#endif
-#ifndef NRW
-#define NRW 8
-#endif
-#ifndef NRV
-#define NRV 2048
-#endif
 namespace fa {
 namespace {
 
@@ -251,13 +234,18 @@ struct Chunk {
   __host__ __device__ static int of(int H) { return (H + kRows - 1) / kRows; }
 };
 constexpr int kFwdSteps = 4;
-constexpr int kBwdSteps = NRS;
+// CTAs an SM of the forward: at three (80 registers) nothing spills; four and
+// five measured 89 and 110 us against 85 (B = 64, N = 1024, 16 + 16 heads, d = 64).
+constexpr int kFwdCtas = 3;
+// The gradient at 4 steps and two CTAs an SM: 153 us; 2 steps and three 171,
+// 1 step and four 188 (the same sizes: 0.8 GB, 119 us at the copy rate).
+constexpr int kBwdSteps = 4;
 static_assert(2 * ((kNormRopeMaxHeads + Chunk<128, kBwdSteps>::kRows - 1) / Chunk<128, kBwdSteps>::kRows) <=
               kNormRopeMaxCtas);
 
 // ----------------------------------------------------------------- forward ---
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, NRF) norm_rope_kernel(const NormRopeLaunch a) {
+__global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const NormRopeLaunch a) {
   using I = Chunk<D, kFwdSteps>;
   const int lane = threadIdx.x & 31, sub = lane / I::LPR;
   const Lane<D, INTER> ln(a.p, lane);
@@ -305,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, NRF) norm_rope_kernel(const NormRope
 // second kernel adds those in a fixed order: no atomics, the same bits on every
 // run.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, NRB) norm_rope_bwd_kernel(const NormRopeLaunch a) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeLaunch a) {
   using I = Chunk<D, kBwdSteps>;
   const int lane = threadIdx.x & 31, sub = lane / I::LPR;
   const Lane<D, INTER> ln(a.p, lane);
@@ -524,11 +512,12 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendL
 
 unsigned token_groups(long long tokens) { return (unsigned)((tokens + kWarps - 1) / kWarps); }
 
-// Tokens a warp of the forward walks: several, as long as the device still gets
-// eight CTAs for each it holds.
+// Tokens a warp of the forward walks: up to four, as long as the device gets
+// two rounds of CTAs.  One token a warp spends as much on its own set-up as on
+// the rows: 94 us against 85 at four (the sizes above); more leave a tail.
 int forward_walk(unsigned groups, int chunks, int sms) {
   int walk = 1;
-  while (walk < NRW && (long long)groups * chunks >= 2ll * walk * NRT * NRF * sms) walk *= 2;
+  while (walk < 4 && (long long)groups * chunks >= 2ll * walk * 2 * kFwdCtas * sms) walk *= 2;
   return walk;
 }
 
@@ -547,7 +536,7 @@ template <int D, bool INTER>
 cudaError_t launch_norm_rope_bwd_t(NormRopeLaunch a, cudaStream_t stream) {
   using I = Chunk<D, kBwdSteps>;
   const unsigned cq = I::of(a.H[0]), chunks = cq + I::of(a.H[1]), groups = token_groups((long long)a.B * a.N);
-  const unsigned runs = NRV / chunks;  // of tokens, at most: a row of partial sums for each
+  const unsigned runs = kNormRopeMaxCtas / chunks;  // of tokens, at most: a row of partial sums for each
   a.walk = (groups + runs - 1) / runs;
   a.by_n = FastDiv(a.N);
   a.by_chunks = FastDiv(chunks);

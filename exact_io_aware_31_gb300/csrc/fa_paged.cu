@@ -21,15 +21,20 @@
 // their maxima and sums in the workspace, at most two a CTA, and a second kernel
 // (a programmatic dependent) merges them in a fixed order: no atomics on results.
 //
-// Two forms of a unit share the code:
-//   two tiles  256 rows against each key tile: warpgroup t owns query tile t
-//   one tile   128 rows or fewer: warpgroup t takes every other key tile of the
-//              same rows, with S and O of its own, merged at the unit's end.
-//              A single token's softmax is one warp's work of about 2000 cycles a
-//              key tile, latency that two key tiles in flight hide behind the
-//              ~2800 cycles in which the SM's share of HBM brings 64 KiB.
-// The kernel for short chunks (WIDE = false) has one query buffer's worth of
-// tile and a deeper K / V ring; the other takes both forms.
+// Three forms of a unit, by its query rows; warpgroups t = 0, 1:
+//   two tiles   up to 256 rows against each key tile: warpgroup t owns tile t
+//   one tile    33 to 128 rows: warpgroup t takes every other key tile of the
+//               same rows, with S and O of its own, merged at the unit's end
+//   four copies up to 32 rows (single tokens): as one tile, and the rows are
+//               copied into each quarter of the tile, whose warp takes a quarter
+//               of the columns (its P is zero in the others).  A warp that had
+//               32 rows to itself spent about 2000 cycles a key tile on one
+//               lane's 128 exponentials while three warps idled: 64 sequences
+//               of 256 to 1024 keys, 8 tokens each, 16 heads, d = 64 ran in 68 us.
+//               The eight partial rows are merged through the unit's own query
+//               buffer, which is dead by then.
+// SHORT kernels hold only the last form: the host takes them where it was told
+// that chunks are short; a longer chunk is then a row of small units.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax warpgroups, 8 producer, 9 MMA issuer,
 // 10 clears the rows of V behind a sequence's end (what lies there in a page is
@@ -38,6 +43,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_common.cuh"
@@ -50,12 +57,15 @@ namespace {
 
 using namespace paged;
 
-template <int D, bool WIDE>
+template <int D>
 struct PagedCfg {
   static constexpr int kTileBytes = kTileRows * D * 2;
   static constexpr int kBlocks = D / 64;
-  static constexpr int kQTiles = WIDE ? 2 : 1;
-  static constexpr int kStages = D == 128 ? (WIDE ? 2 : 3) : (WIDE ? 5 : 6);
+  // Slots of the K and V rings; the rest is two query buffers.  A K slot is
+  // free once S is done, long before its V slot; the next K is what the MMA
+  // issuer waits for first.
+  static constexpr int kKSlots = D == 128 ? 3 : 6;
+  static constexpr int kVSlots = D == 128 ? 2 : 5;
   static constexpr int kThreads = 384;
   // Register split of the forward kernel: 2 x 128 x 200 + 128 x 104 = 384 x 168.
   static constexpr int kLaunchRegs = 168;
@@ -66,13 +76,13 @@ struct PagedCfg {
   static constexpr int kColS = 0;    // + 128 t, P over it
   static constexpr int kColO = 256;  // + 128 t
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kQTiles * kTileBytes;
-  static constexpr int kOffV = kOffK + kStages * kTileBytes;
-  static constexpr int kOffMl = kOffV + kStages * kTileBytes;  // [2][128] (m, l) of the two halves of a one-tile unit
-  static constexpr int kOffPlan = kOffMl + 2 * 128 * 8;
+  static constexpr int kOffK = kOffQ + 2 * kTileBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kTileBytes;
+  static constexpr int kOffMl = kOffV + kVSlots * kTileBytes;  // [2 buffers][8 warps][8 rows] (m, l)
+  static constexpr int kOffPlan = kOffMl + 2 * 64 * 8;
   static constexpr int kPlanBytes = 192;
   static constexpr int kOffBar = kOffPlan + kPlanBytes;
-  static constexpr int kNumBars = 4 + 5 * kStages + 6 + 3;
+  static constexpr int kNumBars = 4 + 4 + 2 * kKSlots + 3 * kVSlots + 6 + 1;
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4;
@@ -194,26 +204,38 @@ __device__ void make_plan(const PagedParams& p, int ut, Plan* plan) {
 }
 
 struct PagedBars {
-  uint64_t* q_full;    // [2] per query tile (two buffers of the one-tile kernel)
-  uint64_t* q_empty;   // [2]
-  uint64_t* k_full;    // [stages]
-  uint64_t* v_full;
+  uint64_t* q_full;   // [2] per query buffer
+  uint64_t* q_empty;  // [2] a two-tile unit's last S has read it
+  uint64_t* x_done;   // [2] a one-tile unit's partial rows are merged: its query buffer is free
+  uint64_t* x_full;   // both warpgroups' partial rows are in shared memory
+  uint64_t* x_next;   // ... and have been read: the unit's next eight rows may follow
+  uint64_t* k_full;   // [K slots]
   uint64_t* k_empty;
+  uint64_t* v_full;   // [V slots]
   uint64_t* v_empty;
-  uint64_t* s_full;    // [2]
-  uint64_t* p_full;    // [2]
-  uint64_t* o_full;    // [2]
-  uint64_t* v_clear;   // [stages] the rows behind the sequence's end are zero (one phase a tile that has such rows)
-  uint64_t* ml_full;   // one-tile units: both halves' (m, l) are in shared memory
-  uint64_t* ml_empty;  // ... and both halves' outputs have been read
+  uint64_t* v_clear;  // the rows behind the sequence's end are zero (one phase a tile that has such rows)
+  uint64_t* s_full;   // [2]
+  uint64_t* p_full;   // [2]
+  uint64_t* o_full;   // [2]
   uint64_t* mma_done;
 };
 
-template <int D, bool WIDE>
+// Which form a segment's unit takes.
+enum Form { kTwoTiles, kOneTile, kFourCopies };
+
+// 32 bytes of a row.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int D, bool SHORT>
 __global__ void __launch_bounds__(384, 1)
-    paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
-  using C = PagedCfg<D, WIDE>;
+    paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q4,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ PagedParams p) {
+  using C = PagedCfg<D>;
   // A negative scale: S is computed negated and the softmax uses |c2|.
   const uint32_t s_negate = p.c2 < 0.f ? kIdescNegateA : 0u;
   const float c2 = fabsf(p.c2);
@@ -226,42 +248,46 @@ __global__ void __launch_bounds__(384, 1)
   PagedBars B;
   B.q_full = bars;
   B.q_empty = B.q_full + 2;
-  B.k_full = B.q_empty + 2;
-  B.v_full = B.k_full + C::kStages;
-  B.k_empty = B.v_full + C::kStages;
-  B.v_empty = B.k_empty + C::kStages;
-  B.s_full = B.v_empty + C::kStages;
+  B.x_done = B.q_empty + 2;
+  B.x_full = B.x_done + 2;
+  B.x_next = B.x_full + 1;
+  B.k_full = B.x_next + 1;
+  B.k_empty = B.k_full + C::kKSlots;
+  B.v_full = B.k_empty + C::kKSlots;
+  B.v_empty = B.v_full + C::kVSlots;
+  B.v_clear = B.v_empty + C::kVSlots;
+  B.s_full = B.v_clear + C::kVSlots;
   B.p_full = B.s_full + 2;
   B.o_full = B.p_full + 2;
-  B.v_clear = B.o_full + 2;
-  B.ml_full = B.v_clear + C::kStages;
-  B.ml_empty = B.ml_full + 1;
-  B.mma_done = B.ml_empty + 1;
+  B.mma_done = B.o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
   Plan* plan = reinterpret_cast<Plan*>(sm + C::kOffPlan);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int tt = p.tile_tokens;
-  const int ut = C::kQTiles * tt;  // tokens a unit
+  const int tt = p.tile_tokens, t4 = p.copy_tokens;
+  const int ut = SHORT ? t4 : 2 * tt;  // tokens a unit
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.q_full[i], 1);
       mbar_init(&B.q_empty[i], 1);
+      mbar_init(&B.x_done[i], 256);
       mbar_init(&B.s_full[i], 1);
       mbar_init(&B.p_full[i], 128);
       mbar_init(&B.o_full[i], 1);
     }
-    for (int st = 0; st < C::kStages; ++st) {
+    for (int st = 0; st < C::kKSlots; ++st) {
       mbar_init(&B.k_full[st], 1);
-      mbar_init(&B.v_full[st], 1);
       mbar_init(&B.k_empty[st], 1);
+    }
+    for (int st = 0; st < C::kVSlots; ++st) {
+      mbar_init(&B.v_full[st], 1);
       mbar_init(&B.v_empty[st], 2);  // the MMA issuer and warp 10
       mbar_init(&B.v_clear[st], 1);
     }
-    mbar_init(B.ml_full, 256);
-    mbar_init(B.ml_empty, 256);
+    mbar_init(B.x_full, 256);
+    mbar_init(B.x_next, 256);
     mbar_init(B.mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -272,6 +298,7 @@ __global__ void __launch_bounds__(384, 1)
   }
   if (warp == 8 && lane == 0) {
     tma_prefetch_map(&tm_q);
+    tma_prefetch_map(&tm_q4);
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
   }
@@ -281,89 +308,111 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const Work work(p);
-  // Whether the segment's unit has one query tile: both warpgroups share its rows.
-  auto one_tile = [&](const Segment& g) { return !WIDE || g.ntok <= tt; };
+  auto form_of = [&](const Segment& g) {
+    return SHORT || g.ntok <= t4 ? kFourCopies : g.ntok <= tt ? kOneTile : kTwoTiles;
+  };
+  auto start = [&] { return walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut); };
 
   if (warp >= 8) {
     regs_dec<C::kAuxRegs>();
-    // Query buffers: [tile] in the two-tile kernel, a ring of q_bufs in the other.
-    const int q_blk = (!WIDE && p.q_bufs == 2) ? kSwzBlockBytes / 2 : kSwzBlockBytes;
-    const int q_bytes = q_blk * C::kBlocks;
-    const int q_bufs = WIDE ? 1 : p.q_bufs;
     if (warp == 8) {
       // ------------------------------------------------------------ producer --
-      Walk w = walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut);
+      Walk w = start();
       Segment g;
       const int box_rows = min(1 << p.page_log2, kTileRows);
-      const int per_tile = kTileRows / box_rows;   // pages of a key tile (1 if pages are longer)
+      const int per_tile = kTileRows / box_rows;  // pages of a key tile (1 if pages are longer)
       const uint32_t box_bytes = box_rows * 128;
-      const uint32_t q_box = tt * p.G * 128;
-      uint32_t qcnt[2] = {0, 0}, kv_it = 0;
+      // Query buffers: two-tile units take both (buffer t for tile t), the
+      // others one in turn.  What frees a buffer depends on its last user.
+      uint32_t q_uses[2] = {0, 0};            // copies into each buffer
+      uint32_t by_mma[2] = {0, 0}, by_merge[2] = {0, 0};
+      bool merged[2] = {false, false};
+      uint32_t turn = 0, kv_it = 0;
       bool ok = true, lost = false;
+      auto wait_q = [&](int b) {
+        if (merged[b]) return mbar_wait_warp(&B.x_done[b], (by_merge[b] - 1) & 1, status);
+        return by_mma[b] == 0 || mbar_wait_warp(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
+      };
       while (ok && walk_get(work, w, ut, g)) {
-        const bool one = one_tile(g);
+        const Form form = form_of(g);
         const int* table = p.page_table + (size_t)w.s * p.max_pages;
-        // this lane's page of key tile j: outside the pool, the copy reads past the
-        // map's last page and fills with zeros
-        auto page_of = [&](int j) {
-          int id = p.num_pages;
-          if (lane < per_tile) {
-            const int first = j * kTileRows + lane * box_rows;
-            if (first < w.q.kv) {
-              id = __ldg(table + (first >> p.page_log2));
-              if (id < 0 || id >= p.num_pages) {
-                id = p.num_pages;
-                lost = true;
-              }
-            }
-          }
-          return id;
+        const int pages = (w.q.kv + (1 << p.page_log2) - 1) >> p.page_log2;
+        // this lane's page of key tile j, asked for a tile ahead
+        auto page_at = [&](int j) {
+          const int at = (j * kTileRows + lane * box_rows) >> p.page_log2;
+          return lane < per_tile && at < pages ? __ldg(table + at) : 0;
         };
-        int page = page_of(g.j0);
-#pragma unroll
-        for (int t = 0; t < C::kQTiles; ++t) {
-          if (!ok || (t == 1 && one)) continue;
-          if (WIDE && !one && t == 0 && tile0_count(w.q, g, tt, p.causal) == 0) continue;
-          const int bi = WIDE ? t : qcnt[0] % q_bufs;
-          const uint32_t use = WIDE ? qcnt[t] : qcnt[0] / q_bufs;
-          if (!(ok = mbar_wait_warp(&B.q_empty[bi], (use & 1) ^ 1, status))) break;
+        int next = page_at(g.j0);
+        const int q_row = w.q.q0 + g.tok0;
+        auto load_q = [&](int b, const CUtensorMap* map, int copies, uint32_t box, int row) {
           if (lane == 0) {
-            uint8_t* dst = sm + C::kOffQ + bi * q_bytes;
-            mbar_expect_tx(&B.q_full[bi], q_box * C::kBlocks);
+            uint8_t* dst = sm + C::kOffQ + b * C::kTileBytes;
+            mbar_expect_tx(&B.q_full[b], copies * box * C::kBlocks);
             for (int kb = 0; kb < C::kBlocks; ++kb)
-              tma_load_4d(dst + kb * q_blk, &tm_q, &B.q_full[bi], 64 * kb, 0, w.hk, w.q.q0 + g.tok0 + t * tt);
+              for (int c = 0; c < copies; ++c)
+                tma_load_4d(dst + kb * kSwzBlockBytes + c * (kSwzBlockBytes / 4), map, &B.q_full[b], 64 * kb, 0, w.hk,
+                            row);
           }
           __syncwarp();
-          ++qcnt[WIDE ? t : 0];
+        };
+        if (form == kTwoTiles) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || (t == 0 && tile0_count(w.q, g, tt, p.causal) == 0)) continue;
+            if (!(ok = wait_q(t))) break;
+            load_q(t, &tm_q, 1, tt * p.G * 128, q_row + t * tt);
+            ++q_uses[t];
+            ++by_mma[t];
+            merged[t] = false;
+          }
+        } else {
+          const int b = turn & 1;
+          ++turn;
+          ok = b ? wait_q(1) : wait_q(0);
+          if (!ok) break;
+          if (form == kFourCopies)
+            load_q(b, &tm_q4, 4, t4 * p.G * 128, q_row);
+          else
+            load_q(b, &tm_q, 1, tt * p.G * 128, q_row);
+          if (b) {
+            ++q_uses[1], ++by_merge[1], merged[1] = true;
+          } else {
+            ++q_uses[0], ++by_merge[0], merged[0] = true;
+          }
         }
         for (int j = g.j0; j < g.j1 && ok; ++j, ++kv_it) {
-          const int st = kv_it % C::kStages;
-          const uint32_t ph = (kv_it / C::kStages) & 1;
           const int left = w.q.kv - j * kTileRows;  // keys from this tile on
           const int boxes = left <= 0 ? 0 : min(per_tile, (left + box_rows - 1) / box_rows);
           const int row = per_tile == 1 ? (j * kTileRows) & ((1 << p.page_log2) - 1) : 0;
-          const int cur = page;
-          if (j + 1 < g.j1) page = page_of(j + 1);
-          if (!(ok = mbar_wait_warp(&B.k_empty[st], ph ^ 1, status))) break;
-          if (lane == 0) mbar_expect_tx(&B.k_full[st], boxes * box_bytes * C::kBlocks);
+          int page = next;
+          if (j + 1 < g.j1) next = page_at(j + 1);
+          if (page < 0 || page >= p.num_pages) {
+            // outside the pool: the copy reads past the map's last page and fills with zeros
+            page = p.num_pages;
+            lost = lost || lane < boxes;
+          }
+          const int ks = kv_it % C::kKSlots, vs = kv_it % C::kVSlots;
+          const uint32_t kph = (kv_it / C::kKSlots) & 1, vph = (kv_it / C::kVSlots) & 1;
+          if (!(ok = mbar_wait_warp(&B.k_empty[ks], kph ^ 1, status))) break;
+          if (lane == 0) mbar_expect_tx(&B.k_full[ks], boxes * box_bytes * C::kBlocks);
           __syncwarp();
           if (lane < boxes) {
-            uint8_t* dst = sm + C::kOffK + st * C::kTileBytes + lane * box_bytes;
+            uint8_t* dst = sm + C::kOffK + ks * C::kTileBytes + lane * box_bytes;
             for (int kb = 0; kb < C::kBlocks; ++kb)
-              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[st], 64 * kb, row, w.hk, cur);
+              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[ks], 64 * kb, row, w.hk, page);
           }
           __syncwarp();
-          if (!(ok = mbar_wait_warp(&B.v_empty[st], ph ^ 1, status))) {
+          if (!(ok = mbar_wait_warp(&B.v_empty[vs], vph ^ 1, status))) {
             // the K copy of this tile is in flight: it lands before the block ends
-            mbar_wait_warp(&B.k_full[st], ph, status);
+            mbar_wait_warp(&B.k_full[ks], kph, status);
             break;
           }
-          if (lane == 0) mbar_expect_tx(&B.v_full[st], boxes * box_bytes * C::kBlocks);
+          if (lane == 0) mbar_expect_tx(&B.v_full[vs], boxes * box_bytes * C::kBlocks);
           __syncwarp();
           if (lane < boxes) {
-            uint8_t* dst = sm + C::kOffV + st * C::kTileBytes + lane * box_bytes;
+            uint8_t* dst = sm + C::kOffV + vs * C::kTileBytes + lane * box_bytes;
             for (int kb = 0; kb < C::kBlocks; ++kb)
-              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_v, &B.v_full[st], 64 * kb, row, w.hk, cur);
+              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_v, &B.v_full[vs], 64 * kb, row, w.hk, page);
           }
           __syncwarp();
         }
@@ -374,70 +423,72 @@ __global__ void __launch_bounds__(384, 1)
       if (lost) atomicExch(status, FA_ERR_DEVICE_INDEX);
       // Drain: every copy this warp started lands before the block ends.
 #pragma unroll
-      for (int t = 0; t < (WIDE ? 2 : 1); ++t) {
-        const uint32_t bufs = q_bufs;
-        for (uint32_t x = qcnt[t] > bufs ? qcnt[t] - bufs : 0; x < qcnt[t]; ++x)
-          mbar_wait_warp(&B.q_full[WIDE ? t : x % bufs], (x / bufs) & 1, status);
-      }
-      for (uint32_t i = kv_it > (uint32_t)C::kStages ? kv_it - C::kStages : 0; i < kv_it; ++i) {
-        mbar_wait_warp(&B.k_full[i % C::kStages], (i / C::kStages) & 1, status);
-        mbar_wait_warp(&B.v_full[i % C::kStages], (i / C::kStages) & 1, status);
-      }
+      for (int b = 0; b < 2; ++b)
+        if (q_uses[b] > 0) mbar_wait_warp(&B.q_full[b], (q_uses[b] - 1) & 1, status);
+      for (uint32_t i = kv_it > (uint32_t)C::kKSlots ? kv_it - C::kKSlots : 0; i < kv_it; ++i)
+        mbar_wait_warp(&B.k_full[i % C::kKSlots], (i / C::kKSlots) & 1, status);
+      for (uint32_t i = kv_it > (uint32_t)C::kVSlots ? kv_it - C::kVSlots : 0; i < kv_it; ++i)
+        mbar_wait_warp(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer --
-      Walk w = walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut);
+      Walk w = start();
       Segment g;
       const uint32_t idS = idesc_bf16(128, 128, 0, 0) | s_negate;  // S = (+/-) Q K^T, both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);            // O += P V, V is MN-major
       const uint32_t q_s = smem_addr(sm + C::kOffQ);
       const uint32_t k_s = smem_addr(sm + C::kOffK);
       const uint32_t v_s = smem_addr(sm + C::kOffV);
-      uint32_t qcnt[2] = {0, 0}, pcnt[2] = {0, 0}, kv_it = 0, clears = 0;  // clears: bit st = parity of v_clear[st]
+      uint32_t q_uses[2] = {0, 0}, pcnt[2] = {0, 0}, turn = 0, kv_it = 0;
+      uint32_t clears = 0;  // bit st: parity of v_clear[st]
       bool ok = true;
       auto issue_s = [&](int t, uint32_t qa, uint32_t it) {
-        const uint32_t ka = k_s + (it % C::kStages) * C::kTileBytes;
+        const uint32_t ka = k_s + (it % C::kKSlots) * C::kTileBytes;
 #pragma unroll
         for (int kb = 0; kb < C::kBlocks; ++kb)
-          mma_ss_run_w<4, 2, 2>(tbase + C::kColS + 128 * t, sdesc(qa + kb * q_blk, 16, 1024),
+          mma_ss_run_w<4, 2, 2>(tbase + C::kColS + 128 * t, sdesc(qa + kb * kSwzBlockBytes, 16, 1024),
                                 sdesc(ka + kb * kSwzBlockBytes, 16, 1024), idS, kb > 0);
         mma_commit_w(&B.s_full[t]);
       };
       auto wait_k = [&](uint32_t it) {
-        if (!mbar_wait_warp(&B.k_full[it % C::kStages], (it / C::kStages) & 1, status)) return false;
+        if (!mbar_wait_warp(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
         tc_fence_after();
         return true;
       };
       auto issue_pv = [&](int t, uint32_t it, bool accumulate) {
         mma_ts_run_w<8, 8, 128>(tbase + C::kColO + 128 * t, tbase + C::kColS + 128 * t,
-                                sdesc(v_s + (it % C::kStages) * C::kTileBytes, kSwzBlockBytes, 1024), kIdO,
+                                sdesc(v_s + (it % C::kVSlots) * C::kTileBytes, kSwzBlockBytes, 1024), kIdO,
                                 accumulate);
       };
       while (ok && walk_get(work, w, ut, g)) {
-        const bool one = one_tile(g);
+        const Form form = form_of(g);
         const int nt = g.j1 - g.j0;
-        const int tail = w.q.kv - (last_tile(w.q.kv) << 7) < kTileRows ? last_tile(w.q.kv) : -1;
-        // V of key tile j: cleared behind the end where the sequence ends in it
+        const int last = last_tile(w.q.kv);
+        const int tail = w.q.kv - (last << 7) < kTileRows ? last - g.j0 : -1;
+        // V of the segment's key tile i: cleared behind the end where the sequence ends in it
         auto wait_v = [&](int i) {
           const uint32_t it = kv_it + i;
-          const int st = it % C::kStages;
-          if (g.j0 + i == tail) {
+          const int st = it % C::kVSlots;
+          if (i == tail) {
             const uint32_t parity = (clears >> st) & 1;
             clears ^= 1u << st;
             return mbar_wait_warp(&B.v_clear[st], parity, status);
           }
-          return mbar_wait_warp(&B.v_full[st], (it / C::kStages) & 1, status);
+          return mbar_wait_warp(&B.v_full[st], (it / C::kVSlots) & 1, status);
         };
-        if (one) {
-          const int bi = WIDE ? 0 : qcnt[0] % q_bufs;
-          const uint32_t qa = q_s + bi * q_bytes;
-          ok = mbar_wait_warp(&B.q_full[bi], (qcnt[0] / q_bufs) & 1, status);
-          ++qcnt[0];
+        if (form != kTwoTiles) {
+          const int b = turn & 1;
+          ++turn;
+          const uint32_t qa = q_s + b * C::kTileBytes;
+          ok = mbar_wait_warp(&B.q_full[b], (b ? q_uses[1] : q_uses[0]) & 1, status);
+          if (b)
+            ++q_uses[1];
+          else
+            ++q_uses[0];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok || i >= nt || !(ok = wait_k(kv_it + i))) continue;
             issue_s(i, qa, kv_it + i);
-            mma_commit_w(&B.k_empty[(kv_it + i) % C::kStages]);
-            if (i + 1 == nt) mma_commit_w(&B.q_empty[bi]);  // the last S of the segment
+            mma_commit_w(&B.k_empty[(kv_it + i) % C::kKSlots]);
           }
           for (int i = 0; i < nt && ok; ++i) {
             const int t = i & 1;
@@ -449,33 +500,32 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok || !(ok = wait_v(i))) break;
             tc_fence_after();
             issue_pv(t, kv_it + i, i >= 2);
-            mma_commit_w(&B.v_empty[(kv_it + i) % C::kStages]);
+            mma_commit_w(&B.v_empty[(kv_it + i) % C::kVSlots]);
             if (i + 2 < nt) {
               if (!(ok = wait_k(kv_it + i + 2))) break;
               issue_s(t, qa, kv_it + i + 2);
-              mma_commit_w(&B.k_empty[(kv_it + i + 2) % C::kStages]);
-              if (i + 3 == nt) mma_commit_w(&B.q_empty[bi]);
+              mma_commit_w(&B.k_empty[(kv_it + i + 2) % C::kKSlots]);
             } else {
-              mma_commit_w(&B.o_full[t]);
+              mma_commit_w(&B.o_full[t]);  // covers the segment's last S too: issued before
             }
           }
-        } else if constexpr (WIDE) {
+        } else if constexpr (!SHORT) {
           const int cnt[2] = {tile0_count(w.q, g, tt, p.causal), nt};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || cnt[t] == 0) continue;
-            ok = mbar_wait_warp(&B.q_full[t], qcnt[t] & 1, status);
-            ++qcnt[t];
+            ok = mbar_wait_warp(&B.q_full[t], q_uses[t] & 1, status);
+            ++q_uses[t];
           }
           if (ok) ok = wait_k(kv_it);
           if (ok) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (cnt[t] == 0) continue;
-              issue_s(t, q_s + t * q_bytes, kv_it);
+              issue_s(t, q_s + t * C::kTileBytes, kv_it);
               if (cnt[t] == 1) mma_commit_w(&B.q_empty[t]);
             }
-            mma_commit_w(&B.k_empty[kv_it % C::kStages]);
+            mma_commit_w(&B.k_empty[kv_it % C::kKSlots]);
           }
           for (int i = 0; i < nt && ok; ++i) {
             bool v_ready = false, k_ready = false;
@@ -494,15 +544,15 @@ __global__ void __launch_bounds__(384, 1)
               if (i + 1 < cnt[t]) {
                 if (!k_ready && !(ok = wait_k(kv_it + i + 1))) break;
                 k_ready = true;
-                issue_s(t, q_s + t * q_bytes, kv_it + i + 1);
+                issue_s(t, q_s + t * C::kTileBytes, kv_it + i + 1);
                 if (i + 2 == cnt[t]) mma_commit_w(&B.q_empty[t]);  // the last S of this tile
               } else {
                 mma_commit_w(&B.o_full[t]);
               }
             }
             if (ok) {
-              mma_commit_w(&B.v_empty[(kv_it + i) % C::kStages]);
-              if (i + 1 < nt) mma_commit_w(&B.k_empty[(kv_it + i + 1) % C::kStages]);
+              mma_commit_w(&B.v_empty[(kv_it + i) % C::kVSlots]);
+              if (i + 1 < nt) mma_commit_w(&B.k_empty[(kv_it + i + 1) % C::kKSlots]);
             }
           }
         }
@@ -517,15 +567,15 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------- rows behind a sequence's end --
       // Follows every V tile (a parity wait must not run ahead of the ring, nor
       // the ring ahead of it: a slot is released by this warp as well).
-      Walk w = walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut);
+      Walk w = start();
       Segment g;
       uint32_t kv_it = 0;
       bool ok = true;
       while (ok && walk_get(work, w, ut, g)) {
         const int last = last_tile(w.q.kv), used = w.q.kv - (last << 7);
         for (int j = g.j0; j < g.j1; ++j, ++kv_it) {
-          const int st = kv_it % C::kStages;
-          if (!(ok = mbar_wait_warp(&B.v_full[st], (kv_it / C::kStages) & 1, status))) break;
+          const int st = kv_it % C::kVSlots;
+          if (!(ok = mbar_wait_warp(&B.v_full[st], (kv_it / C::kVSlots) & 1, status))) break;
           if (j == last && used < kTileRows) {
             for (int kb = 0; kb < C::kBlocks; ++kb) {
               uint4* rows = reinterpret_cast<uint4*>(sm + C::kOffV + st * C::kTileBytes + kb * kSwzBlockBytes);
@@ -548,110 +598,132 @@ __global__ void __launch_bounds__(384, 1)
     // -------------------------------------------------------------- softmax --
     const int t = warp / 4, quarter = warp % 4;
     const int r = quarter * 32 + lane;  // row of the tile
-    const int rtok = r / p.G;           // its token in the tile
-    const int rhead = r - rtok * p.G;
     const uint32_t t_s = tmem_lane_col(tbase, quarter * 32, C::kColS + 128 * t);
     const uint32_t t_o = tmem_lane_col(tbase, quarter * 32, C::kColO + 128 * t);
-    float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
-    uint32_t scnt = 0, ocnt = 0, merges = 0;
+    uint32_t scnt = 0, ocnt = 0, turn = 0;
+    uint32_t x_uses[2] = {0, 0};  // one-tile units that took each query buffer
+    uint32_t fills = 0, nexts = 0;
+    bool guard = false;  // the other half may still read this half's O of the last (one-tile) unit
     bool ok = true;
     int tail_row0 = 0, tail_tok = 0, tail_hk = 0, has_tail = 0, has_head = 0;  // for the header
-    Walk w = walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut);
+    float m_run = -INFINITY, l_run = 0.f;  // running maximum (log2 units) and sum of this row, in this warp's columns
+    // One key tile: NC columns from c0 on.  `cut`: column c is seen iff c <= cut (128: no mask).
+    auto tile = [&](auto nc, int c0, bool first, bool mask, int cut) {
+      constexpr int NC = decltype(nc)::value;
+      uint32_t sv[NC];
+#pragma unroll
+      for (int c = 0; c < NC / 32; ++c) tmem_ld32(t_s + c0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
+      tmem_wait_ld();
+      float* s = reinterpret_cast<float*>(sv);
+      if (mask) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) s[c] = (c > cut) ? -INFINITY : s[c];
+      }
+      float pm[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pm[e] = max3f(s[2 * e], s[2 * e + 1], -INFINITY);
+#pragma unroll
+      for (int c = 16; c < NC; c += 2) pm[(c / 2) & 7] = max3f(pm[(c / 2) & 7], s[c], s[c + 1]);
+      const float mx2 = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * c2;
+      if (first) {
+        m_run = mx2;
+      } else {
+        const bool need = mx2 > m_run + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need)) {
+          // O_t is quiescent: this S was committed after P V of this half's last tile
+          const float m_new = fmaxf(m_run, mx2);
+          const float alpha = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
+          l_run *= alpha;
+          m_run = m_new;
+          const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(t_o + 16 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float lo, hi;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), a2), lo, hi);
+              v[2 * k] = __float_as_uint(lo);
+              v[2 * k + 1] = __float_as_uint(hi);
+            }
+            tmem_st16(t_o + 16 * c, v);
+          }
+        }
+      }
+      // P = 2^(s c2 - m) (0 where masked: a row that has seen no key has m = -inf and
+      // every score -inf), summed in fp32 before its rounding to bf16 for P V
+      const float mref = (m_run == -INFINITY) ? 0.f : m_run;
+      const uint64_t c2x2 = f2_pack(c2, c2), negm = f2_pack(-mref, -mref);
+      uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < NC / 32; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int c = 32 * h + 2 * k;
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2x2, negm), x0, x1);
+          const uint64_t e2 = f2_pack(ex2(x0), ex2(x1));
+          ls[k & 3] = f2_add(ls[k & 3], e2);
+          float p0, p1;
+          f2_unpack(e2, p0, p1);
+          pk[k] = pack_bf16x2(p0, p1);
+        }
+        tmem_st16(t_s + c0 / 2 + 16 * h, pk);
+      }
+      if constexpr (NC == 32) {  // this copy of the rows takes no other columns
+        const uint32_t zero[16] = {};
+#pragma unroll
+        for (int h = 1; h < 4; ++h) tmem_st16(t_s + ((c0 / 2 + 16 * h) & 63), zero);
+      }
+      float a0, a1;
+      f2_unpack(f2_add(f2_add(ls[0], ls[1]), f2_add(ls[2], ls[3])), a0, a1);
+      l_run += a0 + a1;
+      tmem_wait_st();
+      tc_fence_before();
+    };
+    Walk w = start();
     Segment g;
     while (ok && walk_get(work, w, ut, g)) {
-      const bool one = one_tile(g);
+      const Form form = form_of(g);
+      const bool two = form == kTwoTiles, four = form == kFourCopies;
       const int nt = g.j1 - g.j0;
-      const int tok = g.tok0 + (one ? 0 : t * tt) + rtok;         // in the sequence
-      const int tile_rows = min(tt, g.ntok - (one ? 0 : t * tt)) * p.G;
-      const bool valid = r < tile_rows;
-      const bool busy = quarter * 32 < tile_rows;                 // any row of this warp
-      const int cnt = one ? (nt + 1 - t) / 2 : t ? nt : tile0_count(w.q, g, tt, p.causal);
-      const int jfirst = g.j0 + (one ? t : 0), jstep = one ? 2 : 1;
+      const int row = four ? lane : r;              // among the query tile's rows
+      const int rtok = row / p.G, rhead = row - rtok * p.G;
+      const int tile0 = two ? t * tt : 0;           // the query tile's first token in the unit
+      const int tok = g.tok0 + tile0 + rtok;        // in the sequence
+      const int tile_rows = min(tt, g.ntok - tile0) * p.G;
+      const bool valid = row < tile_rows;
+      const bool busy = four || quarter * 32 < tile_rows;  // any row of this warp
+      const int cnt = two ? (t ? nt : tile0_count(w.q, g, tt, p.causal)) : (nt + 1 - t) / 2;
+      const int jfirst = g.j0 + (two ? 0 : t), jstep = two ? 1 : 2;
       const int past = w.q.kv - w.q.qn;
       const int lim = !valid ? -1 : p.causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
-      // the first row's: up to it no tile needs a mask
-      const int lim0 = p.causal ? min(past + tok - rtok, w.q.kv - 1) : w.q.kv - 1;
-      float m_run = -INFINITY, l_run = 0.f;  // log2 units
+      // the tile's first row's: up to it no key tile needs a mask
+      const int lim0 = p.causal ? min(past + g.tok0 + tile0, w.q.kv - 1) : w.q.kv - 1;
+      m_run = -INFINITY;
+      l_run = 0.f;
       for (int i = 0; i < cnt; ++i) {
         if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
         ++scnt;
-        if (busy) {
+        const int kbase = (jfirst + i * jstep) * kTileRows;
+        const bool mask = kbase + kTileRows - 1 > lim0;
+        if (four) {
           tc_fence_after();
-          uint32_t sv[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
-          tmem_wait_ld();
-          float* s = reinterpret_cast<float*>(sv);
-          const int kbase = (jfirst + i * jstep) * kTileRows;
-          if (kbase + kTileRows - 1 > lim0) {
-            const int cut = lim - kbase;  // key kbase + c is seen iff c <= cut
-#pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = (c > cut) ? -INFINITY : s[c];
+          tile(std::integral_constant<int, 32>{}, 32 * quarter, i == 0, mask, lim - kbase - 32 * quarter);
+        } else if constexpr (!SHORT) {
+          if (busy) {
+            tc_fence_after();
+            tile(std::integral_constant<int, 128>{}, 0, i == 0, mask, lim - kbase);
           }
-          float pm[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pm[e] = max3f(s[2 * e], s[2 * e + 1], -INFINITY);
-#pragma unroll
-          for (int c = 16; c < 128; c += 2) pm[(c / 2) & 7] = max3f(pm[(c / 2) & 7], s[c], s[c + 1]);
-          const float mx2 =
-              max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * c2;
-          if (i == 0) {
-            m_run = mx2;
-          } else {
-            const bool need = mx2 > m_run + kRescaleThreshold;
-            if (__any_sync(0xffffffffu, need)) {
-              // O_t is quiescent: S_t(i) was committed after P V of this half's last tile
-              const float m_new = fmaxf(m_run, mx2);
-              const float alpha = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
-              l_run *= alpha;
-              m_run = m_new;
-              const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t v[16];
-                tmem_ld16(t_o + 16 * c, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  float lo, hi;
-                  f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), a2), lo, hi);
-                  v[2 * k] = __float_as_uint(lo);
-                  v[2 * k + 1] = __float_as_uint(hi);
-                }
-                tmem_st16(t_o + 16 * c, v);
-              }
-            }
-          }
-          // P = 2^(s c2 - m) (0 where masked: a row that has seen no key has m = -inf and
-          // every score -inf), summed in fp32 before its rounding to bf16 for P V
-          const float mref = (m_run == -INFINITY) ? 0.f : m_run;
-          const uint64_t c2x2 = f2_pack(c2, c2), negm = f2_pack(-mref, -mref);
-          uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int c = 32 * h + 2 * k;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), c2x2, negm), x0, x1);
-              const uint64_t e2 = f2_pack(ex2(x0), ex2(x1));
-              ls[k & 3] = f2_add(ls[k & 3], e2);
-              float p0, p1;
-              f2_unpack(e2, p0, p1);
-              pk[k] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16(t_s + 16 * h, pk);
-          }
-          float a0, a1;
-          f2_unpack(f2_add(f2_add(ls[0], ls[1]), f2_add(ls[2], ls[3])), a0, a1);
-          l_run += a0 + a1;
-          tmem_wait_st();
-          tc_fence_before();
         }
-        if (i == 0 && merges > 0) {
-          // both halves must have read the last merged unit's O before P V overwrites it
-          if (!(ok = mbar_wait_warp(B.ml_empty, (merges - 1) & 1, status))) break;
+        if (!SHORT && guard) {
+          // both halves must have read that O before P V overwrites it
+          const int b = ~turn & 1;  // that unit's buffer: the one in front of the next
+          if (!(ok = mbar_wait_warp(&B.x_done[b], ((b ? x_uses[1] : x_uses[0]) - 1) & 1, status))) break;
+          guard = false;
         }
         mbar_arrive(&B.p_full[t]);
       }
@@ -661,83 +733,171 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      // One-tile unit of two or more tiles: both halves' (m, l), then each half
-      // writes one half of the columns from both outputs.
-      const bool merge = one && nt > 1;
-      float w0 = 1.f, w1 = 0.f, m_out = m_run, l_out = l_run;  // weights of this half's and the other's output
-      if (merge) {
-        ml[t * 128 + r] = make_float2(m_run, l_run);
-        mbar_arrive(B.ml_full);
-        if (!(ok = mbar_wait_warp(B.ml_full, merges & 1, status))) break;
-        ++merges;
-        const float2 other = ml[(1 - t) * 128 + r];
-        m_out = fmaxf(m_run, other.x);
-        w0 = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_out);
-        w1 = (other.x == -INFINITY) ? 0.f : ex2(other.x - m_out);
-        l_out = l_run * w0 + other.y * w1;
-      }
       const bool whole = g.j0 == 0 && g.j1 == g.n;
-      const bool writes = one && !merge ? t == 0 : true;  // (a single key tile: half 0 alone)
-      if (writes && busy) {
-        const bool empty = l_out == 0.f;  // saw no key: zero, whatever O holds
-        const float scale_o = whole ? (empty ? 0.f : 1.f / l_out) : 1.f;
-        w0 *= scale_o;
-        w1 *= scale_o;
-        const size_t row = (size_t)(w.q.q0 + tok) * (p.Hk * p.G) + w.hk * p.G + rhead;
-        const int slot = g.j0 > 0 ? 0 : 1;
-        const int prow = (one ? 0 : t * 128) + r;
-        const size_t part = ((size_t)blockIdx.x * 2 + slot) * kPagedRows + prow;
-        const int c_lo = merge ? t * (D / 2) : 0, c_hi = merge ? c_lo + D / 2 : D;
-        const uint32_t t_o1 = tmem_lane_col(tbase, quarter * 32, C::kColO + 128 * (1 - t));
-        const bool has_o = cnt > 0;
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += 16) {
-          uint32_t v[16];
-          float x[16];
-          if (has_o) {
-            tmem_ld16(t_o + c, v);
-            if (merge) {
-              uint32_t u[16];
-              tmem_ld16(t_o1 + c, u);
-              tmem_wait_ld();
+      const size_t out_row = (size_t)(w.q.q0 + tok) * (p.Hk * p.G) + w.hk * p.G + rhead;
+      const size_t slot = ((size_t)blockIdx.x * 2 + (g.j0 > 0 ? 0 : 1)) * kPagedRows;
+      if (four) {
+        // Up to eight partial rows (four if there was one key tile) for each query row: eight
+        // query rows at a time, every warp writes its unnormalised outputs to the dead query
+        // buffer (16-byte chunk c of row rr at c ^ rr) with their (m, l); a thread adds up one
+        // chunk of one row.
+        const int b = turn & 1;
+        ++turn;
+        float4* xs = reinterpret_cast<float4*>(sm + C::kOffQ + b * C::kTileBytes);
+        float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl) + 64 * b;
+        const int parts = nt > 1 ? 8 : 4;
+        constexpr int kChunks = D / 4;
+        for (int r0 = 0; r0 < tile_rows; r0 += 8) {
+          if (cnt > 0) {
+            const bool mine = lane >= r0 && lane < r0 + 8 && valid;
+            const int rr = lane & 7;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                // a half that saw no key has weight 0 and an O of zeros times V
-                const float a = w0 == 0.f ? 0.f : w0 * __uint_as_float(v[k]);
-                x[k] = w1 == 0.f ? a : fmaf(w1, __uint_as_float(u[k]), a);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(t_o + 32 * c, v);
+              tmem_wait_ld();
+              if (mine) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  xs[(warp * 8 + rr) * kChunks + ((8 * c + k) ^ rr)] =
+                      make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                  __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+              }
+            }
+            if (mine) ml[warp * 8 + rr] = make_float2(m_run, l_run);
+          }
+          mbar_arrive(B.x_full);
+          if (!(ok = mbar_wait_warp(B.x_full, fills & 1, status))) break;
+          ++fills;
+          guard = false;  // everyone is past the last unit
+          const int rr = threadIdx.x / kChunks, c = threadIdx.x % kChunks, q_row = r0 + rr;
+          if (rr < 8 && q_row < tile_rows) {
+            float m = -INFINITY;
+            float2 part[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              part[i] = i < parts ? ml[i * 8 + rr] : make_float2(-INFINITY, 0.f);
+              m = fmaxf(m, part[i].x);
+            }
+            float l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (part[i].x == -INFINITY) continue;  // saw no key
+              const float wt = ex2(part[i].x - m);
+              const float4 x = xs[(i * 8 + rr) * kChunks + (c ^ rr)];
+              l = fmaf(wt, part[i].y, l);
+              o.x = fmaf(wt, x.x, o.x), o.y = fmaf(wt, x.y, o.y), o.z = fmaf(wt, x.z, o.z), o.w = fmaf(wt, x.w, o.w);
+            }
+            if (whole) {
+              const int qt = q_row / p.G;
+              const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.hk * p.G + (q_row - qt * p.G);
+              const float inv = l == 0.f ? 0.f : 1.f / l;
+              reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D)[c] =
+                  make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+              if (c == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+            } else {
+              reinterpret_cast<float4*>(p.part_o + (slot + q_row) * D)[c] = o;
+              if (c == 0) reinterpret_cast<float2*>(p.part_ml)[slot + q_row] = make_float2(m, l);
+            }
+          }
+          if (r0 + 8 < tile_rows) {
+            mbar_arrive(B.x_next);
+            if (!(ok = mbar_wait_warp(B.x_next, nexts & 1, status))) break;
+            ++nexts;
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();  // the next copy into the buffer comes behind these accesses
+        mbar_arrive(&B.x_done[b]);
+        if (b)
+          ++x_uses[1];
+        else
+          ++x_uses[0];
+      } else if constexpr (!SHORT) {
+        // One-tile unit of two or more key tiles: both halves' (m, l) through the dead query
+        // buffer, then each half writes half of the columns from both outputs.
+        const bool merge = !two && nt > 1;
+        float w0 = 1.f, w1 = 0.f, m_out = m_run, l_out = l_run;  // weights of this half's and the other's output
+        const int b = turn & 1;
+        if (merge) {
+          float2* ml = reinterpret_cast<float2*>(sm + C::kOffQ + b * C::kTileBytes);
+          ml[t * 128 + r] = make_float2(m_run, l_run);
+          mbar_arrive(B.x_full);
+          if (!(ok = mbar_wait_warp(B.x_full, fills & 1, status))) break;
+          ++fills;
+          const float2 other = ml[(1 - t) * 128 + r];
+          m_out = fmaxf(m_run, other.x);
+          w0 = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_out);
+          w1 = (other.x == -INFINITY) ? 0.f : ex2(other.x - m_out);
+          l_out = l_run * w0 + other.y * w1;
+        }
+        if (busy && (two || merge || t == 0)) {  // (a single key tile: half 0 alone)
+          const bool empty = l_out == 0.f;       // saw no key: zero, whatever O holds
+          const float scale_o = whole ? (empty ? 0.f : 1.f / l_out) : 1.f;
+          w0 *= scale_o;
+          w1 *= scale_o;
+          const size_t part = slot + (two ? t * 128 : 0) + r;
+          const int c_lo = merge ? t * (D / 2) : 0, c_hi = merge ? c_lo + D / 2 : D;
+          const uint32_t t_o1 = tmem_lane_col(tbase, quarter * 32, C::kColO + 128 * (1 - t));
+#pragma unroll 1
+          for (int c = c_lo; c < c_hi; c += 16) {
+            float x[16];
+            if (cnt > 0) {
+              uint32_t v[16];
+              tmem_ld16(t_o + c, v);
+              if (merge) {
+                uint32_t u[16];
+                tmem_ld16(t_o1 + c, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  // a half that saw no key has weight 0 and an O of zeros times V
+                  const float a = w0 == 0.f ? 0.f : w0 * __uint_as_float(v[k]);
+                  x[k] = w1 == 0.f ? a : fmaf(w1, __uint_as_float(u[k]), a);
+                }
+              } else {
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = empty ? 0.f : w0 * __uint_as_float(v[k]);
               }
             } else {
-              tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = empty ? 0.f : w0 * __uint_as_float(v[k]);
+              for (int k = 0; k < 16; ++k) x[k] = 0.f;
             }
-          } else {
+            if (!valid) continue;
+            uint32_t y[8];
+            if (whole) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
+              for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+              store32(static_cast<__nv_bfloat16*>(p.o) + out_row * D + c, y);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(x[8 * h + k]);
+                store32(p.part_o + part * D + c + 8 * h, y);
+              }
+            }
           }
-          if (!valid) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D + c);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              dst[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]), pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
-                                  pack_bf16x2(x[8 * k + 4], x[8 * k + 5]), pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          if (valid && (!merge || t == 0)) {
+            if (!whole)
+              reinterpret_cast<float2*>(p.part_ml)[part] = make_float2(m_out, l_out);
+            else if (p.lse)
+              p.lse[out_row] = empty ? -INFINITY : (m_out + __log2f(l_out)) * kLn2;
           }
         }
-        if (valid && (!merge || t == 0)) {
-          if (!whole)
-            reinterpret_cast<float2*>(p.part_ml)[part] = make_float2(m_out, l_out);
-          else if (p.lse)
-            p.lse[row] = empty ? -INFINITY : (m_out + __log2f(l_out)) * kLn2;
+        if (!two) {
+          ++turn;
+          tc_fence_before();
+          fence_proxy_async_smem();
+          mbar_arrive(&B.x_done[b]);
+          if (b)
+            ++x_uses[1];
+          else
+            ++x_uses[0];
+          guard = true;
         }
-      }
-      if (merge) {
-        tc_fence_before();
-        mbar_arrive(B.ml_empty);
       }
       if (g.j0 > 0) {
         has_head = g.j1 == g.n ? 2 : 1;
@@ -834,10 +994,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, i
   }
 }
 
-template <int D, bool WIDE>
+template <int D, bool SHORT>
 cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
-  using C = PagedCfg<D, WIDE>;
-  auto kern = paged_kernel<D, WIDE>;
+  using C = PagedCfg<D>;
+  auto kern = paged_kernel<D, SHORT>;
   // The register split inside the kernel assumes it was built with exactly
   // kLaunchRegs registers a thread: refuse to launch any other build.
   static const bool regs_ok = [&] {
@@ -847,10 +1007,10 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   if (!regs_ok) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_k, a.tm_v, a.p);
+  kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid, WIDE ? 8 : 4);
+  cfg.gridDim = dim3(a.grid, SHORT ? 4 : 16);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -864,8 +1024,8 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged(const PagedLaunch& a, cudaStream_t stream) {
-  if (a.d == 64) return a.wide ? launch_paged_t<64, true>(a, stream) : launch_paged_t<64, false>(a, stream);
-  return a.wide ? launch_paged_t<128, true>(a, stream) : launch_paged_t<128, false>(a, stream);
+  if (a.d == 64) return a.is_short ? launch_paged_t<64, true>(a, stream) : launch_paged_t<64, false>(a, stream);
+  return a.is_short ? launch_paged_t<128, true>(a, stream) : launch_paged_t<128, false>(a, stream);
 }
 
 }  // namespace fa

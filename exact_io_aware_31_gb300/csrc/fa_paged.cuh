@@ -19,7 +19,7 @@ struct PagedParams {
   int causal;
   float c2;               // scale * log2(e)
   int tile_tokens;        // tokens of a 128-row query tile: G * tile_tokens <= 128
-  int q_bufs;             // query buffers of the one-tile kernel (1, or 2 of up to 64 rows)
+  int copy_tokens;        // tokens whose rows fit a quarter of it (0: none)
   int* hdr;               // [grid][kPagedHdr]
   float* part_ml;         // [grid][2][rows][2]: running maximum (log2 units), sum
   float* part_o;          // [grid][2][rows][d]: unnormalised output
@@ -32,12 +32,13 @@ constexpr int kPagedHdr = 8;
 constexpr int kPagedRows = 256;
 
 struct PagedLaunch {
-  CUtensorMap tm_q;  // [T, Hk, G, d]: boxes of 64 columns x G x 1 x tile_tokens
+  CUtensorMap tm_q;   // [T, Hk, G, d]: boxes of 64 columns x G x 1 x tile_tokens
+  CUtensorMap tm_q4;  // ... x copy_tokens
   CUtensorMap tm_k;  // [pages, Hk, page_size, d]: boxes of 64 columns x min(page_size, 128) rows
   CUtensorMap tm_v;
   PagedParams p;
   int d;
-  int wide;  // units of two query tiles
+  int is_short;  // units of copy_tokens only
   int grid;
 };
 

@@ -313,17 +313,12 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   PagedLaunch a = {};
   a.d = d;
   a.grid = dev.sms;
-  // Rows a sequence brings to one key head: over a tile of 128, the two-tile
-  // kernel.  Where they fit 64, the tiles hold no more than 64 rows and two of
-  // them fit the one-tile kernel's query buffer (the next unit's is loaded
-  // while this one runs).
-  const long long rows = (long long)(max_q > 0 ? max_q : T) * G;
-  const int tokens = 128 / G;
-  a.wide = rows > tokens * G;
-  const bool two = !a.wide && G <= 64 && rows <= 64 / G * G;
   PagedParams& p = a.p;
-  p.tile_tokens = two ? 64 / G : tokens;
-  p.q_bufs = two ? 2 : 1;
+  p.tile_tokens = 128 / G;
+  p.copy_tokens = 32 / G;
+  // Chunks whose rows for one key head fit a quarter of a tile take the kernel
+  // that has no other form.
+  a.is_short = max_q > 0 && max_q <= p.copy_tokens;
   p.o = o;
   p.lse = lse;
   p.page_table = page_table;
@@ -345,6 +340,7 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.status = dev.status;
   if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||
+      make_ragged_map(&a.tm_q4, q, T, Hk, G, d, p.copy_tokens > 0 ? p.copy_tokens : 1, q_stride_t, q_stride_h) ||
       make_pool_map(&a.tm_k, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0]) ||
       make_pool_map(&a.tm_v, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1]))
     return FA_ERR_CUDA;

@@ -13,9 +13,8 @@
 // for all of them.
 //
 // Work: a unit is one key head's block of one or two 128-row query tiles and all
-// key tiles (128 keys) it sees.  The key tiles of all units, one unit after the
-// other, are cut into equal runs, one per CTA, whatever mix of lengths a step
-// brings; lengths are read on the device, so the host knows none of them and one
+// key tiles (128 keys) it sees.  The units, one after the other, are cut into
+// runs of equal cost, one per CTA, whatever mix of lengths a step brings; lengths are read on the device, so the host knows none of them and one
 // captured graph serves every step.  A cut that falls near a unit's border moves
 // there.  A unit that is cut leaves unnormalised partial outputs (fp32) with
 // their maxima and sums in the workspace, at most two a CTA, and a second kernel
@@ -94,10 +93,9 @@ struct PagedCfg {
 struct Work {
   const int* cu;
   const int* lens;
-  int S, Hk, T, cap, causal;
+  int S, Hk, T, cap;
   __device__ __forceinline__ explicit Work(const PagedParams& p)
-      : cu(p.cu_seqlens), lens(p.kv_lens), S(p.S), Hk(p.Hk), T(p.T), cap(p.max_pages << p.page_log2),
-        causal(p.causal) {}
+      : cu(p.cu_seqlens), lens(p.kv_lens), S(p.S), Hk(p.Hk), T(p.T), cap(p.max_pages << p.page_log2) {}
   __device__ __forceinline__ Seq seq(int s, bool& bad) const {
     return make_seq(__ldg(cu + s), __ldg(cu + s + 1), __ldg(lens + s), T, cap, bad);
   }
@@ -109,13 +107,19 @@ struct Work {
 
 // The CTA's run in shared memory.
 struct Plan {
-  long long x[2];   // its borders in the row of all key tiles
-  int s, hk, b, j;  // where the first one lies
-  int status;
-  int pad;
-  long long scan[16];
+  Spot at[2];      // its borders
+  Seq q[2];        // the sequences they lie in
+  long long y[2];  // while it is made: places in the cost of their key heads
+  long long scan[12];
 };
 static_assert(sizeof(Plan) <= 192, "plan size");
+
+// n / d for positive n: 32 bits where they do (a 64-bit division is a long
+// stretch of code in front of a CTA's first copy).
+__device__ __forceinline__ long long div_long(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return (unsigned)n / (unsigned)d;
+  return n / d;
+}
 
 // Sum over the block of one value a thread: the exclusive prefix, and the total.
 template <int THREADS>
@@ -143,34 +147,30 @@ __device__ long long block_scan(long long v, long long* warps, long long* total)
 
 // Every thread of the CTA.  Fills *plan: the run of this CTA.  The borders are
 // computed alike by the CTAs on both sides of them.
-template <int THREADS>
-__device__ void make_plan(const PagedParams& p, int ut, Plan* plan) {
+template <int D, int THREADS>
+__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
   const Work work(p);
   const int tid = threadIdx.x;
   bool bad = false;
   Seq q = {0, 0, 0};
   long long per_head = 0, before = 0, total = 0;
   const int chunks = (p.S + THREADS - 1) / THREADS;
+  if (tid < 2) plan->at[tid] = {p.S, 0, 0, 0};  // a border at the end
   for (int c = 0; c < chunks; ++c) {
     const int s = c * THREADS + tid;
     per_head = 0;
     if (s < p.S) {
       q = work.seq(s, bad);
-      per_head = seq_tiles(q, ut, p.causal);
+      per_head = cost_of_seq<D>(q, sh);
     }
     long long part;
     before = total + block_scan<THREADS>(per_head * p.Hk, plan->scan, &part);
     total += part;
   }
   if (bad) atomicExch(p.status, FA_ERR_DEVICE_INDEX);
-  const int ctas = (int)(total < gridDim.x ? total : gridDim.x);  // at least one tile a CTA
-  const long long tol = snap_tolerance(total, ctas);
-  if (tid == 0) {
-    plan->x[0] = plan->x[1] = total;
-    plan->s = p.S;
-    plan->hk = plan->b = plan->j = 0;
-  }
-  __syncthreads();
+  // The sequences that the borders lie in.
+  const int ctas = ctas_for<D>(total, gridDim.x);
+  const long long share = ctas > 0 ? div_long(total, ctas) : 0;
   long long run = 0;
   for (int c = 0; c < chunks; ++c) {
     if (chunks > 1) {  // (with one chunk the values of the first pass are still here)
@@ -178,25 +178,33 @@ __device__ void make_plan(const PagedParams& p, int ut, Plan* plan) {
       per_head = 0;
       if (s < p.S) {
         q = work.seq(s);
-        per_head = seq_tiles(q, ut, p.causal);
+        per_head = cost_of_seq<D>(q, sh);
       }
       long long part;
       before = run + block_scan<THREADS>(per_head * p.Hk, plan->scan, &part);
       run += part;
     }
-#pragma unroll 1
+#pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if ((int)blockIdx.x + e > ctas) continue;
-      const long long x = border(total, blockIdx.x + e, ctas);
-      // the sequence it lies in (none for x == total: as set above)
-      if (x < before || x >= before + per_head * p.Hk) continue;
-      int hk, b, j;
-      plan->x[e] = x + place(q, x - before, per_head, ut, p.causal, tol, hk, b, j);
-      if (e == 0) {
-        plan->s = c * THREADS + tid;
-        plan->hk = hk;
-        plan->b = b;
-        plan->j = j;
+      const long long x = border(total, share, blockIdx.x + e, ctas);
+      if ((int)blockIdx.x + e > ctas || x < before || x >= before + per_head * p.Hk) continue;
+      const int hk = (int)div_long(x - before, per_head);
+      plan->at[e] = {c * THREADS + tid, hk, 0, 0};
+      plan->y[e] = x - before - hk * per_head;
+      plan->q[e] = q;
+    }
+  }
+  __syncthreads();
+  // Their blocks: every thread tries some.
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (plan->at[e].s >= p.S) continue;
+    const Seq sq = plan->q[e];
+    for (int b = tid; b * sh.ut < sq.qn; b += THREADS) {
+      int j;
+      if (place<D>(sq, plan->y[e], b, sh, j)) {
+        plan->at[e].b = b;
+        plan->at[e].j = j;
       }
     }
   }
@@ -220,9 +228,6 @@ struct PagedBars {
   uint64_t* mma_done;
 };
 
-// Which form a segment's unit takes.
-enum Form { kTwoTiles, kOneTile, kFourCopies };
-
 // 32 bytes of a row.
 __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -243,6 +248,9 @@ __global__ void __launch_bounds__(384, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if (!smem_base_ok(smem_raw, status)) return;
   uint8_t* sm = smem_raw;
+  // The merge kernel (a programmatic dependent) may start launching: its blocks
+  // take the room of CTAs that are done, and wait for this grid's results.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   PagedBars B;
@@ -266,30 +274,17 @@ __global__ void __launch_bounds__(384, 1)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tt = p.tile_tokens, t4 = p.copy_tokens;
-  const int ut = SHORT ? t4 : 2 * tt;  // tokens a unit
+  const Shape sh = {SHORT ? t4 : 2 * tt, tt, t4, p.causal};
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.q_full[i], 1);
-      mbar_init(&B.q_empty[i], 1);
-      mbar_init(&B.x_done[i], 256);
-      mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_full[i], 128);
-      mbar_init(&B.o_full[i], 1);
+  if (warp == 0) {
+    for (int i = lane; i < C::kNumBars; i += 32) {
+      uint64_t* bar = bars + i;
+      const bool merge = bar == B.x_full || bar == B.x_next || bar == B.x_done || bar == B.x_done + 1;
+      const bool p_full = bar == B.p_full || bar == B.p_full + 1;
+      const bool v_empty = bar >= B.v_empty && bar < B.v_empty + C::kVSlots;  // the MMA issuer and warp 10
+      mbar_init(bar, merge ? 256 : p_full ? 128 : v_empty ? 2 : 1);
     }
-    for (int st = 0; st < C::kKSlots; ++st) {
-      mbar_init(&B.k_full[st], 1);
-      mbar_init(&B.k_empty[st], 1);
-    }
-    for (int st = 0; st < C::kVSlots; ++st) {
-      mbar_init(&B.v_full[st], 1);
-      mbar_init(&B.v_empty[st], 2);  // the MMA issuer and warp 10
-      mbar_init(&B.v_clear[st], 1);
-    }
-    mbar_init(B.x_full, 256);
-    mbar_init(B.x_next, 256);
-    mbar_init(B.mma_done, 1);
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -302,16 +297,14 @@ __global__ void __launch_bounds__(384, 1)
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
   }
-  make_plan<C::kThreads>(p, ut, plan);
+  make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   const Work work(p);
-  auto form_of = [&](const Segment& g) {
-    return SHORT || g.ntok <= t4 ? kFourCopies : g.ntok <= tt ? kOneTile : kTwoTiles;
-  };
-  auto start = [&] { return walk_start(work, plan->x[1] - plan->x[0], plan->s, plan->hk, plan->b, plan->j, ut); };
+  auto form_of = [&](const Segment& g) { return SHORT ? kFourCopies : sh.form(g.ntok); };
+  auto start = [&] { return walk_start(work, plan->at[0], plan->at[1], plan->q[0], sh); };
 
   if (warp >= 8) {
     regs_dec<C::kAuxRegs>();
@@ -333,9 +326,9 @@ __global__ void __launch_bounds__(384, 1)
         if (merged[b]) return mbar_wait_warp(&B.x_done[b], (by_merge[b] - 1) & 1, status);
         return by_mma[b] == 0 || mbar_wait_warp(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
       };
-      while (ok && walk_get(work, w, ut, g)) {
+      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
         const Form form = form_of(g);
-        const int* table = p.page_table + (size_t)w.s * p.max_pages;
+        const int* table = p.page_table + (size_t)w.at.s * p.max_pages;
         const int pages = (w.q.kv + (1 << p.page_log2) - 1) >> p.page_log2;
         // this lane's page of key tile j, asked for a tile ahead
         auto page_at = [&](int j) {
@@ -350,7 +343,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_expect_tx(&B.q_full[b], copies * box * C::kBlocks);
             for (int kb = 0; kb < C::kBlocks; ++kb)
               for (int c = 0; c < copies; ++c)
-                tma_load_4d(dst + kb * kSwzBlockBytes + c * (kSwzBlockBytes / 4), map, &B.q_full[b], 64 * kb, 0, w.hk,
+                tma_load_4d(dst + kb * kSwzBlockBytes + c * (kSwzBlockBytes / 4), map, &B.q_full[b], 64 * kb, 0, w.at.hk,
                             row);
           }
           __syncwarp();
@@ -358,7 +351,7 @@ __global__ void __launch_bounds__(384, 1)
         if (form == kTwoTiles) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok || (t == 0 && tile0_count(w.q, g, tt, p.causal) == 0)) continue;
+            if (!ok || (t == 0 && tile0_count(w.q, g, sh) == 0)) continue;
             if (!(ok = wait_q(t))) break;
             load_q(t, &tm_q, 1, tt * p.G * 128, q_row + t * tt);
             ++q_uses[t];
@@ -399,7 +392,7 @@ __global__ void __launch_bounds__(384, 1)
           if (lane < boxes) {
             uint8_t* dst = sm + C::kOffK + ks * C::kTileBytes + lane * box_bytes;
             for (int kb = 0; kb < C::kBlocks; ++kb)
-              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[ks], 64 * kb, row, w.hk, page);
+              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[ks], 64 * kb, row, w.at.hk, page);
           }
           __syncwarp();
           if (!(ok = mbar_wait_warp(&B.v_empty[vs], vph ^ 1, status))) {
@@ -412,12 +405,12 @@ __global__ void __launch_bounds__(384, 1)
           if (lane < boxes) {
             uint8_t* dst = sm + C::kOffV + vs * C::kTileBytes + lane * box_bytes;
             for (int kb = 0; kb < C::kBlocks; ++kb)
-              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_v, &B.v_full[vs], 64 * kb, row, w.hk, page);
+              tma_load_4d(dst + kb * kSwzBlockBytes, &tm_v, &B.v_full[vs], 64 * kb, row, w.at.hk, page);
           }
           __syncwarp();
         }
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, ut, g);
+        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
       if (lost) atomicExch(status, FA_ERR_DEVICE_INDEX);
@@ -459,7 +452,7 @@ __global__ void __launch_bounds__(384, 1)
                                 sdesc(v_s + (it % C::kVSlots) * C::kTileBytes, kSwzBlockBytes, 1024), kIdO,
                                 accumulate);
       };
-      while (ok && walk_get(work, w, ut, g)) {
+      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
         const Form form = form_of(g);
         const int nt = g.j1 - g.j0;
         const int last = last_tile(w.q.kv);
@@ -510,7 +503,7 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         } else if constexpr (!SHORT) {
-          const int cnt[2] = {tile0_count(w.q, g, tt, p.causal), nt};
+          const int cnt[2] = {tile0_count(w.q, g, sh), nt};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || cnt[t] == 0) continue;
@@ -558,7 +551,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         kv_it += nt;
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, ut, g);
+        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
       mma_commit_w(B.mma_done);
@@ -571,7 +564,7 @@ __global__ void __launch_bounds__(384, 1)
       Segment g;
       uint32_t kv_it = 0;
       bool ok = true;
-      while (ok && walk_get(work, w, ut, g)) {
+      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
         const int last = last_tile(w.q.kv), used = w.q.kv - (last << 7);
         for (int j = g.j0; j < g.j1; ++j, ++kv_it) {
           const int st = kv_it % C::kVSlots;
@@ -589,7 +582,7 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
         }
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, ut, g);
+        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
     }
@@ -686,7 +679,7 @@ __global__ void __launch_bounds__(384, 1)
     };
     Walk w = start();
     Segment g;
-    while (ok && walk_get(work, w, ut, g)) {
+    while (ok && walk_get(work, w, plan->at[1], sh, g)) {
       const Form form = form_of(g);
       const bool two = form == kTwoTiles, four = form == kFourCopies;
       const int nt = g.j1 - g.j0;
@@ -697,7 +690,7 @@ __global__ void __launch_bounds__(384, 1)
       const int tile_rows = min(tt, g.ntok - tile0) * p.G;
       const bool valid = row < tile_rows;
       const bool busy = four || quarter * 32 < tile_rows;  // any row of this warp
-      const int cnt = two ? (t ? nt : tile0_count(w.q, g, tt, p.causal)) : (nt + 1 - t) / 2;
+      const int cnt = two ? (t ? nt : tile0_count(w.q, g, sh)) : (nt + 1 - t) / 2;
       const int jfirst = g.j0 + (two ? 0 : t), jstep = two ? 1 : 2;
       const int past = w.q.kv - w.q.qn;
       const int lim = !valid ? -1 : p.causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
@@ -734,7 +727,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       tc_fence_after();
       const bool whole = g.j0 == 0 && g.j1 == g.n;
-      const size_t out_row = (size_t)(w.q.q0 + tok) * (p.Hk * p.G) + w.hk * p.G + rhead;
+      const size_t out_row = (size_t)(w.q.q0 + tok) * (p.Hk * p.G) + w.at.hk * p.G + rhead;
       const size_t slot = ((size_t)blockIdx.x * 2 + (g.j0 > 0 ? 0 : 1)) * kPagedRows;
       if (four) {
         // Up to eight partial rows (four if there was one key tile) for each query row: eight
@@ -791,7 +784,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (whole) {
               const int qt = q_row / p.G;
-              const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.hk * p.G + (q_row - qt * p.G);
+              const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.at.hk * p.G + (q_row - qt * p.G);
               const float inv = l == 0.f ? 0.f : 1.f / l;
               reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D)[c] =
                   make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -905,11 +898,11 @@ __global__ void __launch_bounds__(384, 1)
         has_tail = 1;
         tail_row0 = w.q.q0 + g.tok0;
         tail_tok = g.ntok;
-        tail_hk = w.hk;
+        tail_hk = w.at.hk;
       }
       tc_fence_before();
       if (aborted(abort_flag)) ok = false;
-      if (ok) walk_next(work, w, ut, g);
+      if (ok) walk_next(work, w, plan->at[1], sh, g);
     }
     if (!ok) *abort_flag = 1;
     if (threadIdx.x == 0) {
@@ -919,9 +912,6 @@ __global__ void __launch_bounds__(384, 1)
     }
   }
 
-  // The merge kernel (a programmatic dependent) may start launching; it waits
-  // for this grid's results before it reads them.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -933,64 +923,86 @@ __global__ void __launch_bounds__(384, 1)
 
 // Merges the units that were cut: block (c, y) takes rows of the unit that CTA
 // c began and did not end.  Its parts are CTA c's second slot and the first
-// slots of the CTAs behind it up to the one that ended it.  A warp a row.
+// slots of the CTAs behind it up to the one that ended it.  A warp a row; what
+// it reads does not wait for one another where that can be helped (the last
+// part's number, the maxima and the first outputs are asked for together: the
+// kernel is a chain of reads, 5 to 8 us long before).
 template <int D>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, int ctas) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kPer = D / 32, kAhead = 4;
   const int c = blockIdx.x;
   const int lane = threadIdx.x & 31;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  auto slot = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows; };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 h = *reinterpret_cast<const int4*>(p.hdr + (size_t)c * kPagedHdr);
+  int ends = c + 1 + lane < ctas ? p.hdr[(size_t)(c + 1 + lane) * kPagedHdr + 4] : 2;
   if (!h.x) return;
   // the first CTA behind c whose first slot ends its unit
   int last = ctas - 1;
-  for (int at = c + 1; at < ctas; at += 32) {
-    const bool ends = at + lane < ctas && p.hdr[(size_t)(at + lane) * kPagedHdr + 4] != 1;
-    const unsigned found = __ballot_sync(0xffffffffu, ends);
+  for (int at = c + 1;; at += 32) {
+    const unsigned found = __ballot_sync(0xffffffffu, ends != 1);
     if (found) {
-      last = at + __ffs(found) - 1;
+      last = min(last, at + __ffs(found) - 1);
       break;
     }
+    ends = at + 32 + lane < ctas ? p.hdr[(size_t)(at + 32 + lane) * kPagedHdr + 4] : 2;
   }
   const int parts = last - c + 1;
-  auto slot = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows; };
-  const int tt = p.tile_tokens, tile = tt * p.G;
+  const int tile = p.tile_tokens * p.G;
   const int rows = h.z * p.G;  // valid rows, densely numbered
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  constexpr int kPer = D / 32;
   for (int n = blockIdx.y * 8 + threadIdx.x / 32; n < rows; n += gridDim.y * 8) {
     const int prow = n < tile ? n : 128 + n - tile;
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[slot(i) + prow].x);
+    float v[kAhead][kPer];
+    auto load = [&](int i, float (&x)[kPer]) {
+      const float* src = p.part_o + (slot(i) + prow) * D + kPer * lane;
+      if constexpr (kPer == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        x[0] = f.x, x[1] = f.y;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < parts) load(i, v[i]);
+    float2 mine = lane < parts ? ml[slot(lane) + prow] : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
+    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, ml[slot(i) + prow].x);
 #pragma unroll
     for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float l = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float2 x = ml[slot(i) + prow];
-      const float w = x.x == -INFINITY ? 0.f : ex2(x.x - m);
-      l = fmaf(w, x.y, l);
-      const float* src = p.part_o + (slot(i) + prow) * D + kPer * lane;
-      if constexpr (kPer == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      if (i0 > 0) mine = i0 + lane < parts ? ml[slot(i0 + lane) + prow] : make_float2(-INFINITY, 0.f);
+      const float mw = mine.x == -INFINITY ? 0.f : ex2(mine.x - m);
+      const float ml2 = mw * mine.y;
+      for (int i = i0; i < parts && i < i0 + 32; i += kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float w = __shfl_sync(0xffffffffu, mw, (i - i0 + k) & 31);
+          l += __shfl_sync(0xffffffffu, ml2, (i - i0 + k) & 31);
+          if (i + k >= parts) continue;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (i + kAhead + k < parts) load(i + kAhead + k, v[k]);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int tok = n / p.G;
     const size_t row = (size_t)(h.y + tok) * (p.Hk * p.G) + h.w * p.G + (n - tok * p.G);
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D) + (kPer / 2) * lane;
-#pragma unroll
-    for (int e = 0; e < kPer / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+      *dst = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   }
 }
 

@@ -1,17 +1,43 @@
-// How the paged attention kernel divides its work: pure index arithmetic, for
+// How the paged attention kernels divide their work: pure index arithmetic, for
 // host and device.
 //
 // A unit is one key head's block of `ut` new tokens of one sequence, with every
 // key tile (128 keys) that the block sees; the units lie one after the other,
-// sequence by sequence, key head by key head, block by block, and the row of all
-// their key tiles is cut into equal runs, one per CTA.  A role of a CTA walks
-// its run as segments, each the part of one unit that lies in the run.
+// sequence by sequence, key head by key head, block by block.  Each has a cost,
+// and the row of all costs is cut into equal runs, one per CTA.  A role of a CTA
+// walks its run as segments, each the part of one unit that lies in the run.
 #pragma once
 
 #include "fa_common.cuh"
 
 namespace fa {
 namespace paged {
+
+// Which form a unit takes (fa_paged.cu).
+enum Form { kTwoTiles, kOneTile, kFourCopies };
+
+// The launch's division: tokens of a unit, of a query tile, of a quarter tile.
+struct Shape {
+  int ut, tt, t4;
+  int causal;
+  __host__ __device__ Form form(int tokens) const {
+    return tokens <= t4 ? kFourCopies : tokens <= tt ? kOneTile : kTwoTiles;
+  }
+};
+
+// Cost of a unit: `tile` for each key tile, `unit` for its beginning and end.
+// From traces on GB300, in steps of about 0.5 us (d = 128) and 0.4 us (d = 64): a
+// key tile against two query tiles takes 1.5 us, against one 1.1 (0.75 at
+// d = 64), against four copies of short rows 1.1 (0.4); a unit's first scores
+// and its output another 2 to 4 us.
+template <int D>
+__host__ __device__ inline int tile_cost(Form f) {
+  return D == 128 ? (f == kTwoTiles ? 3 : 2) : (f == kTwoTiles ? 4 : f == kOneTile ? 2 : 1);
+}
+template <int D>
+__host__ __device__ inline int unit_cost(Form f) {
+  return D == 128 ? (f == kTwoTiles ? 7 : 4) : (f == kTwoTiles ? 7 : 5);
+}
 
 struct Seq {
   int q0, qn, kv;  // first row, new tokens, keys
@@ -31,87 +57,89 @@ __host__ __device__ inline Seq make_seq(int begin, int end, int kv, int T, int c
   return q;
 }
 
-// sum of floor((a i + b) / m) over i < n, by the reduction of a and b modulo m
-// and the exchange of rows and columns of the lattice points under the line
-// (Euclid's steps).
-__host__ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
-    a %= m;
-    b %= m;
-    const unsigned long long top = (unsigned long long)a * n + b;
-    if (top < m) break;
-    n = (unsigned)(top / m);
-    b = (unsigned)(top % m);
-    const unsigned t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
+__host__ __device__ inline int blocks_of(const Seq& q, int ut) { return (q.qn + ut - 1) / ut; }
+
+// Keys that tokens [.., hi) of the sequence see.
+__host__ __device__ inline int keys_upto(const Seq& q, int hi, int causal) {
+  return imax(0, causal ? q.kv - q.qn + hi : q.kv);
 }
 
-// Key tiles that tokens [.., hi) of the sequence see, at least one (so that
-// rows that see no key are written as well).
-__host__ __device__ inline int tiles_upto(const Seq& q, int hi, int causal) {
-  const int vis = causal ? q.kv - q.qn + hi : q.kv;
-  return imax(1, (vis + kTileRows - 1) >> 7);
+// Key tiles of block b, at least one (so that rows that see no key are written as well).
+__host__ __device__ inline int unit_tiles(const Seq& q, int b, const Shape& sh) {
+  return imax(1, (keys_upto(q, imin(q.qn, (b + 1) * sh.ut), sh.causal) + kTileRows - 1) >> 7);
 }
 
-__host__ __device__ inline int unit_tiles(const Seq& q, int b, int ut, int causal) {
-  return tiles_upto(q, imin(q.qn, (b + 1) * ut), causal);
+// Cost of a unit that sees `keys` keys, in 128ths of the steps above: keys + 127
+// stand for its tiles, so that sums over blocks are arithmetic series.
+template <int D>
+__host__ __device__ inline long long cost_of(long long blocks, long long keys, Form f) {
+  return tile_cost<D>(f) * (keys + 127 * blocks) + 128 * unit_cost<D>(f) * blocks;
 }
 
-// Key tiles of blocks [0, b) of one key head, b < blocks of the sequence.
-__host__ __device__ inline long long tiles_before(const Seq& q, int b, int ut, int causal) {
-  if (!causal) return (long long)b * unit_tiles(q, 0, ut, 0);
-  const int c = q.kv - q.qn;  // block i sees c + (i + 1) ut keys
-  const int one = 128 - c < 0 ? 0 : imin(b, (128 - c) / ut);  // blocks with a single tile
-  return one + floor_sum(b - one, 128, ut, (unsigned)(c + (one + 1) * ut + 127) * (b > one));
+// Cost of blocks [0, b) of one key head, all of them full.
+template <int D>
+__host__ __device__ inline long long cost_before(const Seq& q, int b, const Shape& sh) {
+  const Form f = sh.form(sh.ut);
+  if (!sh.causal) return cost_of<D>(b, (long long)b * q.kv, f);
+  const int c = q.kv - q.qn;  // block i sees c + (i + 1) ut keys, or none
+  const int z = c >= 0 ? 0 : imin(b, -c / sh.ut);
+  const long long keys = (long long)(b - z) * c + (long long)sh.ut * ((long long)b * (b + 1) - (long long)z * (z + 1)) / 2;
+  return cost_of<D>(b, keys, f);
 }
 
-__host__ __device__ inline long long seq_tiles(const Seq& q, int ut, int causal) {  // of one key head
-  const int nb = (q.qn + ut - 1) / ut;
-  if (nb == 0) return 0;
-  return (nb > 1 ? tiles_before(q, nb - 1, ut, causal) : 0) + unit_tiles(q, nb - 1, ut, causal);
+template <int D>
+__host__ __device__ inline long long cost_of_block(const Seq& q, int b, const Shape& sh) {
+  const int hi = imin(q.qn, (b + 1) * sh.ut);
+  return cost_of<D>(1, keys_upto(q, hi, sh.causal), sh.form(hi - b * sh.ut));
 }
 
-// Border c of `ctas` equal runs of `total` tiles.
-__host__ __device__ inline long long border(long long total, int c, int ctas) {
-  return c >= ctas ? total : total * c / ctas;
+// Of one key head.
+template <int D>
+__host__ __device__ inline long long cost_of_seq(const Seq& q, const Shape& sh) {
+  const int nb = blocks_of(q, sh.ut);
+  return nb == 0 ? 0 : cost_before<D>(q, nb - 1, sh) + cost_of_block<D>(q, nb - 1, sh);
 }
 
-// Tile x of a sequence (all key heads; `per_head` tiles each): its key head,
-// block and key tile.  A tile within `tol` of its unit's border moves there:
-// returns the distance moved, and j = the unit's tiles where it moved to the end.
-__host__ __device__ inline int place(const Seq& q, long long x, long long per_head, int ut, int causal, long long tol,
-                                     int& hk, int& b, int& j) {
-  hk = (int)(x / per_head);
-  const long long y = x - hk * per_head;
-  int lo = 0, hi = (q.qn + ut - 1) / ut;  // tiles_before(lo) <= y < tiles_before(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (tiles_before(q, mid, ut, causal) <= y)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  b = lo;
-  const int at = (int)(y - tiles_before(q, lo, ut, causal)), n = unit_tiles(q, lo, ut, causal);
-  j = at <= tol ? 0 : n - at <= tol ? n : at;
-  return j - at;
+// CTAs that work of this total is given to: each gets a tile's cost at least.
+template <int D>
+__host__ __device__ inline int ctas_for(long long total, int grid) {
+  const long long most = total / (128 * (tile_cost<D>(kFourCopies) + unit_cost<D>(kFourCopies)));
+  return most >= grid ? grid : most > 0 ? (int)most : total > 0 ? 1 : 0;
 }
 
-// How near to a unit's border a cut moves there: a sixteenth of a run, so that
-// runs stay equal within an eighth and fewer units leave partial outputs.
-__host__ __device__ inline long long snap_tolerance(long long total, int ctas) {
-  return ctas > 0 ? total / ctas / 16 : 0;
+// Border c of `ctas` runs of `total`, whose ctas-th part is `part`.
+__host__ __device__ inline long long border(long long total, long long part, int c, int ctas) {
+  const int rest = (int)(total - part * ctas);
+  return c >= ctas ? total : part * c + imin(c, rest);
 }
 
-// A run's segments: parts of units, each walked by every role on its own.
-struct Walk {
-  long long rem;  // key tiles left
+// Whether position y of a key head's cost lies in block b.  Then j is the key
+// tile at which the unit is cut: 0 or its number of tiles (no cut) where that is
+// near.  A cut costs both sides about what `unit_cost` says, and saves each side
+// as many tiles as it moves.
+template <int D>
+__host__ __device__ inline bool place(const Seq& q, long long y, int b, const Shape& sh, int& j) {
+  const long long at = y - cost_before<D>(q, b, sh);
+  if (at < 0 || at >= cost_of_block<D>(q, b, sh)) return false;
+  const Form f = sh.form(imin(q.qn, (b + 1) * sh.ut) - b * sh.ut);
+  const int n = unit_tiles(q, b, sh), near = f == kTwoTiles ? 2 : 1;
+  const long long in = at - 128 * unit_cost<D>(f);
+  j = in <= 0 ? 0 : imin(n, (int)(in / (128 * tile_cost<D>(f))));
+  if (j <= near)
+    j = 0;
+  else if (n - j <= near)
+    j = n;
+  return true;
+}
+
+// A place in the row of units: key tile j of block b of key head hk of sequence s.
+struct Spot {
   int s, hk, b, j;
+};
+
+// Where a role stands in its walk through the run.
+struct Walk {
+  Spot at;
   Seq q;
 };
 
@@ -120,55 +148,57 @@ struct Segment {
   int n, j0, j1;   // key tiles of the unit, of this segment
 };
 
-// What a walk needs to know: `seq(s)` gives a sequence, S, Hk, causal.
+__host__ __device__ inline bool same_unit(const Spot& a, const Spot& b) { return a.s == b.s && a.hk == b.hk && a.b == b.b; }
+
+// To the next unit.  P tells what a walk needs to know: `seq(s)` gives a sequence; S, Hk.
 template <class P>
-__host__ __device__ inline void walk_skip(const P& p, Walk& w, int ut) {  // to the next unit
-  w.j = 0;
-  if (++w.b * ut < w.q.qn) return;
-  w.b = 0;
-  if (++w.hk < p.Hk) return;
-  w.hk = 0;
-  while (++w.s < p.S) {
-    w.q = p.seq(w.s);
+__host__ __device__ inline void walk_skip(const P& p, Walk& w, const Shape& sh) {
+  w.at.j = 0;
+  if (++w.at.b * sh.ut < w.q.qn) return;
+  w.at.b = 0;
+  if (++w.at.hk < p.Hk) return;
+  w.at.hk = 0;
+  while (++w.at.s < p.S) {
+    w.q = p.seq(w.at.s);
     if (w.q.qn > 0) return;
   }
-  w.rem = 0;
 }
 
-// `rem` tiles from tile j of block b of key head hk of sequence s on.
+// The current segment of a run up to `end`; false at its end.
 template <class P>
-__host__ __device__ inline Walk walk_start(const P& p, long long rem, int s, int hk, int b, int j, int ut) {
-  Walk w = {s >= p.S ? 0 : rem, s, hk, b, j, {0, 0, 0}};
-  if (w.rem > 0) {
-    w.q = p.seq(s);
-    if (w.j == unit_tiles(w.q, w.b, ut, p.causal)) walk_skip(p, w, ut);
-  }
-  return w;
-}
-
-// The current segment; false at the run's end.
-template <class P>
-__host__ __device__ inline bool walk_get(const P& p, const Walk& w, int ut, Segment& g) {
-  if (w.rem <= 0) return false;
-  g.tok0 = w.b * ut;
-  g.ntok = imin(ut, w.q.qn - g.tok0);
-  g.n = unit_tiles(w.q, w.b, ut, p.causal);
-  g.j0 = w.j;
-  g.j1 = (int)(w.rem < g.n - w.j ? w.j + w.rem : g.n);
+__host__ __device__ inline bool walk_get(const P& p, const Walk& w, const Spot& end, const Shape& sh, Segment& g) {
+  if (w.at.s >= p.S) return false;
+  const bool last = same_unit(w.at, end);
+  if (last && w.at.j >= end.j) return false;
+  g.tok0 = w.at.b * sh.ut;
+  g.ntok = imin(sh.ut, w.q.qn - g.tok0);
+  g.n = unit_tiles(w.q, w.at.b, sh);
+  g.j0 = w.at.j;
+  g.j1 = last ? end.j : g.n;
   return true;
 }
 
 template <class P>
-__host__ __device__ inline void walk_next(const P& p, Walk& w, int ut, const Segment& g) {
-  w.rem -= g.j1 - g.j0;
-  if (w.rem > 0) walk_skip(p, w, ut);
+__host__ __device__ inline void walk_next(const P& p, Walk& w, const Spot& end, const Shape& sh, const Segment& g) {
+  if (same_unit(w.at, end))
+    w.at.j = g.j1;  // the run's last segment
+  else
+    walk_skip(p, w, sh);
+}
+
+// `q` is sequence at.s (anything for at.s >= S).
+template <class P>
+__host__ __device__ inline Walk walk_start(const P& p, const Spot& at, const Spot& end, const Seq& q, const Shape& sh) {
+  Walk w = {at, q};
+  if (at.s < p.S && !same_unit(at, end) && at.j >= unit_tiles(q, at.b, sh)) walk_skip(p, w, sh);
+  return w;
 }
 
 // Key tiles of query tile 0 of a two-tile unit within the segment (tile 1
 // sees every one of the unit's).
-__host__ __device__ inline int tile0_count(const Seq& q, const Segment& g, int tt, int causal) {
-  const int vis = causal ? q.kv - q.qn + g.tok0 + tt : q.kv;
-  const int n0 = vis <= 0 ? 0 : imin((vis + kTileRows - 1) >> 7, g.n);
+__host__ __device__ inline int tile0_count(const Seq& q, const Segment& g, const Shape& sh) {
+  const int vis = keys_upto(q, g.tok0 + sh.tt, sh.causal);
+  const int n0 = imin((vis + kTileRows - 1) >> 7, g.n);
   return imax(0, imin(g.j1, n0) - g.j0);
 }
 

@@ -3,10 +3,10 @@
 ``fa_paged_plan.cuh`` holds the index arithmetic that the CTAs share.  A driver
 built from it walks random ragged batches (empty sequences, single tokens, long
 chunks, lengths shorter than their chunk, unusual block sizes) and checks that
-the tile counts in closed form equal sums over the blocks, that the runs of all
-CTAs together visit every key tile of every unit once and in order, that a
-unit that is cut is continued by the following CTAs until one ends it, and that
-no run exceeds its even share by more than the two moved borders.
+costs in closed form equal sums over the blocks, that the runs of all CTAs
+together visit every key tile of every unit once and in order, that a unit that
+is cut is continued by the CTAs right behind until one ends it, and that no run
+costs more than its even share and what its two borders may move.
 """
 
 import os
@@ -30,26 +30,24 @@ static int fail(const char* what, long long a, long long b, long long c) {
 }
 struct Batch {
   std::vector<Seq> seqs;
-  int S, Hk, causal;
+  int S, Hk;
   Seq seq(int s) const { return seqs[s]; }
 };
-int main() {
-  std::mt19937 g(7);
+template <int D>
+int run() {
+  std::mt19937 g(7 + D);
   auto pick = [&](int lo, int hi) { return (int)(lo + g() % (unsigned)(hi - lo + 1)); };
-  for (int i = 0; i < 20000; ++i) {
-    const unsigned n = pick(0, 40), m = pick(1, 200), a = pick(0, 400), b = pick(0, 500);
-    long long want = 0;
-    for (unsigned k = 0; k < n; ++k) want += (a * k + b) / m;
-    if (floor_sum(n, m, a, b) != want) return fail("floor_sum", n, m, a);
-  }
-  const int uts[] = {1, 2, 3, 8, 21, 32, 64, 85, 128, 200, 256};
+  const int Gs[] = {1, 2, 3, 4, 5, 6, 8, 16, 20, 32, 33, 64, 128};
   for (int round = 0; round < 3000; ++round) {
     Batch p;
     p.S = pick(1, round % 10 ? 12 : 60);
     p.Hk = pick(1, 5);
-    p.causal = pick(0, 3) > 0;
-    const int ut = uts[pick(0, 10)], grid = pick(0, 1) ? 152 : pick(1, 40);
-    const int long_q = pick(0, 2) ? 3 : 3000, long_kv = pick(0, 2) ? 400 : 9000;
+    const int G = Gs[pick(0, 12)], grid = pick(0, 1) ? 152 : pick(1, 40);
+    const bool is_short = G <= 32 && pick(0, 2) == 0;
+    Shape sh = {0, 128 / G, 32 / G, pick(0, 3) > 0};
+    sh.ut = is_short ? sh.t4 : 2 * sh.tt;
+    const int ut = sh.ut;
+    const int long_q = pick(0, 2) ? 3 : is_short ? 200 : 3000, long_kv = pick(0, 2) ? 400 : 9000;
     std::vector<long long> before(p.S + 1, 0);
     for (int s = 0; s < p.S; ++s) {
       bool bad = false;
@@ -59,65 +57,80 @@ int main() {
       p.seqs.push_back(q);
       long long sum = 0;
       for (int b = 0; b * ut < qn; ++b) {
-        if (tiles_before(q, b, ut, p.causal) != sum) return fail("tiles_before", s, b, sum);
+        if (cost_before<D>(q, b, sh) != sum) return fail("cost_before", s, b, sum);
         int most = 0;  // by the definition, over the block's tokens
         for (int t = b * ut; t < qn && t < (b + 1) * ut; ++t) {
-          const int see = p.causal ? kv - qn + t + 1 : kv;
+          const int see = sh.causal ? kv - qn + t + 1 : kv;
           most = see > most ? see : most;
         }
         const int n = most > 128 ? (most + 127) / 128 : 1;
-        if (unit_tiles(q, b, ut, p.causal) != n) return fail("unit_tiles", s, b, n);
-        sum += n;
+        if (unit_tiles(q, b, sh) != n) return fail("unit_tiles", s, b, n);
+        if (cost_of_block<D>(q, b, sh) <= 0) return fail("cost", s, b, 0);
+        sum += cost_of_block<D>(q, b, sh);
       }
-      if (seq_tiles(q, ut, p.causal) != sum) return fail("seq_tiles", s, sum, 0);
+      if (cost_of_seq<D>(q, sh) != sum) return fail("cost_of_seq", s, sum, 0);
       before[s + 1] = before[s] + sum * p.Hk;
     }
     const long long total = before[p.S];
-    const int ctas = (int)(total < grid ? total : grid);
-    const long long tol = snap_tolerance(total, ctas);
-    // every CTA's run, as the kernel computes it
-    struct Run { long long x0, x1; int s, hk, b, j; };
-    auto at = [&](int c, Run* r) -> long long {
-      const long long x = border(total, c, ctas);
+    const int ctas = ctas_for<D>(total, grid);
+    if (ctas > grid || (total > 0) != (ctas > 0)) return fail("ctas", ctas, grid, total);
+    const long long share = ctas ? total / ctas : 0;
+    // every CTA's borders, as the kernel computes them
+    Seq found_q = {0, 0, 0};
+    auto spot = [&](int c, Spot* out) -> bool {
+      const long long x = border(total, share, c, ctas);
+      *out = {p.S, 0, 0, 0};
       for (int s = 0; s < p.S; ++s)
         if (x >= before[s] && x < before[s + 1]) {
-          int hk, b, j;
-          const int moved = place(p.seqs[s], x - before[s], (before[s + 1] - before[s]) / p.Hk, ut, p.causal, tol, hk,
-                                  b, j);
-          if (r) r->s = s, r->hk = hk, r->b = b, r->j = j;
-          return x + moved;
+          const long long per_head = (before[s + 1] - before[s]) / p.Hk;
+          const int hk = (int)((x - before[s]) / per_head);
+          int found = 0;
+          for (int b = 0; b * ut < p.seqs[s].qn; ++b) {
+            int j;
+            if (!place<D>(p.seqs[s], x - before[s] - hk * per_head, b, sh, j)) continue;
+            ++found;
+            *out = {s, hk, b, j};
+            found_q = p.seqs[s];
+          }
+          return found == 1;
         }
-      return total;
+      return x == total;
     };
     int s = 0, hk = 0, b = 0, j = 0;  // the tile that comes next
     bool open = false;                // the unit of the last segment goes on
     auto skip_empty = [&] { while (s < p.S && p.seqs[s].qn == 0) ++s; };
     skip_empty();
-    long long seen = 0;
+    long long dearest = 0;
+    for (int s2 = 0; s2 < p.S; ++s2)
+      for (int b2 = 0; b2 * ut < p.seqs[s2].qn; ++b2) {
+        const Form f = sh.form(p.seqs[s2].qn - b2 * ut < ut ? p.seqs[s2].qn - b2 * ut : ut);
+        const long long slack = 128 * (unit_cost<D>(f) + 3 * tile_cost<D>(f)) + 128;
+        dearest = slack > dearest ? slack : dearest;
+      }
     for (int c = 0; c < ctas; ++c) {
-      Run r = {0, 0, p.S, 0, 0, 0};
-      r.x0 = at(c, &r);
-      r.x1 = at(c + 1, nullptr);
-      if (r.x1 < r.x0) return fail("run order", c, r.x0, r.x1);
-      if (r.x1 - r.x0 > total / ctas + 1 + 2 * tol) return fail("run length", c, r.x1 - r.x0, total / ctas);
-      Walk w = walk_start(p, r.x1 - r.x0, r.s, r.hk, r.b, r.j, ut);
+      Spot at, end;
+      if (!spot(c + 1, &end) || !spot(c, &at)) return fail("spot", c, ctas, total);
+      Walk w = walk_start(p, at, end, found_q, sh);
       Segment e;
-      while (walk_get(p, w, ut, e)) {
-        if (w.s != s || w.hk != hk || w.b != b || e.j0 != j) return fail("walk", c, w.s, e.j0);
-        if (open != (e.j0 > 0)) return fail("continued", c, w.s, e.j0);
+      long long cost = 0;
+      const bool owed = open;
+      int segments = 0;
+      while (walk_get(p, w, end, sh, e)) {
+        if (w.at.s != s || w.at.hk != hk || w.at.b != b || e.j0 != j) return fail("walk", c, w.at.s, e.j0);
+        if (open != (e.j0 > 0)) return fail("continued", c, w.at.s, e.j0);
         if (e.j1 <= e.j0 || e.j1 > e.n) return fail("segment", e.j0, e.j1, e.n);
         if (e.ntok < 1 || e.ntok > ut || e.tok0 + e.ntok > w.q.qn) return fail("tokens", e.tok0, e.ntok, ut);
-        for (int tt = 1; tt < e.ntok; ++tt) {
-          const int c0 = tile0_count(w.q, e, tt, p.causal);
-          int want = 0;
-          for (int k = e.j0; k < e.j1; ++k) {
-            const int last = p.causal ? w.q.kv - w.q.qn + e.tok0 + tt - 1 : w.q.kv - 1;
-            want += k * 128 <= last;
-          }
-          if (c0 != want) return fail("tile0_count", c0, want, tt);
+        const int c0 = tile0_count(w.q, e, sh);
+        int want = 0;
+        for (int k = e.j0; k < e.j1 && e.ntok > sh.tt; ++k) {
+          const int last = sh.causal ? w.q.kv - w.q.qn + e.tok0 + sh.tt - 1 : w.q.kv - 1;
+          want += k * 128 <= last;
         }
-        seen += e.j1 - e.j0;
+        if (e.ntok > sh.tt && c0 != want) return fail("tile0_count", c0, want, sh.tt);
+        const Form f = sh.form(e.ntok);
+        cost += 128 * ((long long)tile_cost<D>(f) * (e.j1 - e.j0) + (e.j0 == 0 ? unit_cost<D>(f) : 0));
         open = e.j1 < e.n;
+        ++segments;
         if (open) {
           j = e.j1;
         } else {
@@ -131,11 +144,18 @@ int main() {
             }
           }
         }
-        walk_next(p, w, ut, e);
+        walk_next(p, w, end, sh, e);
       }
+      if (owed && segments == 0) return fail("gap in a unit", c, ctas, total);
+      // even shares, but for the two moved borders
+      if (cost > share + 2 * dearest) return fail("share", c, cost, share);
     }
-    if (seen != total || open) return fail("cover", seen, total, open);
+    if (s != p.S || open) return fail("cover", s, p.S, open);
   }
+  return 0;
+}
+int main() {
+  if (run<64>() || run<128>()) return 1;
   std::printf("OK\n");
   return 0;
 }

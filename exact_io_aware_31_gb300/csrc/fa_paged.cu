@@ -81,7 +81,7 @@ struct PagedCfg {
   static constexpr int kOffPlan = kOffMl + 2 * 64 * 8;
   static constexpr int kPlanBytes = 192;
   static constexpr int kOffBar = kOffPlan + kPlanBytes;
-  static constexpr int kNumBars = 4 + 4 + 2 * kKSlots + 3 * kVSlots + 6 + 1;
+  static constexpr int kNumBars = 4 + 4 + 2 * kKSlots + 3 * kVSlots + 8 + 1;
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4;
@@ -224,6 +224,7 @@ struct PagedBars {
   uint64_t* v_clear;  // the rows behind the sequence's end are zero (one phase a tile that has such rows)
   uint64_t* s_full;   // [2]
   uint64_t* p_full;   // [2]
+  uint64_t* p_half;   // [2] (not with four copies) P of the first 64 keys is there
   uint64_t* o_full;   // [2]
   uint64_t* mma_done;
 };
@@ -266,7 +267,8 @@ __global__ void __launch_bounds__(384, 1)
   B.v_clear = B.v_empty + C::kVSlots;
   B.s_full = B.v_clear + C::kVSlots;
   B.p_full = B.s_full + 2;
-  B.o_full = B.p_full + 2;
+  B.p_half = B.p_full + 2;
+  B.o_full = B.p_half + 2;
   B.mma_done = B.o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = lane; i < C::kNumBars; i += 32) {
       uint64_t* bar = bars + i;
       const bool merge = bar == B.x_full || bar == B.x_next || bar == B.x_done || bar == B.x_done + 1;
-      const bool p_full = bar == B.p_full || bar == B.p_full + 1;
+      const bool p_full = bar >= B.p_full && bar < B.p_full + 4;  // p_half too
       const bool v_empty = bar >= B.v_empty && bar < B.v_empty + C::kVSlots;  // the MMA issuer and warp 10
       mbar_init(bar, merge ? 256 : p_full ? 128 : v_empty ? 2 : 1);
     }
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t q_s = smem_addr(sm + C::kOffQ);
       const uint32_t k_s = smem_addr(sm + C::kOffK);
       const uint32_t v_s = smem_addr(sm + C::kOffV);
-      uint32_t q_uses[2] = {0, 0}, pcnt[2] = {0, 0}, turn = 0, kv_it = 0;
+      uint32_t q_uses[2] = {0, 0}, pcnt[2] = {0, 0}, hcnt[2] = {0, 0}, turn = 0, kv_it = 0;
       uint32_t clears = 0;  // bit st: parity of v_clear[st]
       bool ok = true;
       auto issue_s = [&](int t, uint32_t qa, uint32_t it) {
@@ -446,6 +448,13 @@ __global__ void __launch_bounds__(384, 1)
         if (!mbar_wait_warp(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
         tc_fence_after();
         return true;
+      };
+      // O_t (+)= P_t V: the first or second 64 keys (4 steps of 16), or all
+      auto issue_pv_half = [&](int t, uint32_t it, int h, bool accumulate) {
+        mma_ts_run_w<4, 8, 128>(tbase + C::kColO + 128 * t, tbase + C::kColS + 128 * t + 32 * h,
+                                sdesc(v_s + (it % C::kVSlots) * C::kTileBytes + h * (kSwzBlockBytes / 2),
+                                      kSwzBlockBytes, 1024),
+                                kIdO, accumulate);
       };
       auto issue_pv = [&](int t, uint32_t it, bool accumulate) {
         mma_ts_run_w<8, 8, 128>(tbase + C::kColO + 128 * t, tbase + C::kColS + 128 * t,
@@ -485,14 +494,28 @@ __global__ void __launch_bounds__(384, 1)
           }
           for (int i = 0; i < nt && ok; ++i) {
             const int t = i & 1;
+            const bool halves = !SHORT && form == kOneTile;
+            if (halves) {
+              ok = mbar_wait_warp(&B.p_half[t], (t ? hcnt[1] : hcnt[0]) & 1, status);
+              if (t)
+                ++hcnt[1];
+              else
+                ++hcnt[0];
+              if (!ok || !(ok = wait_v(i))) break;
+              tc_fence_after();
+              issue_pv_half(t, kv_it + i, 0, i >= 2);
+            }
             ok = mbar_wait_warp(&B.p_full[t], (t ? pcnt[1] : pcnt[0]) & 1, status);
             if (t)
               ++pcnt[1];
             else
               ++pcnt[0];
-            if (!ok || !(ok = wait_v(i))) break;
+            if (!ok || (!halves && !(ok = wait_v(i)))) break;
             tc_fence_after();
-            issue_pv(t, kv_it + i, i >= 2);
+            if (halves)
+              issue_pv_half(t, kv_it + i, 1, true);
+            else
+              issue_pv(t, kv_it + i, i >= 2);
             mma_commit_w(&B.v_empty[(kv_it + i) % C::kVSlots]);
             if (i + 2 < nt) {
               if (!(ok = wait_k(kv_it + i + 2))) break;
@@ -525,15 +548,20 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (!ok || i >= cnt[t]) continue;
-              ok = mbar_wait_warp(&B.p_full[t], pcnt[t] & 1, status);
-              ++pcnt[t];
+              ok = mbar_wait_warp(&B.p_half[t], hcnt[t] & 1, status);
+              ++hcnt[t];
               if (ok && !v_ready) {
                 ok = wait_v(i);
                 v_ready = true;
               }
               if (!ok) break;
               tc_fence_after();
-              issue_pv(t, kv_it + i, i > 0);
+              issue_pv_half(t, kv_it + i, 0, i > 0);
+              ok = mbar_wait_warp(&B.p_full[t], pcnt[t] & 1, status);
+              ++pcnt[t];
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv_half(t, kv_it + i, 1, true);
               if (i + 1 < cnt[t]) {
                 if (!k_ready && !(ok = wait_k(kv_it + i + 1))) break;
                 k_ready = true;
@@ -600,15 +628,16 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     int tail_row0 = 0, tail_tok = 0, tail_hk = 0, has_tail = 0, has_head = 0;  // for the header
     float m_run = -INFINITY, l_run = 0.f;  // running maximum (log2 units) and sum of this row, in this warp's columns
-    // One key tile: NC columns from c0 on.  `cut`: column c is seen iff c <= cut (128: no mask).
-    auto tile = [&](auto nc, int c0, bool first, bool mask, int cut) {
+    // One key tile: NC columns from c0 on; MASK: column c is seen iff c <= cut.
+    auto tile = [&](auto nc, auto masked, int c0, bool first, int cut) {
       constexpr int NC = decltype(nc)::value;
+      tc_fence_after();
       uint32_t sv[NC];
 #pragma unroll
       for (int c = 0; c < NC / 32; ++c) tmem_ld32(t_s + c0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
       tmem_wait_ld();
       float* s = reinterpret_cast<float*>(sv);
-      if (mask) {
+      if constexpr (decltype(masked)::value) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) s[c] = (c > cut) ? -INFINITY : s[c];
       }
@@ -665,6 +694,11 @@ __global__ void __launch_bounds__(384, 1)
           pk[k] = pack_bf16x2(p0, p1);
         }
         tmem_st16(t_s + c0 / 2 + 16 * h, pk);
+        if (NC == 128 && h == 1) {  // P V of the first 64 keys may start
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&B.p_half[t]);
+        }
       }
       if constexpr (NC == 32) {  // this copy of the rows takes no other columns
         const uint32_t zero[16] = {};
@@ -698,27 +732,42 @@ __global__ void __launch_bounds__(384, 1)
       const int lim0 = p.causal ? min(past + g.tok0 + tile0, w.q.kv - 1) : w.q.kv - 1;
       m_run = -INFINITY;
       l_run = 0.f;
-      for (int i = 0; i < cnt; ++i) {
-        if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
-        ++scnt;
-        const int kbase = (jfirst + i * jstep) * kTileRows;
-        const bool mask = kbase + kTileRows - 1 > lim0;
-        if (four) {
-          tc_fence_after();
-          tile(std::integral_constant<int, 32>{}, 32 * quarter, i == 0, mask, lim - kbase - 32 * quarter);
-        } else if constexpr (!SHORT) {
-          if (busy) {
-            tc_fence_after();
-            tile(std::integral_constant<int, 128>{}, 0, i == 0, mask, lim - kbase);
+      if (!SHORT && cnt > 0 && guard) {
+        // both halves must have read that O before P V overwrites it
+        const int b = ~turn & 1;  // that unit's buffer: the one in front of the next
+        if (!(ok = mbar_wait_warp(&B.x_done[b], ((b ? x_uses[1] : x_uses[0]) - 1) & 1, status))) break;
+        guard = false;
+      }
+      // Key tiles [0, free) need no mask, the others come behind them: two loops, so
+      // that the first has no masking in it (4% of a long chunk's time).
+      const int free = min(cnt, max(0, ((lim0 + 1) >> 7) - jfirst + jstep - 1) / jstep);
+      auto tiles = [&](auto nc, auto masked, int c0, int from, int to) {
+        for (int i = from; i < to && ok; ++i) {
+          if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
+          ++scnt;
+          tile(nc, masked, c0, i == 0, lim - (jfirst + i * jstep) * kTileRows - c0);
+          mbar_arrive(&B.p_full[t]);
+        }
+      };
+      constexpr std::false_type kFree{};
+      constexpr std::true_type kMasked{};
+      if (four) {
+        constexpr std::integral_constant<int, 32> kQuarter{};
+        tiles(kQuarter, kFree, 32 * quarter, 0, free);
+        tiles(kQuarter, kMasked, 32 * quarter, free, cnt);
+      } else if constexpr (!SHORT) {
+        constexpr std::integral_constant<int, 128> kAll{};
+        if (busy) {
+          tiles(kAll, kFree, 0, 0, free);
+          tiles(kAll, kMasked, 0, free, cnt);
+        } else {
+          for (int i = 0; i < cnt && ok; ++i) {
+            if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
+            ++scnt;
+            mbar_arrive(&B.p_half[t]);
+            mbar_arrive(&B.p_full[t]);
           }
         }
-        if (!SHORT && guard) {
-          // both halves must have read that O before P V overwrites it
-          const int b = ~turn & 1;  // that unit's buffer: the one in front of the next
-          if (!(ok = mbar_wait_warp(&B.x_done[b], ((b ? x_uses[1] : x_uses[0]) - 1) & 1, status))) break;
-          guard = false;
-        }
-        mbar_arrive(&B.p_full[t]);
       }
       if (ok && cnt > 0) {
         ok = mbar_wait_warp(&B.o_full[t], ocnt & 1, status);

@@ -883,41 +883,45 @@ __global__ void __launch_bounds__(384, 1)
           const int c_lo = merge ? t * (D / 2) : 0, c_hi = merge ? c_lo + D / 2 : D;
           const uint32_t t_o1 = tmem_lane_col(tbase, quarter * 32, C::kColO + 128 * (1 - t));
 #pragma unroll 1
-          for (int c = c_lo; c < c_hi; c += 16) {
-            float x[16];
+          for (int c = c_lo; c < c_hi; c += 32) {
+            uint32_t v[32];
             if (cnt > 0) {
-              uint32_t v[16];
-              tmem_ld16(t_o + c, v);
+              tmem_ld32(t_o + c, v);
               if (merge) {
-                uint32_t u[16];
-                tmem_ld16(t_o1 + c, u);
+                uint32_t u[32];
+                tmem_ld32(t_o1 + c, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
+                for (int k = 0; k < 32; ++k) {
                   // a half that saw no key has weight 0 and an O of zeros times V
-                  const float a = w0 == 0.f ? 0.f : w0 * __uint_as_float(v[k]);
-                  x[k] = w1 == 0.f ? a : fmaf(w1, __uint_as_float(u[k]), a);
+                  const float x = w0 == 0.f ? 0.f : w0 * __uint_as_float(v[k]);
+                  v[k] = __float_as_uint(w1 == 0.f ? x : fmaf(w1, __uint_as_float(u[k]), x));
                 }
               } else {
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = empty ? 0.f : w0 * __uint_as_float(v[k]);
+                for (int k = 0; k < 32; ++k) v[k] = empty ? 0u : __float_as_uint(w0 * __uint_as_float(v[k]));
               }
             } else {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = 0.f;
+              for (int k = 0; k < 32; ++k) v[k] = 0u;
             }
             if (!valid) continue;
-            uint32_t y[8];
             if (whole) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-              store32(static_cast<__nv_bfloat16*>(p.o) + out_row * D + c, y);
+              for (int h = 0; h < 2; ++h) {
+                uint32_t y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  y[k] = pack_bf16x2(__uint_as_float(v[16 * h + 2 * k]), __uint_as_float(v[16 * h + 2 * k + 1]));
+                store32(static_cast<__nv_bfloat16*>(p.o) + out_row * D + c + 16 * h, y);
+              }
             } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < 4; ++h) {
+                uint32_t y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(x[8 * h + k]);
+                for (int k = 0; k < 8; ++k) y[k] = v[8 * h + k];
                 store32(p.part_o + part * D + c + 8 * h, y);
               }
             }
@@ -972,15 +976,15 @@ __global__ void __launch_bounds__(384, 1)
 
 // Merges the units that were cut: block (c, y) takes rows of the unit that CTA
 // c began and did not end.  Its parts are CTA c's second slot and the first
-// slots of the CTAs behind it up to the one that ended it.  A warp a row; what
-// it reads does not wait for one another where that can be helped (the last
-// part's number, the maxima and the first outputs are asked for together: the
-// kernel is a chain of reads, 5 to 8 us long before).
-template <int D>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, int ctas) {
-  constexpr int kPer = D / 32, kAhead = 4;
+// slots of the CTAs behind it up to the one that ended it, added in that order.
+// D / 8 lanes a row, AHEAD parts asked for at once: two where the rows are many
+// (40 MB in all where every CTA cut a unit of 256 rows), eight for the few
+// rows of short chunks, whose keys may be spread over many CTAs.
+template <int D, int AHEAD>
+__global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(const PagedParams p, int ctas) {
+  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kRowsABlock = 8 * kRowsAWarp;
   const int c = blockIdx.x;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, l8 = lane % kLanes;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   auto slot = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1000,58 +1004,54 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const PagedParams p, i
   const int parts = last - c + 1;
   const int tile = p.tile_tokens * p.G;
   const int rows = h.z * p.G;  // valid rows, densely numbered
-  for (int n = blockIdx.y * 8 + threadIdx.x / 32; n < rows; n += gridDim.y * 8) {
+  for (int n0 = blockIdx.y * kRowsABlock + threadIdx.x / 32 * kRowsAWarp; n0 < rows; n0 += gridDim.y * kRowsABlock) {
+    const int n = min(n0 + lane / kLanes, rows - 1);  // (rows past the end repeat the last one)
     const int prow = n < tile ? n : 128 + n - tile;
-    float v[kAhead][kPer];
-    auto load = [&](int i, float (&x)[kPer]) {
-      const float* src = p.part_o + (slot(i) + prow) * D + kPer * lane;
-      if constexpr (kPer == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        x[0] = f.x, x[1] = f.y;
-      }
+    float4 v[AHEAD][2];
+    float2 x[AHEAD];
+    auto load = [&](int i, int k) {
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot(i) + prow) * D) + 2 * l8;
+      v[k][0] = src[0];
+      v[k][1] = src[1];
+      x[k] = ml[slot(i) + prow];
     };
+    float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i < parts) load(i, v[i]);
-    float2 mine = lane < parts ? ml[slot(lane) + prow] : make_float2(-INFINITY, 0.f);
-    float m = mine.x;
-    for (int i = lane + 32; i < parts; i += 32) m = fmaxf(m, ml[slot(i) + prow].x);
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < 2 || k < parts) load(k, k);  // a cut unit has two parts at least
 #pragma unroll
-    for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.f, acc[kPer];
+    for (int k = 0; k < AHEAD; ++k)
+      if (k < 2 || k < parts) m = fmaxf(m, x[k].x);
+    if (parts > AHEAD) {
+      for (int i = AHEAD + l8; i < parts; i += kLanes) m = fmaxf(m, ml[slot(i) + prow].x);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      if (i0 > 0) mine = i0 + lane < parts ? ml[slot(i0 + lane) + prow] : make_float2(-INFINITY, 0.f);
-      const float mw = mine.x == -INFINITY ? 0.f : ex2(mine.x - m);
-      const float ml2 = mw * mine.y;
-      for (int i = i0; i < parts && i < i0 + 32; i += kAhead) {
+      for (int off = kLanes / 2; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+    float l = 0.f, acc[8] = {};
+    for (int i = 0; i < parts; i += AHEAD) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float w = __shfl_sync(0xffffffffu, mw, (i - i0 + k) & 31);
-          l += __shfl_sync(0xffffffffu, ml2, (i - i0 + k) & 31);
-          if (i + k >= parts) continue;
+      for (int k = 0; k < AHEAD; ++k) {
+        if (i + k >= parts) continue;
+        const float w = x[k].x == -INFINITY ? 0.f : ex2(x[k].x - m);
+        l = fmaf(w, x[k].y, l);
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        for (int e = 0; e < 2; ++e) {
+          acc[4 * e + 0] = fmaf(w, v[k][e].x, acc[4 * e + 0]);
+          acc[4 * e + 1] = fmaf(w, v[k][e].y, acc[4 * e + 1]);
+          acc[4 * e + 2] = fmaf(w, v[k][e].z, acc[4 * e + 2]);
+          acc[4 * e + 3] = fmaf(w, v[k][e].w, acc[4 * e + 3]);
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (i + kAhead + k < parts) load(i + kAhead + k, v[k]);
+        if (i + k + AHEAD < parts) load(i + k + AHEAD, k);
       }
     }
+    if (n0 + lane / kLanes >= rows) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int tok = n / p.G;
     const size_t row = (size_t)(h.y + tok) * (p.Hk * p.G) + h.w * p.G + (n - tok * p.G);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D) + (kPer / 2) * lane;
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-      *dst = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[l8] =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (l8 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
   }
 }
 
@@ -1071,7 +1071,7 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.grid, SHORT ? 4 : 16);
+  cfg.gridDim = dim3(a.grid, SHORT ? 2 : 4);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1079,7 +1079,7 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, a.p, a.grid);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, SHORT ? 8 : 2>, a.p, a.grid);
 }
 
 }  // namespace

@@ -25,18 +25,16 @@ struct Shape {
   }
 };
 
-// Cost of a unit: `tile` for each key tile, `unit` for its beginning and end.
-// From traces on GB300, in steps of about 0.5 us (d = 128) and 0.4 us (d = 64): a
-// key tile against two query tiles takes 1.5 us, against one 1.1 (0.75 at
-// d = 64), against four copies of short rows 1.1 (0.4); a unit's first scores
-// and its output another 2 to 4 us.
+// Cost of a unit: `tile` for each key tile, `unit` for its beginning and end, in
+// tenths of a microsecond as traced on GB300 in batches of all forms.  (Four
+// copies: what the SM's share of HBM takes for a tile; two tiles: the softmax.)
 template <int D>
 __host__ __device__ inline int tile_cost(Form f) {
-  return D == 128 ? (f == kTwoTiles ? 3 : 2) : (f == kTwoTiles ? 4 : f == kOneTile ? 2 : 1);
+  return D == 128 ? (f == kTwoTiles ? 15 : f == kOneTile ? 10 : 12) : (f == kTwoTiles ? 12 : f == kOneTile ? 7 : 6);
 }
 template <int D>
 __host__ __device__ inline int unit_cost(Form f) {
-  return D == 128 ? (f == kTwoTiles ? 7 : 4) : (f == kTwoTiles ? 7 : 5);
+  return D == 128 ? (f == kTwoTiles ? 45 : f == kOneTile ? 35 : 24) : (f == kTwoTiles ? 30 : f == kOneTile ? 25 : 11);
 }
 
 struct Seq {
@@ -69,7 +67,7 @@ __host__ __device__ inline int unit_tiles(const Seq& q, int b, const Shape& sh) 
   return imax(1, (keys_upto(q, imin(q.qn, (b + 1) * sh.ut), sh.causal) + kTileRows - 1) >> 7);
 }
 
-// Cost of a unit that sees `keys` keys, in 128ths of the steps above: keys + 127
+// Cost of a unit that sees `keys` keys, in 128ths of the above: keys + 127
 // stand for its tiles, so that sums over blocks are arithmetic series.
 template <int D>
 __host__ __device__ inline long long cost_of(long long blocks, long long keys, Form f) {
@@ -100,10 +98,11 @@ __host__ __device__ inline long long cost_of_seq(const Seq& q, const Shape& sh) 
   return nb == 0 ? 0 : cost_before<D>(q, nb - 1, sh) + cost_of_block<D>(q, nb - 1, sh);
 }
 
-// CTAs that work of this total is given to: each gets a tile's cost at least.
+// CTAs that work of this total is given to: each gets more than the dearest
+// tile's cost, so that every CTA behind a cut has a tile of the unit.
 template <int D>
 __host__ __device__ inline int ctas_for(long long total, int grid) {
-  const long long most = total / (128 * (tile_cost<D>(kFourCopies) + unit_cost<D>(kFourCopies)));
+  const long long most = total / (128 * (tile_cost<D>(kTwoTiles) + 1));
   return most >= grid ? grid : most > 0 ? (int)most : total > 0 ? 1 : 0;
 }
 
@@ -115,19 +114,18 @@ __host__ __device__ inline long long border(long long total, long long part, int
 
 // Whether position y of a key head's cost lies in block b.  Then j is the key
 // tile at which the unit is cut: 0 or its number of tiles (no cut) where that is
-// near.  A cut costs both sides about what `unit_cost` says, and saves each side
-// as many tiles as it moves.
+// a tile away, which costs less than a unit's other beginning and its partial outputs.
 template <int D>
 __host__ __device__ inline bool place(const Seq& q, long long y, int b, const Shape& sh, int& j) {
   const long long at = y - cost_before<D>(q, b, sh);
   if (at < 0 || at >= cost_of_block<D>(q, b, sh)) return false;
   const Form f = sh.form(imin(q.qn, (b + 1) * sh.ut) - b * sh.ut);
-  const int n = unit_tiles(q, b, sh), near = f == kTwoTiles ? 2 : 1;
+  const int n = unit_tiles(q, b, sh);
   const long long in = at - 128 * unit_cost<D>(f);
   j = in <= 0 ? 0 : imin(n, (int)(in / (128 * tile_cost<D>(f))));
-  if (j <= near)
+  if (j <= 1)
     j = 0;
-  else if (n - j <= near)
+  else if (n - j <= 1)
     j = n;
   return true;
 }

@@ -11,7 +11,8 @@ of ``fa_bwd`` (``fa_bwd_preprocess``, ``fa_bwd_dkdv``, ``fa_bwd_dq_convert``),
 the split-KV decode forward (``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_size``), the norm and rotation of queries and keys
 (``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
-``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``, ``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``),
+``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``,
+``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``),
 ``fa_get_device_status``, ``fa_status_string``.
 Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`,
 :func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`,
@@ -374,20 +375,26 @@ def _refuse(t, name, shape, dtype, device):
                      f"{tuple(t.shape)}, strides {t.stride()}")
 
 
-def _dims(t, name, n):
-    """Shape of a tensor of n dimensions on a CUDA device, and the device's index."""
+def _elsewhere(first, stream):
+    """Where a helper must not run as it is called: None, or the context that makes the first tensor's device and the
+    given stream current (what is allocated there belongs to the stream that uses it)."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != n:
-        raise ValueError(f"{name} must be a CUDA tensor of {n} dimensions")
-    return t.shape, t.get_device()
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("the first argument must be a CUDA tensor")
+    if stream is not None:
+        if stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the first tensor on {first.device}")
+        return torch.cuda.stream(stream)
+    device = first.get_device()
+    return None if device == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _rows(t, name, shape, dtype, device):
     """Check rows of any layout; their strides without the last.  Where a size is 1 a stride means nothing, and any
     valid one will do."""
-    st = t.stride()
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or st[-1] != 1:
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or t.stride(-1) != 1:
         _refuse(t, name, shape, dtype, device)
+    st = t.stride()
     if 1 in shape:
         return [s if n > 1 else shape[-1] for s, n in zip(st[:-1], shape[:-1])]
     return st[:-1]
@@ -402,28 +409,12 @@ def _flat(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
-def _on_stream(fn):
-    """The helper run on its tensors' device and, where ``stream`` is given, on that stream: what it allocates belongs
-    to the stream that uses it."""
-    import functools
-
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if stream is None:
-            import torch
-            if not isinstance(first, torch.Tensor) or not first.is_cuda:
-                raise ValueError(f"{fn.__name__} takes CUDA tensors")
-            if first.get_device() == torch.cuda.current_device():
-                return fn(first, *args, **kw)
-            with torch.cuda.device(first.get_device()):
-                return fn(first, *args, **kw)
-        import torch
-        if not isinstance(first, torch.Tensor) or first.device != stream.device:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the first tensor is not")
-        with torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
-
-    return call
+def _shape(t, name, n):
+    """Shape of a tensor of n dimensions."""
+    shape = getattr(t, "shape", ())
+    if len(shape) != n:
+        raise ValueError(f"{name} must be a CUDA tensor of {n} dimensions")
+    return shape
 
 
 def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, device):
@@ -432,7 +423,7 @@ def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, device)
     first = q_weight if q_weight is not None else k_weight
     wt = torch.float32 if first is not None and first.dtype == torch.float32 else torch.bfloat16
     qw, kw = _flat(q_weight, "q_weight", (d,), wt, device), _flat(k_weight, "k_weight", (d,), wt, device)
-    rope_len, rope_dim = (0, 0) if rope is None else _dims(rope, "rope", 2)[0]
+    rope_len, rope_dim = (0, 0) if rope is None else _shape(rope, "rope", 2)
     return (1 if norm else 0, qw, kw, 1 if wt == torch.float32 else 0, eps,
             _flat(rope, "rope", (rope_len, rope_dim), torch.float32, device), rope_len, rope_dim,
             1 if interleaved else 0)
@@ -450,18 +441,20 @@ def rope_table(length, rope_dim, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
-@_on_stream
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6, interleaved=False,
-                 norm=True, out=None):
+                 norm=True, out=None, stream=None):
     """Norm of queries and keys for each head, then rotation: ``q [B, Hq, N, d]``, ``k [B, Hk, N, d]`` bf16 of any
     strides (``x.transpose(1, 2)`` of a token-major projection, a slice of a wider row) -> contiguous
     ``(q_out, k_out)``, what :func:`forward` takes.  ``rope`` is a :func:`rope_table` (None: no rotation),
-    ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only.  ``stream`` (keyword): a stream
-    to run on instead of the current one."""
+    ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only."""
+    where = _elsewhere(q, stream)
+    if where is not None:
+        with where:
+            return qk_norm_rope(q, k, q_weight, k_weight, rope, positions, eps, interleaved, norm, out)
     import torch
     bf16 = torch.bfloat16
-    (B, Hq, N, d), dev = _dims(q, "q", 4)
-    Hk = _dims(k, "k", 4)[0][1]
+    B, Hq, N, d = _shape(q, "q", 4)
+    dev, Hk = q.get_device(), _shape(k, "k", 4)[1]
     sq, sk = _rows(q, "q", (B, Hq, N, d), bf16, dev), _rows(k, "k", (B, Hk, N, d), bf16, dev)
     args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
     pos = _flat(positions, "positions", (B, N), torch.int32, dev)
@@ -478,16 +471,20 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, 
     return q_out, k_out
 
 
-@_on_stream
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6,
-                          interleaved=False, norm=True, grads=None, weight_grads=True, workspace=None):
+                          interleaved=False, norm=True, grads=None, weight_grads=True, workspace=None, stream=None):
     """Gradients ``(dq, dk, dq_weight, dk_weight)`` of :func:`qk_norm_rope` from those of its outputs
     (:func:`backward`'s ``dq, dk``).  ``dq, dk`` have q's and k's shapes, token-major in memory
     (``[B, N, H, d]``) unless ``grads=(dq, dk)`` gives tensors of any strides.  The weights' gradients are
     fp32 ``[d]`` (None with ``norm=False`` or ``weight_grads=False``)."""
+    where = _elsewhere(dq_out, stream)
+    if where is not None:
+        with where:
+            return qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, rope, positions, eps, interleaved,
+                                         norm, grads, weight_grads, workspace)
     import torch
-    (B, Hq, N, d), dev = _dims(q, "q", 4)
-    Hk = _dims(k, "k", 4)[0][1]
+    B, Hq, N, d = _shape(q, "q", 4)
+    dev, Hk = q.get_device(), _shape(k, "k", 4)[1]
     bf16 = torch.bfloat16
     sq, sk = _rows(q, "q", (B, Hq, N, d), bf16, dev), _rows(k, "k", (B, Hk, N, d), bf16, dev)
     dqo = _flat(dq_out, "dq_out", (B, Hq, N, d), bf16, dev)
@@ -520,27 +517,31 @@ def _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, d, device):
     """Checks of the paged cache's tensors: their addresses, ``(S, Hk, num_pages, page_size, max_pages)``, strides."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
-    (num_pages, Hk, page_size, _), _ = _dims(k_pages, "k_pages", 4)
+    num_pages, Hk, page_size, _ = _shape(k_pages, "k_pages", 4)
     shape = (num_pages, Hk, page_size, d)
     steps = (*_rows(k_pages, "k_pages", shape, bf16, device), *_rows(v_pages, "v_pages", shape, bf16, device))
-    (S, max_pages), _ = _dims(page_table, "page_table", 2)
+    S, max_pages = _shape(page_table, "page_table", 2)
     addresses = (_flat(page_table, "page_table", (S, max_pages), i32, device),
                  _flat(cu_seqlens, "cu_seqlens", (S + 1,), i32, device), _flat(kv_lens, "kv_lens", (S,), i32, device))
     return addresses, S, Hk, num_pages, page_size, max_pages, steps
 
 
-@_on_stream
 def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight=None, k_weight=None, rope=None,
-                 eps=1e-6, interleaved=False, norm=True, out=None):
+                 eps=1e-6, interleaved=False, norm=True, out=None, stream=None):
     """Norm and rotate the new tokens' ``q [T, Hq, d]`` and ``k [T, Hk, d]`` at their positions, write keys and values
     into the cache ``k_pages, v_pages [num_pages, Hk, page_size, d]`` (any strides: a token-major pool is a
     ``transpose(1, 2)`` view), and return the queries ``[T, Hq, d]`` for :func:`paged_forward`.
     ``page_table [S, max_pages]``, ``cu_seqlens [S + 1]`` and ``kv_lens [S]`` (new tokens included) are int32 on
-    the device.  ``rope=None, norm=False`` caches k and v as they are.  ``stream`` (keyword): a stream to run on
-    instead of the current one."""
+    the device.  ``rope=None, norm=False`` caches k and v as they are."""
+    where = _elsewhere(q, stream)
+    if where is not None:
+        with where:
+            return paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight, k_weight, rope,
+                                eps, interleaved, norm, out)
     import torch
     bf16 = torch.bfloat16
-    (T, Hq, d), dev = _dims(q, "q", 3)
+    T, Hq, d = _shape(q, "q", 3)
+    dev = q.get_device()
     meta, S, Hk, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                                                                       d, dev)
     sq, sk, sv = (_rows(q, "q", (T, Hq, d), bf16, dev), _rows(k, "k", (T, Hk, d), bf16, dev),
@@ -561,15 +562,20 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
 _paged_workspace = {}  # (device, d) -> bytes
 
 
-@_on_stream
 def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,
-                  lse=None, workspace=None):
+                  lse=None, workspace=None, stream=None):
     """Attention of the new tokens ``q [T, Hq, d]`` (any strides) over the paged cache that :func:`paged_append` wrote;
     returns ``(o [T, Hq, d], lse [T, Hq])``.  ``max_q`` is the longest chunk of the step (0: not known; a hint that
-    selects the kernel variant).  ``stream`` (keyword): a stream to run on instead of the current one."""
+    selects the kernel variant)."""
+    where = _elsewhere(q, stream)
+    if where is not None:
+        with where:
+            return paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale, causal, max_q, out, lse,
+                                 workspace)
     import torch
     bf16 = torch.bfloat16
-    (T, Hq, d), dev = _dims(q, "q", 3)
+    T, Hq, d = _shape(q, "q", 3)
+    dev = q.get_device()
     meta, S, Hk, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens,
                                                                       d, dev)
     sq = _rows(q, "q", (T, Hq, d), bf16, dev)

@@ -1070,6 +1070,8 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // Units of up to three key tiles are never cut (fa_paged_plan.cuh, place()).
+  if (((long long)a.p.max_pages << a.p.page_log2) <= kNeverCut * kTileRows) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid, SHORT ? 2 : 4);
   cfg.blockDim = dim3(256);

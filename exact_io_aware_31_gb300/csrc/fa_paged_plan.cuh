@@ -112,6 +112,9 @@ __host__ __device__ inline long long border(long long total, long long part, int
   return c >= ctas ? total : part * c + imin(c, rest);
 }
 
+// Key tiles of a unit that place() never cuts: no tile of three is two away from both ends.
+constexpr int kNeverCut = 3;
+
 // Whether position y of a key head's cost lies in block b.  Then j is the key
 // tile at which the unit is cut: 0 or its number of tiles (no cut) where that is
 // a tile away, which costs less than a unit's other beginning and its partial outputs.

@@ -90,6 +90,8 @@ int run() {
             if (!place<D>(p.seqs[s], x - before[s] - hk * per_head, b, sh, j)) continue;
             ++found;
             *out = {s, hk, b, j};
+            const int n = unit_tiles(p.seqs[s], b, sh);
+            if (n <= kNeverCut && j != 0 && j != n) return false;
             found_q = p.seqs[s];
           }
           return found == 1;

@@ -185,15 +185,15 @@ struct Factors {
   }
 };
 
-// 1 / rms of STEPS = 4 rows at once.  The lanes of a row exchange halves of the
-// four sums instead of all of them: after two rounds each lane goes on with one
-// row's, so the reduction and the root are done once, not four times.
+// 1 / rms of STEPS (one, two or four) rows at once.  The lanes of a row exchange
+// halves of the sums instead of all of them: after one or two rounds each lane
+// goes on with one row's, so the reduction and the root are done once.
 template <int D, int STEPS>
 __device__ __forceinline__ void inverse_rms(const uint4 (&raw)[STEPS], int l, float eps, float (&r)[STEPS]) {
-  static_assert(STEPS == 4, "four rows");
-  float v[4];
+  static_assert(STEPS == 1 || STEPS == 2 || STEPS == 4, "one, two or four rows");
+  float v[STEPS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     Row x;
     unpack8(raw[i], x);
     uint64_t ss = f2_mul(x[0], x[0]);
@@ -202,14 +202,24 @@ __device__ __forceinline__ void inverse_rms(const uint4 (&raw)[STEPS], int l, fl
     v[i] = pair_sum(ss);
   }
   const bool b0 = l & 1, b1 = l & 2;
-  const float t0 = (b0 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2], 1);
-  const float t1 = (b0 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b0 ? v[1] : v[3], 1);
-  float u = (b1 ? t1 : t0) + __shfl_xor_sync(0xffffffffu, b1 ? t0 : t1, 2);  // row 2 b0 + b1
+  float u;
+  if constexpr (STEPS == 4) {
+    const float t0 = (b0 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[2], 1);
+    const float t1 = (b0 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b0 ? v[1] : v[3], 1);
+    u = (b1 ? t1 : t0) + __shfl_xor_sync(0xffffffffu, b1 ? t0 : t1, 2);  // row 2 b0 + b1
+  } else if constexpr (STEPS == 2) {
+    u = (b0 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, b0 ? v[0] : v[1], 1);  // row b0
+    u += __shfl_xor_sync(0xffffffffu, u, 2);
+  } else {
+    u = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+    u += __shfl_xor_sync(0xffffffffu, u, 2);
+  }
 #pragma unroll
   for (int off = 4; off < D / 8; off *= 2) u += __shfl_xor_sync(0xffffffffu, u, off);
   u = rsqrtf(u * (1.f / D) + eps);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, u, (i >> 1) | ((i & 1) << 1), D / 8);
+  for (int i = 0; i < STEPS; ++i)
+    r[i] = STEPS == 1 ? u : __shfl_sync(0xffffffffu, u, STEPS == 4 ? (i >> 1) | ((i & 1) << 1) : i, D / 8);
 }
 
 // A row's 8 columns of this lane, turned and scaled (c and s folded).
@@ -225,6 +235,74 @@ __device__ __forceinline__ uint4 turn_row(const NormRopeParams& p, const Lane<D,
   return pack8(x);
 }
 
+// The gradient of a row's 8 columns: dz -> dx (c and s of minus the angle), and its part of dw added to `dw` if it
+// counts (a row without a position has no gradient; one that is not there may have no finite 1 / rms).
+template <int D, bool INTER>
+__device__ __forceinline__ uint4 turn_row_back(const NormRopeParams& p, const Lane<D, INTER>& ln, const Row& c,
+                                               const Row& s, const Row& w, const uint4& raw, const uint4& dz,
+                                               bool counts, Row& dw) {
+  Row g, o;
+  unpack8(dz, g);
+  unpack8(partner_of<D, INTER>(p, ln, dz), o);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) g[e] = f2_fma(o[e], s[e], f2_mul(g[e], c[e]));  // dy
+  if (p.norm) {
+    Row x, gw;
+    unpack8(raw, x);
+    uint64_t ss2 = 0, sg2 = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gw[e] = f2_mul(g[e], w[e]);
+      ss2 = f2_fma(x[e], x[e], ss2);
+      sg2 = f2_fma(x[e], gw[e], sg2);
+    }
+    float ss = pair_sum(ss2), sg = pair_sum(sg2);
+    // both sums at once: even lanes go on with one, odd lanes with the other
+    const bool odd = ln.l & 1;
+    float v = (odd ? sg : ss) + __shfl_xor_sync(0xffffffffu, odd ? ss : sg, 1);
+#pragma unroll
+    for (int off = D / 16; off > 1; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+    ss = odd ? u : v;
+    sg = odd ? v : u;
+    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+    const float k = -sg * (1.f / D) * r * r * r;  // -mean(g x r) r^2, per unit of x
+    const float rw = counts ? r : 0.f;
+    const uint64_t r2 = f2_pack(r, r), k2 = f2_pack(k, k), rw2 = f2_pack(rw, rw);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      dw[e] = f2_fma(g[e], f2_mul(x[e], rw2), dw[e]);
+      g[e] = f2_fma(x[e], k2, f2_mul(gw[e], r2));
+    }
+  }
+  return pack8(g);
+}
+
+// A CTA's sums of the weights' gradients: rows of the warp, then its warps.
+template <int D>
+__device__ __forceinline__ void store_partial(const Row& dw, int l, int sub, float* partial) {
+  constexpr int LPR = D / 8;
+  __shared__ float acc[kWarps][D];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    f2_unpack(dw[e], lo, hi);
+#pragma unroll
+    for (int off = LPR; off < 32; off *= 2) {
+      lo += __shfl_xor_sync(0xffffffffu, lo, off);
+      hi += __shfl_xor_sync(0xffffffffu, hi, off);
+    }
+    if (sub == 0) acc[threadIdx.x / 32][8 * l + 2 * e] = lo, acc[threadIdx.x / 32][8 * l + 2 * e + 1] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int wp = 0; wp < kWarps; ++wp) v += acc[wp][threadIdx.x];
+    partial[(size_t)blockIdx.x * D + threadIdx.x] = v;
+  }
+}
+
 // A chunk: up to kRows heads of one token.
 template <int D, int STEPS>
 struct Chunk {
@@ -233,20 +311,14 @@ struct Chunk {
   static constexpr int kRows = RPW * STEPS;   // heads a chunk
   __host__ __device__ static int of(int H) { return (H + kRows - 1) / kRows; }
 };
-constexpr int kFwdSteps = 4;
 // CTAs an SM of the forward: at three (80 registers) nothing spills; four and
 // five measured 89 and 110 us against 85 (B = 64, N = 1024, 16 + 16 heads, d = 64).
 constexpr int kFwdCtas = 3;
-// The gradient at 4 steps and two CTAs an SM: 153 us; 2 steps and three 171,
-// 1 step and four 188 (the same sizes: 0.8 GB, 119 us at the copy rate).
-constexpr int kBwdSteps = 4;
-static_assert(2 * ((kNormRopeMaxHeads + Chunk<128, kBwdSteps>::kRows - 1) / Chunk<128, kBwdSteps>::kRows) <=
-              kNormRopeMaxCtas);
 
 // ----------------------------------------------------------------- forward ---
-template <int D, bool INTER>
+template <int D, bool INTER, int STEPS>
 __global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const NormRopeLaunch a) {
-  using I = Chunk<D, kFwdSteps>;
+  using I = Chunk<D, STEPS>;
   const int lane = threadIdx.x & 31, sub = lane / I::LPR;
   const Lane<D, INTER> ln(a.p, lane);
   const unsigned cq = I::of(a.H[0]);
@@ -266,20 +338,20 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const Nor
     if (token >= (unsigned)a.B * a.N) return;
     const unsigned b = a.by_n.div(token), n = token - b * a.N;
     const __nv_bfloat16* src = base + b * in.sb + n * in.sn;
-    uint4 raw[kFwdSteps];
+    uint4 raw[STEPS];
 #pragma unroll
-    for (int i = 0; i < kFwdSteps; ++i, src += hop)
+    for (int i = 0; i < STEPS; ++i, src += hop)
       raw[i] = h0 + i * I::RPW < H ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
     const int pos = a.positions ? __ldg(a.positions + token) : (int)n;
     const bool bad = a.p.dr > 0 && (pos < 0 || pos >= a.p.rope_len);
     Row c, s;
     load_angles<D, INTER>(a.p, ln, bad ? 0 : pos, c, s);
     f.fold(c, s);
-    float r[kFwdSteps];
-    if (a.p.norm) inverse_rms<D, kFwdSteps>(raw, ln.l, a.p.eps, r);
+    float r[STEPS];
+    if (a.p.norm) inverse_rms<D, STEPS>(raw, ln.l, a.p.eps, r);
     __nv_bfloat16* dst = out + ((size_t)b * H * a.N + n) * D;
 #pragma unroll
-    for (int i = 0; i < kFwdSteps; ++i, dst += out_hop) {
+    for (int i = 0; i < STEPS; ++i, dst += out_hop) {
       const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
       if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
     }
@@ -292,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const Nor
 // tokens; a CTA adds up its warps and writes one row of partial sums, and a
 // second kernel adds those in a fixed order: no atomics, the same bits on every
 // run.
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeLaunch a) {
-  using I = Chunk<D, kBwdSteps>;
+template <int D, bool INTER, int STEPS>
+__global__ void __launch_bounds__(kThreads, STEPS == 4 ? 2 : 3) norm_rope_bwd_kernel(const NormRopeLaunch a) {
+  using I = Chunk<D, STEPS>;
   const int lane = threadIdx.x & 31, sub = lane / I::LPR;
   const Lane<D, INTER> ln(a.p, lane);
   const unsigned cq = I::of(a.H[0]);
@@ -315,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
     const unsigned b = a.by_n.div(token), n = token - b * a.N;
     const __nv_bfloat16* src = base + b * in.sb + n * in.sn;
     const __nv_bfloat16* dsrc = dbase + ((size_t)b * H * a.N + n) * D;
-    uint4 raw[kBwdSteps], dz[kBwdSteps];
+    uint4 raw[STEPS], dz[STEPS];
 #pragma unroll
-    for (int i = 0; i < kBwdSteps; ++i, src += hop, dsrc += dhop) {
+    for (int i = 0; i < STEPS; ++i, src += hop, dsrc += dhop) {
       const bool row = h0 + i * I::RPW < H;
       raw[i] = row && a.p.norm ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
       dz[i] = row ? __ldg(reinterpret_cast<const uint4*>(dsrc)) : make_uint4(0, 0, 0, 0);
@@ -329,84 +401,153 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
     signed_row<D, INTER, true>(ln, s);
     __nv_bfloat16* dst = out + b * dx.sb + n * dx.sn;
 #pragma unroll
-    for (int i = 0; i < kBwdSteps; ++i, dst += out_hop) {
-      Row g, o;
-      unpack8(dz[i], g);
-      unpack8(partner_of<D, INTER>(a.p, ln, dz[i]), o);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = f2_fma(o[e], s[e], f2_mul(g[e], c[e]));  // dy
-      if (a.p.norm) {
-        Row x, gw;
-        unpack8(raw[i], x);
-        uint64_t ss2 = 0, sg2 = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          gw[e] = f2_mul(g[e], w[e]);
-          ss2 = f2_fma(x[e], x[e], ss2);
-          sg2 = f2_fma(x[e], gw[e], sg2);
-        }
-        float ss = pair_sum(ss2), sg = pair_sum(sg2);
-        // both sums at once: even lanes go on with one, odd lanes with the other
-        const bool odd = lane & 1;
-        float v = (odd ? sg : ss) + __shfl_xor_sync(0xffffffffu, odd ? ss : sg, 1);
-#pragma unroll
-        for (int off = I::LPR / 2; off > 1; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
-        const float u = __shfl_xor_sync(0xffffffffu, v, 1);
-        ss = odd ? u : v;
-        sg = odd ? v : u;
-        const float r = rsqrtf(ss * (1.f / D) + a.p.eps);
-        const float kk = -sg * (1.f / D) * r * r * r;  // -mean(g x r) r^2, per unit of x
-        const float rw = bad ? 0.f : r;               // a row without a position has no gradient
-        const uint64_t r2 = f2_pack(r, r), k2 = f2_pack(kk, kk), rw2 = f2_pack(rw, rw);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dw[e] = f2_fma(g[e], f2_mul(x[e], rw2), dw[e]);
-          g[e] = f2_fma(x[e], k2, f2_mul(gw[e], r2));
-        }
-      }
-      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : pack8(g);
+    for (int i = 0; i < STEPS; ++i, dst += out_hop) {
+      const uint4 g = turn_row_back<D, INTER>(a.p, ln, c, s, w, raw[i], dz[i],
+                                                         !bad && h0 + i * I::RPW < H, dw);
+      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : g;
     }
     if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
   }
-  if (a.partial != nullptr) {
-    // rows of the warp, then the warps of the CTA
-    __shared__ float acc[kWarps][D];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float lo, hi;
-      f2_unpack(dw[e], lo, hi);
-#pragma unroll
-      for (int off = I::LPR; off < 32; off *= 2) {
-        lo += __shfl_xor_sync(0xffffffffu, lo, off);
-        hi += __shfl_xor_sync(0xffffffffu, hi, off);
-      }
-      if (sub == 0) acc[threadIdx.x / 32][8 * ln.l + 2 * e] = lo, acc[threadIdx.x / 32][8 * ln.l + 2 * e + 1] = hi;
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float v = 0.f;
-#pragma unroll
-      for (int wp = 0; wp < kWarps; ++wp) v += acc[wp][threadIdx.x];
-      a.partial[(size_t)blockIdx.x * D + threadIdx.x] = v;
-    }
-  }
+  if (a.partial != nullptr) store_partial<D>(dw, ln.l, sub, a.partial);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Adds the rows of partial sums, those of the queries' chunks and those of the
-// keys' (row r belongs to chunk r mod `chunks`): 8 columns a block, 128 threads
-// a column.
+// ------------------------------------------------------- few heads a token ---
+// The same two passes where a chunk of heads would leave most of a warp idle
+// (one query and one key head fill 2 of 32 rows at d = 64: 597 us where the
+// copy rate allows 60): the rows of a tensor in order of token and head, a warp
+// takes neighbouring ones of any tokens, and each row loads its own angles.
+// The first q_blocks CTAs take the queries, the others the keys.
+constexpr int kRowSteps = 2;
+
+template <int D>
+struct RowWalk {
+  static constexpr int RPW = 256 / D;                            // rows a warp and step
+  static constexpr int kBlockRows = kWarps * RPW * kRowSteps;    // a CTA and turn
+  long long rows;      // of the tensor
+  long long first;     // this CTA's first row
+  long long token0;    // its token
+  unsigned head0;      // and head
+  __device__ __forceinline__ RowWalk(const NormRopeLaunch& a, int which, unsigned block) {
+    rows = (long long)a.B * a.N * a.H[which];
+    first = (long long)block * a.walk * kBlockRows;
+    token0 = first / a.H[which];
+    head0 = (unsigned)(first - token0 * a.H[which]);
+  }
+};
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_rows_kernel(const NormRopeLaunch a) {
+  using W = RowWalk<D>;
+  const int lane = threadIdx.x & 31, sub = lane / (D / 8);
+  const Lane<D, INTER> ln(a.p, lane);
+  const int which = blockIdx.x >= a.q_blocks;
+  const W walk(a, which, which ? blockIdx.x - a.q_blocks : blockIdx.x);
+  const HeadRows in = a.in[which];
+  const int H = a.H[which];
+  Factors<D, INTER> f;
+  f.load(a.p, ln, which);
+#pragma unroll 1
+  for (int k = 0; k < a.walk; ++k) {
+    const unsigned at = (k * kWarps + threadIdx.x / 32) * (W::RPW * kRowSteps) + sub;  // behind walk.first
+    if (walk.first + at - sub >= walk.rows) return;
+    uint4 raw[kRowSteps];
+    int pos[kRowSteps];
+    size_t to[kRowSteps];
+    bool there[kRowSteps], bad[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      const unsigned o = at + i * W::RPW;
+      there[i] = walk.first + o < walk.rows;
+      const unsigned t = a.by_h[which].div(walk.head0 + o);
+      const unsigned h = walk.head0 + o - t * H, token = there[i] ? (unsigned)(walk.token0 + t) : 0;
+      const unsigned b = a.by_n.div(token), n = token - b * a.N;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + b * in.sb + n * in.sn + h * in.sh + 8 * ln.l;
+      raw[i] = there[i] ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      pos[i] = a.positions ? __ldg(a.positions + token) : (int)n;
+      to[i] = (((size_t)b * H + h) * a.N + n) * D + 8 * ln.l;
+    }
+    float r[kRowSteps];
+    if (a.p.norm) inverse_rms<D, kRowSteps>(raw, ln.l, a.p.eps, r);
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      bad[i] = a.p.dr > 0 && (pos[i] < 0 || pos[i] >= a.p.rope_len);
+      Row c, s;
+      load_angles<D, INTER>(a.p, ln, bad[i] ? 0 : pos[i], c, s);
+      f.fold(c, s);
+      const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
+      if (!there[i]) continue;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out[which]) + to[i]) =
+          bad[i] ? make_uint4(0, 0, 0, 0) : z;
+      if (bad[i] && ln.l == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+    }
+  }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_rows_bwd_kernel(const NormRopeLaunch a) {
+  using W = RowWalk<D>;
+  const int lane = threadIdx.x & 31, sub = lane / (D / 8);
+  const Lane<D, INTER> ln(a.p, lane);
+  const int which = blockIdx.x >= a.q_blocks;
+  const W walk(a, which, which ? blockIdx.x - a.q_blocks : blockIdx.x);
+  const HeadRows in = a.in[which], dx = a.dx[which];
+  const int H = a.H[which];
+  Row w, dw = {0, 0, 0, 0};
+  load_weights(a.p, which, ln.l, w);
+#pragma unroll 1
+  for (int k = 0; k < a.walk; ++k) {
+    const unsigned at = (k * kWarps + threadIdx.x / 32) * (W::RPW * kRowSteps) + sub;
+    if (walk.first + at - sub >= walk.rows) break;
+    uint4 raw[kRowSteps], dz[kRowSteps];
+    int pos[kRowSteps];
+    __nv_bfloat16* to[kRowSteps];
+    bool there[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      const unsigned o = at + i * W::RPW;
+      there[i] = walk.first + o < walk.rows;
+      const unsigned t = a.by_h[which].div(walk.head0 + o);
+      const unsigned h = walk.head0 + o - t * H, token = there[i] ? (unsigned)(walk.token0 + t) : 0;
+      const unsigned b = a.by_n.div(token), n = token - b * a.N;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + b * in.sb + n * in.sn + h * in.sh + 8 * ln.l;
+      const __nv_bfloat16* dsrc =
+          static_cast<const __nv_bfloat16*>(a.dout[which]) + (((size_t)b * H + h) * a.N + n) * D + 8 * ln.l;
+      raw[i] = there[i] && a.p.norm ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+      dz[i] = there[i] ? __ldg(reinterpret_cast<const uint4*>(dsrc)) : make_uint4(0, 0, 0, 0);
+      pos[i] = a.positions ? __ldg(a.positions + token) : (int)n;
+      to[i] = static_cast<__nv_bfloat16*>(const_cast<void*>(dx.p)) + b * dx.sb + n * dx.sn + h * dx.sh + 8 * ln.l;
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      const bool bad = a.p.dr > 0 && (pos[i] < 0 || pos[i] >= a.p.rope_len);
+      Row c, s;
+      load_angles<D, INTER>(a.p, ln, bad ? 0 : pos[i], c, s);
+      signed_row<D, INTER, true>(ln, s);
+      const uint4 g = turn_row_back<D, INTER>(a.p, ln, c, s, w, raw[i], dz[i], !bad && there[i], dw);
+      if (!there[i]) continue;
+      *reinterpret_cast<uint4*>(to[i]) = bad ? make_uint4(0, 0, 0, 0) : g;
+      if (bad && ln.l == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+    }
+  }
+  if (a.partial != nullptr) store_partial<D>(dw, ln.l, sub, a.partial);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Adds the rows of partial sums, those of the queries' CTAs and those of the
+// keys': row r is a query row if r mod `period` < `cq`.  8 columns a block, 128
+// threads a column.
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ partial, int rows, int d,
-                                                            int cq, int chunks, float* dqw, float* dkw) {
+                                                            int cq, int period, float* dqw, float* dkw) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float acc[32][8];
   const int x = threadIdx.x % 8, y = threadIdx.x / 8;
   const int col = blockIdx.x * 8 + x, which = blockIdx.y;
-  const int first = which ? cq : 0, width = which ? chunks - cq : cq;
-  const int count = rows / chunks * width;
+  const int first = which ? cq : 0, width = which ? period - cq : cq;
+  const int count = rows / period * width;
   float v = 0.f;
 #pragma unroll 4
-  for (int i = y; i < count; i += 128) v += partial[(size_t)(i / width * chunks + first + i % width) * d + col];
+  for (int i = y; i < count; i += 128) v += partial[(size_t)(i / width * period + first + i % width) * d + col];
 #pragma unroll
   for (int off = 8; off < 32; off *= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
   if (threadIdx.x % 32 < 8) acc[threadIdx.x / 32][x] = v;
@@ -443,70 +584,78 @@ __device__ __forceinline__ int find_sequence(const int* cu, int S, int t) {
 // one without a slot (in front of position 0, behind the page table or the
 // rotation table, or in a page outside the pool) is not cached, and its query
 // row is zero where it has no position.
-template <int D, bool INTER>
+// A warp takes one token: one chunk of its heads, or (`span`) all of them, so
+// that the search for its sequence and slot is made once.
+template <int D, bool INTER, int STEPS>
 __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendLaunch a) {
-  using I = Chunk<D, kFwdSteps>;
+  using I = Chunk<D, STEPS>;
   const int lane = threadIdx.x & 31, sub = lane / I::LPR;
   const Lane<D, INTER> ln(a.p, lane);
   const unsigned cq = I::of(a.Hq), ck = I::of(a.Hk);
-  const unsigned group = a.by_chunks.div(blockIdx.x), chunk = blockIdx.x - group * a.by_chunks.d;
+  const unsigned group = a.span ? blockIdx.x : a.by_chunks.div(blockIdx.x);
   const unsigned token = group * kWarps + threadIdx.x / 32;
   if (token >= (unsigned)a.T) return;
   const int t = (int)token;
-  const int which = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;  // queries, keys, values
-  const int h0 = (chunk - (which == 0 ? 0 : which == 1 ? cq : cq + ck)) * I::kRows + sub;
-  const int H = which ? a.Hk : a.Hq;
-  const HeadRows in = a.in[which];
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + t * in.sn + h0 * in.sh + 8 * ln.l;
-  const long long in_hop = in.sh * I::RPW;
-  uint4 raw[kFwdSteps];
+  uint4 raw[STEPS];
+  auto load = [&](unsigned chunk) {  // 0 .. cq: queries, then keys, then values
+    const int which = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;
+    const int h0 = (chunk - (which == 0 ? 0 : which == 1 ? cq : cq + ck)) * I::kRows + sub, H = which ? a.Hk : a.Hq;
+    const HeadRows in = a.in[which];
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(in.p) + t * in.sn + h0 * in.sh + 8 * ln.l;
+    const long long hop = in.sh * I::RPW;
 #pragma unroll
-  for (int i = 0; i < kFwdSteps; ++i, src += in_hop)
-    raw[i] = h0 + i * I::RPW < H ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < STEPS; ++i, src += hop)
+      raw[i] = h0 + i * I::RPW < H ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+  };
+  unsigned chunk = a.span ? 0 : blockIdx.x - group * a.by_chunks.d;
+  const unsigned end = a.span ? cq + 2 * ck : chunk + 1;
+  load(chunk);
   const int sq = find_sequence(a.cu_seqlens, a.S, t);
   if (sq < 0 || sq >= a.S) return;  // a row of no sequence: left as it was
   const long long pos = (long long)__ldg(a.kv_lens + sq) - __ldg(a.cu_seqlens + sq + 1) + t;
   const int cap = a.max_pages << a.page_log2;
   const bool bad = pos < 0 || pos >= cap || (a.p.dr > 0 && pos >= a.p.rope_len);
   const int at = bad ? 0 : (int)pos;
-  __nv_bfloat16* dst = nullptr;
-  long long step = 0;
-  bool lost = bad;  // no place to write
-  if (which == 0) {
-    dst = static_cast<__nv_bfloat16*>(a.q_out) + (size_t)t * a.Hq * D + 8 * ln.l;
-    step = D;
-    lost = false;
-  } else if (!bad) {
-    const int page = __ldg(a.page_table + (size_t)sq * a.max_pages + (at >> a.page_log2));
-    lost = page < 0 || page >= a.num_pages;
-    if (!lost) {
-      const int kv = which - 1;
-      dst = static_cast<__nv_bfloat16*>(a.pages[kv]) + page * a.page_sp[kv] +
-            (at & ((1 << a.page_log2) - 1)) * a.page_sr[kv] + 8 * ln.l;
-      step = a.page_sh[kv];
+  const int page = bad || end <= cq ? -1 : __ldg(a.page_table + (size_t)sq * a.max_pages + (at >> a.page_log2));
+  const bool lost = page < 0 || page >= a.num_pages;  // no slot
+  if ((bad || (lost && end > cq)) && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+#pragma unroll 1
+  while (true) {
+    const int which = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;
+    const int h0 = (chunk - (which == 0 ? 0 : which == 1 ? cq : cq + ck)) * I::kRows + sub, H = which ? a.Hk : a.Hq;
+    if (which > 0 && lost) return;
+    __nv_bfloat16* dst;
+    long long hop;
+    if (which == 0) {
+      dst = static_cast<__nv_bfloat16*>(a.q_out) + (size_t)t * a.Hq * D;
+      hop = D;
+    } else {
+      dst = static_cast<__nv_bfloat16*>(a.pages[which - 1]) + page * a.page_sp[which - 1] +
+            (at & ((1 << a.page_log2) - 1)) * a.page_sr[which - 1];
+      hop = a.page_sh[which - 1];
     }
-  }
-  if ((bad || lost) && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
-  if (lost) return;
-  dst += h0 * step;
-  step *= I::RPW;
-  if (which == 2) {
+    dst += h0 * hop + 8 * ln.l;
+    hop *= I::RPW;
+    if (which == 2) {
 #pragma unroll
-    for (int i = 0; i < kFwdSteps; ++i, dst += step)
-      if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = raw[i];
-    return;
-  }
-  Row c, s;
-  load_angles<D, INTER>(a.p, ln, at, c, s);
-  Factors<D, INTER> f;
-  f.load(a.p, ln, which);
-  f.fold(c, s);
-  float r[kFwdSteps];
-  if (a.p.norm) inverse_rms<D, kFwdSteps>(raw, ln.l, a.p.eps, r);
+      for (int i = 0; i < STEPS; ++i, dst += hop)
+        if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = raw[i];
+    } else {
+      Row c, s;
+      load_angles<D, INTER>(a.p, ln, at, c, s);
+      Factors<D, INTER> f;
+      f.load(a.p, ln, which);
+      f.fold(c, s);
+      float r[STEPS];
+      if (a.p.norm) inverse_rms<D, STEPS>(raw, ln.l, a.p.eps, r);
 #pragma unroll
-  for (int i = 0; i < kFwdSteps; ++i, dst += step) {
-    const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
-    if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
+      for (int i = 0; i < STEPS; ++i, dst += hop) {
+        const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
+        if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
+      }
+    }
+    if (++chunk == end) return;
+    load(chunk);
   }
 }
 
@@ -521,27 +670,103 @@ int forward_walk(unsigned groups, int chunks, int sms) {
   return walk;
 }
 
-template <int D, bool INTER>
-cudaError_t launch_norm_rope_t(NormRopeLaunch a, cudaStream_t stream) {
-  using I = Chunk<D, kFwdSteps>;
+// Steps of a chunk (4, 2 or 1), or 0 for row by row: the cheapest for these
+// heads.  Costs of a chunk and of a step of the row kernels, from times with
+// 1 to 40 heads at d = 64 and 128 (nanoseconds x 100 a warp's chunk on the
+// whole device): a chunk's set-up weighs more than its rows, so empty rows cost
+// little at four steps, and few heads gain by fewer steps or none.  16 + 16 heads,
+// d = 64, 32000 tokens: 45 us at four steps, 61 at two, 77 row by row; 1 + 1 heads,
+// 400000 tokens: 365, 319, 72.
+template <int D>
+int steps_for(int Hq, int Hk, int keys, const int (&cost)[4]) {  // of 4, 2, 1 steps, of a row step (0: not built)
+  const int of[3] = {Chunk<D, 4>::of(Hq) + keys * Chunk<D, 4>::of(Hk), Chunk<D, 2>::of(Hq) + keys * Chunk<D, 2>::of(Hk),
+                     Chunk<D, 1>::of(Hq) + keys * Chunk<D, 1>::of(Hk)};
+  int best = 0, least = cost[3] > 0 ? cost[3] * (Hq + Hk) / RowWalk<D>::RPW : 1 << 30;
+  for (int i = 0; i < 3; ++i)
+    if (cost[i] > 0 && cost[i] * of[i] <= least) least = cost[i] * of[i], best = 4 >> i;
+  return best;
+}
+
+// Turns of a CTA that walks rows: `most` CTAs at most, the first q_blocks for the queries.
+template <int D>
+unsigned row_blocks(NormRopeLaunch* a, long long most, int max_walk) {
+  const long long tokens = (long long)a->B * a->N, turns = RowWalk<D>::kBlockRows;
+  auto blocks = [&](int which, long long walk) {
+    return (tokens * a->H[which] + walk * turns - 1) / (walk * turns);
+  };
+  long long walk = 1;
+  while (blocks(0, walk) + blocks(1, walk) > most && (max_walk == 0 || walk < max_walk)) walk *= 2;
+  a->walk = (int)walk;
+  a->q_blocks = (unsigned)blocks(0, walk);
+  a->by_n = FastDiv(a->N);
+  a->by_h[0] = FastDiv(a->H[0]);
+  a->by_h[1] = FastDiv(a->H[1]);
+  return (unsigned)(a->q_blocks + blocks(1, walk));
+}
+
+template <int D, bool INTER, int STEPS>
+void launch_chunks(NormRopeLaunch a, cudaStream_t stream) {
+  using I = Chunk<D, STEPS>;
   const unsigned chunks = I::of(a.H[0]) + I::of(a.H[1]), groups = token_groups((long long)a.B * a.N);
   a.walk = forward_walk(groups, chunks, a.sms);
   a.by_n = FastDiv(a.N);
   a.by_chunks = FastDiv(chunks);
-  norm_rope_kernel<D, INTER><<<(groups + a.walk - 1) / a.walk * chunks, kThreads, 0, stream>>>(a);
+  norm_rope_kernel<D, INTER, STEPS><<<(groups + a.walk - 1) / a.walk * chunks, kThreads, 0, stream>>>(a);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_norm_rope_t(NormRopeLaunch a, cudaStream_t stream) {
+  constexpr int kCost[4] = {46, 40, 0, 34};
+  switch (steps_for<D>(a.H[0], a.H[1], 1, kCost)) {
+    case 4:
+      launch_chunks<D, INTER, 4>(a, stream);
+      break;
+    case 2:
+      launch_chunks<D, INTER, 2>(a, stream);
+      break;
+    default:
+      const unsigned blocks = row_blocks<D>(&a, 2ll * kFwdCtas * a.sms, 4);
+      norm_rope_rows_kernel<D, INTER><<<blocks, kThreads, 0, stream>>>(a);
+  }
   return cudaGetLastError();
+}
+
+// Launches, and returns the grid; *cq of every *period rows of partial sums are the queries'.
+template <int D, bool INTER, int STEPS>
+int launch_bwd_chunks(NormRopeLaunch a, int* cq, int* period, cudaStream_t stream) {
+  using I = Chunk<D, STEPS>;
+  *cq = I::of(a.H[0]);
+  *period = *cq + I::of(a.H[1]);
+  const unsigned groups = token_groups((long long)a.B * a.N);
+  const unsigned runs = kNormRopeMaxCtas / *period;  // of tokens, at most: a row of partial sums for each
+  a.walk = (groups + runs - 1) / runs;
+  a.by_n = FastDiv(a.N);
+  a.by_chunks = FastDiv(*period);
+  const int grid = (groups + a.walk - 1) / a.walk * *period;
+  norm_rope_bwd_kernel<D, INTER, STEPS><<<grid, kThreads, 0, stream>>>(a);
+  return grid;
 }
 
 template <int D, bool INTER>
 cudaError_t launch_norm_rope_bwd_t(NormRopeLaunch a, cudaStream_t stream) {
-  using I = Chunk<D, kBwdSteps>;
-  const unsigned cq = I::of(a.H[0]), chunks = cq + I::of(a.H[1]), groups = token_groups((long long)a.B * a.N);
-  const unsigned runs = kNormRopeMaxCtas / chunks;  // of tokens, at most: a row of partial sums for each
-  a.walk = (groups + runs - 1) / runs;
-  a.by_n = FastDiv(a.N);
-  a.by_chunks = FastDiv(chunks);
-  const int grid = (groups + a.walk - 1) / a.walk * chunks;
-  norm_rope_bwd_kernel<D, INTER><<<grid, kThreads, 0, stream>>>(a);
+  constexpr int kCost[4] = {110, 65, 40, 46};
+  int grid, cq, period;
+  switch (steps_for<D>(a.H[0], a.H[1], 1, kCost)) {
+    case 4:
+      grid = launch_bwd_chunks<D, INTER, 4>(a, &cq, &period, stream);
+      break;
+    case 2:
+      grid = launch_bwd_chunks<D, INTER, 2>(a, &cq, &period, stream);
+      break;
+    case 1:
+      grid = launch_bwd_chunks<D, INTER, 1>(a, &cq, &period, stream);
+      break;
+    default:
+      grid = (int)row_blocks<D>(&a, kNormRopeMaxCtas, 0);
+      cq = (int)a.q_blocks;
+      period = grid;
+      norm_rope_rows_bwd_kernel<D, INTER><<<grid, kThreads, 0, stream>>>(a);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.partial == nullptr) return e;
   cudaLaunchConfig_t cfg = {};
@@ -553,15 +778,35 @@ cudaError_t launch_norm_rope_bwd_t(NormRopeLaunch a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), grid, D, (int)cq,
-                            (int)chunks, a.dw[0], a.dw[1]);
+  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), grid, D, cq, period,
+                            a.dw[0], a.dw[1]);
+}
+
+template <int D, bool INTER, int STEPS>
+void launch_append(AppendLaunch a, cudaStream_t stream) {
+  using I = Chunk<D, STEPS>;
+  const unsigned groups = token_groups(a.T), chunks = I::of(a.Hq) + 2 * I::of(a.Hk);
+  a.by_chunks = FastDiv(chunks);
+  // One warp for all of a token's chunks where there are tokens enough to fill
+  // the device (16000 tokens, 4 + 4 heads, d = 128: 34 -> 31 us); few tokens are
+  // spread chunk by chunk.
+  a.span = groups >= 4u * a.sms;
+  paged_append_kernel<D, INTER, STEPS><<<a.span ? groups : groups * chunks, kThreads, 0, stream>>>(a);
 }
 
 template <int D, bool INTER>
-cudaError_t launch_paged_append_t(AppendLaunch a, cudaStream_t stream) {
-  using I = Chunk<D, kFwdSteps>;
-  a.by_chunks = FastDiv(I::of(a.Hq) + 2 * I::of(a.Hk));
-  paged_append_kernel<D, INTER><<<token_groups(a.T) * a.by_chunks.d, kThreads, 0, stream>>>(a);
+cudaError_t launch_paged_append_t(const AppendLaunch& a, cudaStream_t stream) {
+  constexpr int kCost[4] = {100, 78, 62, 0};
+  switch (steps_for<D>(a.Hq, a.Hk, 2, kCost)) {
+    case 4:
+      launch_append<D, INTER, 4>(a, stream);
+      break;
+    case 2:
+      launch_append<D, INTER, 2>(a, stream);
+      break;
+    default:
+      launch_append<D, INTER, 1>(a, stream);
+  }
   return cudaGetLastError();
 }
 

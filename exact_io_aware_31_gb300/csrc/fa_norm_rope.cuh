@@ -48,6 +48,8 @@ struct NormRopeLaunch {
   const int* positions;    // [B, N] or null (n)
   int walk;                // tokens a warp takes
   FastDiv by_n, by_chunks;
+  unsigned q_blocks;       // row by row: CTAs of the queries
+  FastDiv by_h[2];
   // backward: dout is what `out` was, dx is strided
   const void* dout[2];
   HeadRows dx[2];
@@ -67,6 +69,7 @@ struct AppendLaunch {
   const int* kv_lens;      // [S]
   int T, S, Hq, Hk, num_pages, page_log2, max_pages;
   FastDiv by_chunks;
+  int span, sms;
 };
 
 // Heads of a tensor at most, and CTAs of the backward kernel (the rows of its

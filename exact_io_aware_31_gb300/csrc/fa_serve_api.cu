@@ -226,6 +226,7 @@ extern "C" int fa_paged_append(const void* q, const void* k, const void* v, void
   a.num_pages = num_pages;
   while ((1 << a.page_log2) < page_size) ++a.page_log2;
   a.max_pages = max_pages;
+  a.sms = dev.sms;
   return cuda_status(launch_paged_append(a, stream));
 }
 

@@ -129,6 +129,20 @@ def test_backward_into_a_packed_buffer_and_without_weight_gradients():
     assert bool((buf[:, :, Hq + Hk:] == 7.0).all())
 
 
+@pytest.mark.parametrize("H", [(3, 1), (17, 9)])
+def test_no_eps(H):
+    """eps = 0: rows of a warp that belong to no head must not reach the weights' gradients."""
+    g = torch.Generator().manual_seed(12)
+    q, k = (torch.randn(2, h, 7, 64, generator=g).bfloat16().cuda() for h in H)
+    dz = [torch.randn(x.shape, generator=g).bfloat16().cuda() for x in (q, k)]
+    grads = fa.qk_norm_rope_backward(*dz, q, k, eps=0.0)
+    for dx, dw, x, z in zip(grads[:2], grads[2:], (q, k), dz):
+        rx, rw = serve.norm_rope_grad(f64(z), f64(x), None, 0.0, None, None, False)
+        assert np.abs(f64(dx) - rx).max() <= 2 * BF * np.abs(rx).max()
+        assert np.abs(f64(dw) - rw).max() <= 1e-4 * np.abs(rw).max()
+    assert all(bool(t.isfinite().all()) for t in fa.qk_norm_rope(q, k, eps=0.0))
+
+
 def test_positions_outside_the_table():
     q, k, w, kw, ref = setup((1, 4, 2, 6, 64, 64, False, True, "f32", "packed"))
     good = fa.qk_norm_rope(q, k, *w, **kw)

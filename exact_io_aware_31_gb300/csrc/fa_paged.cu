@@ -114,6 +114,11 @@ struct Plan {
 };
 static_assert(sizeof(Plan) <= 192, "plan size");
 
+// Token of a row: row / G for rows up to 256 and G up to 128.  With m = 65536 / G + 1
+// the product is row / G + row * e / (65536 G) for an e of 1 .. G: too little to
+// reach the next integer while row * e < 65536.
+__device__ __forceinline__ int token_of(const PagedParams& p, int row) { return (row * p.g_inverse) >> 16; }
+
 // n / d for positive n: 32 bits where they do (a 64-bit division is a long
 // stretch of code in front of a CTA's first copy).
 __device__ __forceinline__ long long div_long(long long n, long long d) {
@@ -722,14 +727,14 @@ __global__ void __launch_bounds__(384, 1)
       const bool two = form == kTwoTiles, four = form == kFourCopies;
       const int nt = g.j1 - g.j0;
       const int row = four ? lane : r;              // among the query tile's rows
-      const int rtok = row / p.G, rhead = row - rtok * p.G;
+      const int rtok = token_of(p, row), rhead = row - rtok * p.G;
       const int tile0 = two ? t * tt : 0;           // the query tile's first token in the unit
       const int tok = g.tok0 + tile0 + rtok;        // in the sequence
       const int tile_rows = min(tt, g.ntok - tile0) * p.G;
       const bool valid = row < tile_rows;
       const bool busy = four || quarter * 32 < tile_rows;  // any row of this warp
       const int cnt = two ? (t ? nt : tile0_count(w.q, g, sh)) : (nt + 1 - t) / 2;
-      const int jfirst = g.j0 + (two ? 0 : t), jstep = two ? 1 : 2;
+      const int jfirst = g.j0 + (two ? 0 : t), jshift = two ? 0 : 1;  // every second key tile
       const int past = w.q.kv - w.q.qn;
       const int lim = !valid ? -1 : p.causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
       // the tile's first row's: up to it no key tile needs a mask
@@ -744,12 +749,12 @@ __global__ void __launch_bounds__(384, 1)
       }
       // Key tiles [0, free) need no mask, the others come behind them: two loops, so
       // that the first has no masking in it (4% of a long chunk's time).
-      const int free = min(cnt, max(0, ((lim0 + 1) >> 7) - jfirst + jstep - 1) / jstep);
+      const int free = min(cnt, max(0, ((lim0 + 1) >> 7) - jfirst + jshift) >> jshift);
       auto tiles = [&](auto nc, auto masked, int c0, int from, int to) {
         for (int i = from; i < to && ok; ++i) {
           if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
           ++scnt;
-          tile(nc, masked, c0, i == 0, lim - (jfirst + i * jstep) * kTileRows - c0);
+          tile(nc, masked, c0, i == 0, lim - (jfirst + (i << jshift)) * kTileRows - c0);
           mbar_arrive(&B.p_full[t]);
         }
       };
@@ -836,7 +841,7 @@ __global__ void __launch_bounds__(384, 1)
               o.x = fmaf(wt, x.x, o.x), o.y = fmaf(wt, x.y, o.y), o.z = fmaf(wt, x.z, o.z), o.w = fmaf(wt, x.w, o.w);
             }
             if (whole) {
-              const int qt = q_row / p.G;
+              const int qt = token_of(p, q_row);
               const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.at.hk * p.G + (q_row - qt * p.G);
               const float inv = l == 0.f ? 0.f : 1.f / l;
               reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D)[c] =
@@ -1050,7 +1055,7 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
     }
     if (n0 + lane / kLanes >= rows) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int tok = n / p.G;
+    const int tok = token_of(p, n);
     const size_t row = (size_t)(h.y + tok) * (p.Hk * p.G) + h.w * p.G + (n - tok * p.G);
     reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[l8] =
         make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),

@@ -16,6 +16,7 @@ struct PagedParams {
   const int* kv_lens;     // [S]
   int T, S, Hk, G;        // G query heads a key head
   int num_pages, page_log2, max_pages;
+  int g_inverse;          // 65536 / G + 1
   int causal;
   float c2;               // scale * log2(e)
   int tile_tokens;        // tokens of a 128-row query tile: G * tile_tokens <= 128

@@ -329,6 +329,7 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   p.S = S;
   p.Hk = Hk;
   p.G = G;
+  p.g_inverse = 65536 / G + 1;
   p.num_pages = num_pages;
   p.page_log2 = 0;
   while ((1 << p.page_log2) < page_size) ++p.page_log2;

@@ -409,6 +409,15 @@ def _flat(t, name, shape, dtype, device):
     return t.data_ptr()
 
 
+def _room(workspace, device):
+    """Address and bytes of a workspace (None: no room)."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", workspace.shape, workspace.dtype, device)
+    return workspace.data_ptr(), workspace.nbytes
+
+
 def _shape(t, name, n):
     """Shape of a tensor of n dimensions."""
     shape = getattr(t, "shape", ())
@@ -503,7 +512,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
         dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in "qk")
         if workspace is None:
             workspace = torch.empty(fa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
-    ws, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    ws, wbytes = _room(workspace, dev)
     st = load_library().fa_qk_norm_rope_bwd(dqo, dko, q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                             None if dqw is None else dqw.data_ptr(),
                                             None if dkw is None else dkw.data_ptr(), B, Hq, Hk, N, d, *sq, *sk, *sdq,
@@ -592,10 +601,11 @@ def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=No
         if need is None:
             need = _paged_workspace[dev, d] = fa_fwd_paged_workspace_size(d)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws, wbytes = _room(workspace, dev)
     st = load_library().fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
                                      lse.data_ptr(), *meta, T, S, Hq, Hk, d, num_pages, page_size, max_pages, *sq,
                                      *steps, d ** -0.5 if scale is None else scale, 1 if causal else 0, max_q,
-                                     workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(dev))
+                                     ws, wbytes, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged")
     return out, lse

@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(384, 1)
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (part[i].x == -INFINITY) continue;  // saw no key
+              if (part[i].y == 0.f) continue;  // saw no key (a row of NaN has a maximum of -inf, too)
               const float wt = ex2(part[i].x - m);
               const float4 x = xs[(i * 8 + rr) * kChunks + (c ^ rr)];
               l = fmaf(wt, part[i].y, l);
@@ -879,8 +879,8 @@ __global__ void __launch_bounds__(384, 1)
           ++fills;
           const float2 other = ml[(1 - t) * 128 + r];
           m_out = fmaxf(m_run, other.x);
-          w0 = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_out);
-          w1 = (other.x == -INFINITY) ? 0.f : ex2(other.x - m_out);
+          w0 = l_run == 0.f ? 0.f : ex2(m_run - m_out);
+          w1 = other.y == 0.f ? 0.f : ex2(other.x - m_out);
           l_out = l_run * w0 + other.y * w1;
         }
         if (busy && (two || merge || t == 0)) {  // (a single key tile: half 0 alone)
@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         if (i + k >= parts) continue;
-        const float w = x[k].x == -INFINITY ? 0.f : ex2(x[k].x - m);
+        const float w = x[k].y == 0.f ? 0.f : ex2(x[k].x - m);
         l = fmaf(w, x[k].y, l);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

@@ -109,6 +109,23 @@ def test_scales(case, scale):
     check(o, lse, ref)
 
 
+@pytest.mark.parametrize("hint", [None, 0, 1])
+@pytest.mark.parametrize("case", CASES[1:9] + CASES[11:17], ids=IDS[1:9] + IDS[11:17])
+def test_a_query_of_nan_is_seen(case, hint):
+    """Rows whose query is NaN are NaN (not zero, as rows without a key are), the others as before."""
+    q, pages, table, cu, lens = batch(case)
+    o, lse, reach = reference(q, pages, table, cu, lens, 0.11, case[7])
+    poisoned = torch.zeros(q.shape[:2], dtype=torch.bool)
+    poisoned[::3, ::2] = True
+    q.masked_fill_(poisoned[..., None].cuda(), float("nan"))
+    lse = np.where(poisoned.numpy() & np.isfinite(lse), np.nan, lse)
+    got, got_lse = fa.paged_forward(q, *pages, table.cuda(), cu.cuda(), lens.cuda(), scale=0.11, causal=case[7],
+                                    max_q=max(case[0]) if hint is None else hint)
+    assert status() == fa.FA_OK
+    check(got, got_lse, (o, lse, reach))
+    assert np.isnan(f64(got)[np.isnan(lse)]).all() and np.isnan(f64(got_lse)[np.isnan(lse)]).all()
+
+
 @pytest.mark.parametrize("fill", [float("nan"), float("inf")])
 @pytest.mark.parametrize("case", CASES[3:8] + CASES[15:19], ids=IDS[3:8] + IDS[15:19])
 def test_what_lies_behind_a_sequence_does_not_matter(case, fill):
@@ -329,3 +346,28 @@ def test_a_served_sequence_equals_the_whole_attention(Hq, Hk, d, page, inter):
                                     d ** -0.5, True)
         check(torch.cat(out[s]), torch.cat(lses[s]), ref)
         check(o[0].transpose(0, 1), lse[0].T, ref)
+
+
+def test_helpers_refuse_on_the_host():
+    """What would be read or written at a wrong address is refused before any launch."""
+    case = CASES[3]
+    q, pages, table, cu, lens = batch(case)
+    good = dict(q=q, k_pages=pages[0], v_pages=pages[1], page_table=table.cuda(), cu_seqlens=cu.cuda(), kv_lens=lens.cuda())
+    fa.paged_forward(**good)
+    room = torch.empty(fa.fa_fwd_paged_workspace_size(case[4]), dtype=torch.uint8)
+    for bad in (dict(workspace=room), dict(page_table=table), dict(kv_lens=lens.cuda().long()), dict(kv_lens=lens.cuda()[:-1]),
+                dict(cu_seqlens=cu.cuda()[:-1]), dict(page_table=table.cuda().t()), dict(q=q.float()), dict(q=q[..., :64]),
+                dict(v_pages=pages[1].cpu()), dict(v_pages=pages[1][:, :1]), dict(out=torch.empty_like(q).float()),
+                dict(out=torch.empty(q.shape, dtype=q.dtype)), dict(lse=torch.empty(q.shape[:2], device="cuda").t()),
+                dict(q=q[0])):
+        with pytest.raises(ValueError):
+            fa.paged_forward(**good | bad)
+    for bad in (dict(workspace=room.cuda()[:-1].clone()), dict(max_q=-1), dict(q=q[:, :3])):
+        with pytest.raises(fa.FaError):
+            fa.paged_forward(**good | bad)
+    x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)), dict(q_weight=torch.ones(64)),
+                dict(grads=(x.cpu(), x)), dict(positions=torch.zeros(1, 8, device="cuda")), dict(rope=torch.zeros(8, 64))):
+        with pytest.raises(ValueError):
+            fa.qk_norm_rope_backward(x, x, x, x, **bad)
+    assert status() == fa.FA_OK

@@ -739,6 +739,7 @@ int launch_bwd_chunks(NormRopeLaunch a, int* cq, int* period, cudaStream_t strea
   *period = *cq + I::of(a.H[1]);
   const unsigned groups = token_groups((long long)a.B * a.N);
   const unsigned runs = kNormRopeMaxCtas / *period;  // of tokens, at most: a row of partial sums for each
+  static_assert(2 * kNormRopeMaxHeads / I::kRows <= kNormRopeMaxCtas, "a run at least");
   a.walk = (groups + runs - 1) / runs;
   a.by_n = FastDiv(a.N);
   a.by_chunks = FastDiv(*period);

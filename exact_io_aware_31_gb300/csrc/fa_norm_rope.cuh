@@ -72,9 +72,8 @@ struct AppendLaunch {
   int span, sms;
 };
 
-// Heads of a tensor at most, and CTAs of the backward kernel (the rows of its
-// partial sums): it takes one for every chunk of at least four heads, and
-// multiples of that up to three an SM.
+// Heads of a tensor at most, and CTAs of the backward kernel at most (the rows of
+// its partial sums): at least one for every chunk of heads of either tensor.
 constexpr int kNormRopeMaxHeads = 2048;
 constexpr int kNormRopeMaxCtas = 2048;
 

@@ -360,7 +360,9 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  *             graph's must live as long as the graph.
  *
  * A row that sees no key is zero with lse = -infinity.  What a page holds
- * behind its sequence's end does not matter (NaN included).  Keys of a page
+ * behind its sequence's end does not matter (NaN included); within it values
+ * must be finite, as in fa_fwd: a masked key's probability is zero, and 0 * NaN
+ * is NaN for the rows that share its tile.  Keys of a page
  * outside the pool count as zeros with zero values, lengths outside their
  * range are cut to it; both record FA_ERR_DEVICE_INDEX.  Two launches.  Results
  * are the same bits on every run.

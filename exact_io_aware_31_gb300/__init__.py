@@ -379,34 +379,47 @@ def _elsewhere(first, stream):
     """Where a helper must not run as it is called: None, or the context that makes the first tensor's device and the
     given stream current (what is allocated there belongs to the stream that uses it)."""
     import torch
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+    device = first.get_device() if isinstance(first, torch.Tensor) else -1
+    if device < 0:
         raise ValueError("the first argument must be a CUDA tensor")
     if stream is not None:
         if stream.device != first.device:
             raise ValueError(f"the stream is on {stream.device}, the first tensor on {first.device}")
         return torch.cuda.stream(stream)
-    device = first.get_device()
-    return None if device == torch.cuda.current_device() else torch.cuda.device(device)
+    return None if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+# The checks below run before every call, so they are short: a serving step of a few tokens takes the device no longer
+# than its call takes the host.
 
 
 def _rows(t, name, shape, dtype, device):
-    """Check rows of any layout; their strides without the last.  Where a size is 1 a stride means nothing, and any
-    valid one will do."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or t.stride(-1) != 1:
+    """Check rows of any layout; their strides without the last (where a size is 1 a stride may be anything)."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device or (steps := t.stride())[-1] != 1):
         _refuse(t, name, shape, dtype, device)
-    st = t.stride()
-    if 1 in shape:
-        return [s if n > 1 else shape[-1] for s, n in zip(st[:-1], shape[:-1])]
-    return st[:-1]
+    return steps[:-1]
 
 
 def _flat(t, name, shape, dtype, device):
     """Check a contiguous tensor (None passes); its address."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         _refuse(t, name, shape, dtype, device)
     return t.data_ptr()
+
+
+_rooms = {}
+
+
+def _room_for(size, device, d):
+    """Workspace bytes that ``size(d)`` gives on the current device, asked for once."""
+    need = _rooms.get((size, device, d))
+    if need is None:
+        need = size(d)
+        if need:  # (0: refused by the call itself)
+            _rooms[size, device, d] = need
+    return need
 
 
 def _room(workspace, device):
@@ -468,7 +481,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, 
     args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
     pos = _flat(positions, "positions", (B, N), torch.int32, dev)
     if out is None:
-        q_out, k_out = (torch.empty((B, h, N, d), dtype=bf16, device=q.device) for h in (Hq, Hk))
+        q_out = torch.empty(B, Hq, N, d, dtype=bf16, device=q.device)
+        k_out = torch.empty(B, Hk, N, d, dtype=bf16, device=q.device)
     else:
         q_out, k_out = out
         _flat(q_out, "q_out", (B, Hq, N, d), bf16, dev)
@@ -501,17 +515,19 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ro
     args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
     pos = _flat(positions, "positions", (B, N), torch.int32, dev)
     if grads is None:
-        dq, dk = (torch.empty_strided((B, h, N, d), (N * h * d, d, h * d, 1), dtype=bf16, device=q.device)
-                  for h in (Hq, Hk))
         sdq, sdk = (N * Hq * d, d, Hq * d), (N * Hk * d, d, Hk * d)
+        dq = torch.empty_strided((B, Hq, N, d), (*sdq, 1), dtype=bf16, device=q.device)
+        dk = torch.empty_strided((B, Hk, N, d), (*sdk, 1), dtype=bf16, device=q.device)
     else:
         dq, dk = grads
         sdq, sdk = _rows(dq, "dq", (B, Hq, N, d), bf16, dev), _rows(dk, "dk", (B, Hk, N, d), bf16, dev)
     dqw = dkw = None
     if norm and weight_grads:
-        dqw, dkw = (torch.empty(d, dtype=torch.float32, device=q.device) for _ in "qk")
+        dqw = torch.empty(d, dtype=torch.float32, device=q.device)
+        dkw = torch.empty(d, dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(fa_qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(_room_for(fa_qk_norm_rope_bwd_workspace_size, dev, d), dtype=torch.uint8,
+                                    device=q.device)
     ws, wbytes = _room(workspace, dev)
     st = load_library().fa_qk_norm_rope_bwd(dqo, dko, q.data_ptr(), k.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                             None if dqw is None else dqw.data_ptr(),
@@ -557,7 +573,7 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
                   _rows(v, "v", (T, Hk, d), bf16, dev))
     args = _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, dev)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
+        out = torch.empty(T, Hq, d, dtype=bf16, device=q.device)
     else:
         _flat(out, "out", (T, Hq, d), bf16, dev)
     st = load_library().fa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), k_pages.data_ptr(),
@@ -566,9 +582,6 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
     if st != FA_OK:
         raise FaError(st, "fa_paged_append")
     return out
-
-
-_paged_workspace = {}  # (device, d) -> bytes
 
 
 def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,
@@ -589,18 +602,15 @@ def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=No
                                                                       d, dev)
     sq = _rows(q, "q", (T, Hq, d), bf16, dev)
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=bf16, device=q.device)
+        out = torch.empty(T, Hq, d, dtype=bf16, device=q.device)
     else:
         _flat(out, "out", (T, Hq, d), bf16, dev)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     else:
         _flat(lse, "lse", (T, Hq), torch.float32, dev)
     if workspace is None:
-        need = _paged_workspace.get((dev, d))
-        if need is None:
-            need = _paged_workspace[dev, d] = fa_fwd_paged_workspace_size(d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_room_for(fa_fwd_paged_workspace_size, dev, d), dtype=torch.uint8, device=q.device)
     ws, wbytes = _room(workspace, dev)
     st = load_library().fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
                                      lse.data_ptr(), *meta, T, S, Hq, Hk, d, num_pages, page_size, max_pages, *sq,

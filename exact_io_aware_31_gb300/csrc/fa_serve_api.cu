@@ -20,11 +20,23 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 bool flag(int v) { return v == 0 || v == 1; }
 
-// An input's stride: 16-byte steps, zero allowed (a broadcast dimension).
-bool stride_in(long long s) { return s >= 0 && s % 8 == 0; }
+// Strides are 16-byte steps.  Where a size is 1 the stride means nothing: it is
+// not looked at, and none is taken.
+//
+// An input's stride: zero allowed (a broadcast dimension).
+bool stride_in(long long* s, long long size) {
+  if (size <= 1) *s = 0;
+  return *s >= 0 && *s % 8 == 0;
+}
 
 // An output's: rows of d elements must not overlap.
-bool stride_out(long long s, long long size, int d) { return stride_in(s) && (size <= 1 || s >= d); }
+bool stride_out(long long* s, long long size, int d) { return stride_in(s, size) && (size <= 1 || *s >= d); }
+
+// One that is written into a tensor map: positive even where it means nothing.
+bool stride_map(long long* s, long long size, int d, long long below) {
+  if (size <= 1) *s = d;
+  return *s >= d && *s % 8 == 0 && *s < below;
+}
 
 int cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return FA_OK;
@@ -80,8 +92,8 @@ extern "C" int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* 
   if (st != FA_OK) return st;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned4(positions))
     return FA_ERR_INVALID_ARG;
-  if (!stride_in(q_stride_b) || !stride_in(q_stride_h) || !stride_in(q_stride_n) || !stride_in(k_stride_b) ||
-      !stride_in(k_stride_h) || !stride_in(k_stride_n))
+  if (!stride_in(&q_stride_b, B) || !stride_in(&q_stride_h, Hq) || !stride_in(&q_stride_n, N) ||
+      !stride_in(&k_stride_b, B) || !stride_in(&k_stride_h, Hk) || !stride_in(&k_stride_n, N))
     return FA_ERR_INVALID_ARG;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != FA_OK) return st;
@@ -122,11 +134,11 @@ extern "C" int fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const
   if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(q) ||
       !aligned16(k) || !aligned4(positions) || !aligned4(dq_weight) || !aligned4(dk_weight))
     return FA_ERR_INVALID_ARG;
-  if (!stride_in(q_stride_b) || !stride_in(q_stride_h) || !stride_in(q_stride_n) || !stride_in(k_stride_b) ||
-      !stride_in(k_stride_h) || !stride_in(k_stride_n))
+  if (!stride_in(&q_stride_b, B) || !stride_in(&q_stride_h, Hq) || !stride_in(&q_stride_n, N) ||
+      !stride_in(&k_stride_b, B) || !stride_in(&k_stride_h, Hk) || !stride_in(&k_stride_n, N))
     return FA_ERR_INVALID_ARG;
-  if (!stride_out(dq_stride_b, B, d) || !stride_out(dq_stride_h, Hq, d) || !stride_out(dq_stride_n, N, d) ||
-      !stride_out(dk_stride_b, B, d) || !stride_out(dk_stride_h, Hk, d) || !stride_out(dk_stride_n, N, d))
+  if (!stride_out(&dq_stride_b, B, d) || !stride_out(&dq_stride_h, Hq, d) || !stride_out(&dq_stride_n, N, d) ||
+      !stride_out(&dk_stride_b, B, d) || !stride_out(&dk_stride_h, Hk, d) || !stride_out(&dk_stride_n, N, d))
     return FA_ERR_INVALID_ARG;
   const bool weights = dq_weight != nullptr || dk_weight != nullptr;
   if (weights && !norm) return FA_ERR_INVALID_ARG;
@@ -159,19 +171,18 @@ namespace {
 
 // The cache arguments that every paged call shares (T, S >= 1 here).
 int check_cache(const void* k_pages, const void* v_pages, const int* page_table, const int* cu_seqlens,
-                const int* kv_lens, int Hk, int d, int num_pages, int page_size, int max_pages, const long long* sp,
-                const long long* sh, const long long* sr) {
+                const int* kv_lens, int Hk, int d, int num_pages, int page_size, int max_pages, long long* sp,
+                long long* sh, long long* sr) {
   if (num_pages < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
   if ((long long)max_pages * page_size > (1 << 30)) return FA_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
   if (!page_table || !cu_seqlens || !kv_lens || !aligned4(page_table) || !aligned4(cu_seqlens) || !aligned4(kv_lens))
     return FA_ERR_INVALID_ARG;
-  for (int i = 0; i < 2; ++i) {
-    // strides are written into a tensor map, so they are positive even where the size is 1
-    if (sp[i] < d || sh[i] < d || sr[i] < d || sp[i] % 8 || sh[i] % 8 || sr[i] % 8) return FA_ERR_INVALID_ARG;
-    if (sp[i] >= (1ll << 38) || sh[i] >= (1ll << 38) || sr[i] >= (1ll << 38)) return FA_ERR_INVALID_ARG;
-  }
+  for (int i = 0; i < 2; ++i)
+    if (!stride_map(&sp[i], num_pages, d, 1ll << 38) || !stride_map(&sh[i], Hk, d, 1ll << 38) ||
+        !stride_map(&sr[i], page_size, d, 1ll << 38))
+      return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -194,11 +205,11 @@ extern "C" int fa_paged_append(const void* q, const void* k, const void* v, void
   if (st != FA_OK) return st;
   if (T == 0 || S == 0) return FA_OK;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return FA_ERR_INVALID_ARG;
-  if (!stride_in(q_stride_t) || !stride_in(q_stride_h) || !stride_in(k_stride_t) || !stride_in(k_stride_h) ||
-      !stride_in(v_stride_t) || !stride_in(v_stride_h))
+  if (!stride_in(&q_stride_t, T) || !stride_in(&q_stride_h, Hq) || !stride_in(&k_stride_t, T) ||
+      !stride_in(&k_stride_h, Hk) || !stride_in(&v_stride_t, T) || !stride_in(&v_stride_h, Hk))
     return FA_ERR_INVALID_ARG;
-  const long long sp[2] = {kp_stride_p, vp_stride_p}, sh[2] = {kp_stride_h, vp_stride_h},
-                  sr[2] = {kp_stride_r, vp_stride_r};
+  long long sp[2] = {kp_stride_p, vp_stride_p}, sh[2] = {kp_stride_h, vp_stride_h},
+            sr[2] = {kp_stride_r, vp_stride_r};
   st = check_cache(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d, num_pages, page_size, max_pages, sp, sh,
                    sr);
   if (st != FA_OK) return st;
@@ -299,10 +310,10 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   if ((d != 64 && d != 128) || G > 128) return FA_ERR_UNSUPPORTED;
   if (T == 0 || S == 0) return FA_OK;
   if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
-  for (long long st : {q_stride_t, q_stride_h})  // written into a tensor map: positive
-    if (st < d || st % 8 != 0 || st >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-  const long long sp[2] = {kp_stride_p, vp_stride_p}, sh[2] = {kp_stride_h, vp_stride_h},
-                  sr[2] = {kp_stride_r, vp_stride_r};
+  if (!stride_map(&q_stride_t, T, d, 1ll << 31) || !stride_map(&q_stride_h, Hq, d, 1ll << 31))
+    return FA_ERR_INVALID_ARG;
+  long long sp[2] = {kp_stride_p, vp_stride_p}, sh[2] = {kp_stride_h, vp_stride_h},
+            sr[2] = {kp_stride_r, vp_stride_r};
   int st = check_cache(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d, num_pages, page_size, max_pages, sp,
                        sh, sr);
   if (st != FA_OK) return st;

@@ -244,7 +244,8 @@ int fa_bwd_dq_convert(void* dq, int B, int H, int N, int d, float scale, const v
  *   q, k      in   bf16 [B, Hq, N, d] and [B, Hk, N, d] of any strides: element
  *                  (b, h, n, c) at b*stride_b + h*stride_h + n*stride_n + c.
  *                  Strides are in elements, >= 0 and multiples of 8 (a
- *                  token-major projection is stride_n = its row, stride_h = d).
+ *                  token-major projection is stride_n = its row, stride_h = d);
+ *                  where a size is 1 the stride means nothing and may be anything
  *   q_out, k_out   out  contiguous [B, Hq, N, d], [B, Hk, N, d] bf16
  *   q_weight, k_weight  in  [d] norm weights shared by the heads, bf16
  *                  (weights_f32 = 0) or fp32 (1); NULL means ones
@@ -301,7 +302,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *  A cache is a pool of num_pages pages of page_size keys each, for all Hk key
  *  heads: element (page, h, row, c) of k_pages at page*stride_p + h*stride_h +
  *  row*stride_r + c (v_pages likewise, with strides of its own).  Strides are
- *  in elements, multiples of 8, > 0; both head-major ([pages, Hk, page_size, d])
+ *  in elements, multiples of 8, >= d (of no meaning where the size is 1); both
+ *  head-major ([pages, Hk, page_size, d])
  *  and token-major ([pages, page_size, Hk, d]) pools are covered.  page_size is
  *  a power of two, 16 to 65536.
  *  page_table [S, max_pages] int32 (contiguous): key j of sequence s is row

@@ -348,6 +348,32 @@ def test_a_served_sequence_equals_the_whole_attention(Hq, Hk, d, page, inter):
         check(o[0].transpose(0, 1), lse[0].T, ref)
 
 
+def test_strides_of_single_elements_mean_nothing():
+    """A dimension of size 1 may come with any stride: one page, one key head, one token, one row."""
+    g = torch.Generator().manual_seed(31)
+    d, page = 64, 16
+    new = lambda *n: torch.randn(n, generator=g).bfloat16().cuda()
+    q, k, v, kp, vp = new(1, 4, d), new(1, 1, d), new(1, 1, d), new(1, 1, page, d), new(1, 1, page, d)
+    rope = fa.rope_table(page, d)
+    table, cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0]], [0, 1], [9]))
+    odd = lambda t, *steps: torch.as_strided(t, t.shape, steps)
+    kp2, vp2 = kp.clone(), vp.clone()
+    plain = fa.paged_append(q, k, v, kp, vp, table, cu, lens, rope=rope)
+    strange = fa.paged_append(odd(q, 3, d, 1), odd(k, 5, 0, 1), odd(v, 0, 1, 1), odd(kp2, 1, 3, d, 1), odd(vp2, 0, 0, d, 1),
+                              table, cu, lens, rope=rope)
+    assert torch.equal(plain, strange) and torch.equal(kp, kp2) and torch.equal(vp, vp2)
+    for a, b in zip(fa.paged_forward(plain, kp, vp, table, cu, lens),
+                    fa.paged_forward(odd(plain, 7, d, 1), odd(kp, 1, 3, d, 1), odd(vp, 0, 0, d, 1), table, cu, lens)):
+        assert torch.equal(a, b)
+    x, y = new(1, 2, 8, d), new(1, 1, 8, d)
+    for a, b in zip(fa.qk_norm_rope(x, y), fa.qk_norm_rope(odd(x, 9, 8 * d, d, 1), odd(y, 1, 2, d, 1))):
+        assert torch.equal(a, b)
+    for a, b in zip(fa.qk_norm_rope_backward(x, y, x, y),
+                    fa.qk_norm_rope_backward(x, y, odd(x, 9, 8 * d, d, 1), odd(y, 1, 2, d, 1))):
+        assert torch.equal(a, b)
+    assert status() == fa.FA_OK
+
+
 def test_helpers_refuse_on_the_host():
     """What would be read or written at a wrong address is refused before any launch."""
     case = CASES[3]

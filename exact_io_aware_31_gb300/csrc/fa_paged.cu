@@ -241,6 +241,28 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// mbar_wait_warp in fewer instructions.  The kernels of short chunks pass through
+// all of their code for every small unit, and wait for instructions a good part of
+// their time: what is shorter there is faster (64 sequences of 8 tokens, d = 64:
+// 43.5 -> 42.7 us); the softmax of long chunks came out slower with it (468 -> 480).
+template <bool SHORT>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status) {
+  if constexpr (!SHORT) return mbar_wait_warp(bar, parity, status);
+  const uint32_t a = smem_addr(bar);
+  uint32_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_test(a, parity))) return true;
+    if (n & 31) continue;
+    const uint32_t now = (uint32_t)(global_ns() >> 10);  // (about a microsecond)
+    if (n == 0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > (uint32_t)(kWaitLimitNs >> 10))) {
+      atomicExch(status, kDevTimeout);
+      return false;
+    }
+  }
+}
+
 template <int D, bool SHORT>
 __global__ void __launch_bounds__(384, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q4,
@@ -334,8 +356,8 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t turn = 0, kv_it = 0;
       bool ok = true, lost = false;
       auto wait_q = [&](int b) {
-        if (merged[b]) return mbar_wait_warp(&B.x_done[b], (by_merge[b] - 1) & 1, status);
-        return by_mma[b] == 0 || mbar_wait_warp(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
+        if (merged[b]) return wait_warp<SHORT>(&B.x_done[b], (by_merge[b] - 1) & 1, status);
+        return by_mma[b] == 0 || wait_warp<SHORT>(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
       };
       while (ok && walk_get(work, w, plan->at[1], sh, g)) {
         const Form form = form_of(g);
@@ -352,7 +374,9 @@ __global__ void __launch_bounds__(384, 1)
           if (lane == 0) {
             uint8_t* dst = sm + C::kOffQ + b * C::kTileBytes;
             mbar_expect_tx(&B.q_full[b], copies * box * C::kBlocks);
+#pragma unroll 1
             for (int kb = 0; kb < C::kBlocks; ++kb)
+#pragma unroll 1
               for (int c = 0; c < copies; ++c)
                 tma_load_4d(dst + kb * kSwzBlockBytes + c * (kSwzBlockBytes / 4), map, &B.q_full[b], 64 * kb, 0, w.at.hk,
                             row);
@@ -397,7 +421,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           const int ks = kv_it % C::kKSlots, vs = kv_it % C::kVSlots;
           const uint32_t kph = (kv_it / C::kKSlots) & 1, vph = (kv_it / C::kVSlots) & 1;
-          if (!(ok = mbar_wait_warp(&B.k_empty[ks], kph ^ 1, status))) break;
+          if (!(ok = wait_warp<SHORT>(&B.k_empty[ks], kph ^ 1, status))) break;
           if (lane == 0) mbar_expect_tx(&B.k_full[ks], boxes * box_bytes * C::kBlocks);
           __syncwarp();
           if (lane < boxes) {
@@ -406,9 +430,9 @@ __global__ void __launch_bounds__(384, 1)
               tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[ks], 64 * kb, row, w.at.hk, page);
           }
           __syncwarp();
-          if (!(ok = mbar_wait_warp(&B.v_empty[vs], vph ^ 1, status))) {
+          if (!(ok = wait_warp<SHORT>(&B.v_empty[vs], vph ^ 1, status))) {
             // the K copy of this tile is in flight: it lands before the block ends
-            mbar_wait_warp(&B.k_full[ks], kph, status);
+            wait_warp<SHORT>(&B.k_full[ks], kph, status);
             break;
           }
           if (lane == 0) mbar_expect_tx(&B.v_full[vs], boxes * box_bytes * C::kBlocks);
@@ -428,11 +452,11 @@ __global__ void __launch_bounds__(384, 1)
       // Drain: every copy this warp started lands before the block ends.
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        if (q_uses[b] > 0) mbar_wait_warp(&B.q_full[b], (q_uses[b] - 1) & 1, status);
+        if (q_uses[b] > 0) wait_warp<SHORT>(&B.q_full[b], (q_uses[b] - 1) & 1, status);
       for (uint32_t i = kv_it > (uint32_t)C::kKSlots ? kv_it - C::kKSlots : 0; i < kv_it; ++i)
-        mbar_wait_warp(&B.k_full[i % C::kKSlots], (i / C::kKSlots) & 1, status);
+        wait_warp<SHORT>(&B.k_full[i % C::kKSlots], (i / C::kKSlots) & 1, status);
       for (uint32_t i = kv_it > (uint32_t)C::kVSlots ? kv_it - C::kVSlots : 0; i < kv_it; ++i)
-        mbar_wait_warp(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
+        wait_warp<SHORT>(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer --
       Walk w = start();
@@ -447,14 +471,14 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       auto issue_s = [&](int t, uint32_t qa, uint32_t it) {
         const uint32_t ka = k_s + (it % C::kKSlots) * C::kTileBytes;
-#pragma unroll
+#pragma unroll(SHORT ? 1 : C::kBlocks)
         for (int kb = 0; kb < C::kBlocks; ++kb)
           mma_ss_run_w<4, 2, 2>(tbase + C::kColS + 128 * t, sdesc(qa + kb * kSwzBlockBytes, 16, 1024),
                                 sdesc(ka + kb * kSwzBlockBytes, 16, 1024), idS, kb > 0);
         mma_commit_w(&B.s_full[t]);
       };
       auto wait_k = [&](uint32_t it) {
-        if (!mbar_wait_warp(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
+        if (!wait_warp<SHORT>(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
         tc_fence_after();
         return true;
       };
@@ -482,15 +506,15 @@ __global__ void __launch_bounds__(384, 1)
           if (i == tail) {
             const uint32_t parity = (clears >> st) & 1;
             clears ^= 1u << st;
-            return mbar_wait_warp(&B.v_clear[st], parity, status);
+            return wait_warp<SHORT>(&B.v_clear[st], parity, status);
           }
-          return mbar_wait_warp(&B.v_full[st], (it / C::kVSlots) & 1, status);
+          return wait_warp<SHORT>(&B.v_full[st], (it / C::kVSlots) & 1, status);
         };
         if (form != kTwoTiles) {
           const int b = turn & 1;
           ++turn;
           const uint32_t qa = q_s + b * C::kTileBytes;
-          ok = mbar_wait_warp(&B.q_full[b], (b ? q_uses[1] : q_uses[0]) & 1, status);
+          ok = wait_warp<SHORT>(&B.q_full[b], (b ? q_uses[1] : q_uses[0]) & 1, status);
           if (b)
             ++q_uses[1];
           else
@@ -505,7 +529,7 @@ __global__ void __launch_bounds__(384, 1)
             const int t = i & 1;
             const bool halves = !SHORT && form == kOneTile;
             if (halves) {
-              ok = mbar_wait_warp(&B.p_half[t], (t ? hcnt[1] : hcnt[0]) & 1, status);
+              ok = wait_warp<SHORT>(&B.p_half[t], (t ? hcnt[1] : hcnt[0]) & 1, status);
               if (t)
                 ++hcnt[1];
               else
@@ -514,7 +538,7 @@ __global__ void __launch_bounds__(384, 1)
               tc_fence_after();
               issue_pv_half(t, kv_it + i, 0, i >= 2);
             }
-            ok = mbar_wait_warp(&B.p_full[t], (t ? pcnt[1] : pcnt[0]) & 1, status);
+            ok = wait_warp<SHORT>(&B.p_full[t], (t ? pcnt[1] : pcnt[0]) & 1, status);
             if (t)
               ++pcnt[1];
             else
@@ -539,7 +563,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || cnt[t] == 0) continue;
-            ok = mbar_wait_warp(&B.q_full[t], q_uses[t] & 1, status);
+            ok = wait_warp<SHORT>(&B.q_full[t], q_uses[t] & 1, status);
             ++q_uses[t];
           }
           if (ok) ok = wait_k(kv_it);
@@ -557,7 +581,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (!ok || i >= cnt[t]) continue;
-              ok = mbar_wait_warp(&B.p_half[t], hcnt[t] & 1, status);
+              ok = wait_warp<SHORT>(&B.p_half[t], hcnt[t] & 1, status);
               ++hcnt[t];
               if (ok && !v_ready) {
                 ok = wait_v(i);
@@ -566,7 +590,7 @@ __global__ void __launch_bounds__(384, 1)
               if (!ok) break;
               tc_fence_after();
               issue_pv_half(t, kv_it + i, 0, i > 0);
-              ok = mbar_wait_warp(&B.p_full[t], pcnt[t] & 1, status);
+              ok = wait_warp<SHORT>(&B.p_full[t], pcnt[t] & 1, status);
               ++pcnt[t];
               if (!ok) break;
               tc_fence_after();
@@ -592,7 +616,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) *abort_flag = 1;
       mma_commit_w(B.mma_done);
-      mbar_wait_warp(B.mma_done, 0, status);
+      wait_warp<SHORT>(B.mma_done, 0, status);
     } else if (warp == 10) {
       // ------------------------------------------- rows behind a sequence's end --
       // Follows every V tile (a parity wait must not run ahead of the ring, nor
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(384, 1)
         const int last = last_tile(w.q.kv), used = w.q.kv - (last << 7);
         for (int j = g.j0; j < g.j1; ++j, ++kv_it) {
           const int st = kv_it % C::kVSlots;
-          if (!(ok = mbar_wait_warp(&B.v_full[st], (kv_it / C::kVSlots) & 1, status))) break;
+          if (!(ok = wait_warp<SHORT>(&B.v_full[st], (kv_it / C::kVSlots) & 1, status))) break;
           if (j == last && used < kTileRows) {
             for (int kb = 0; kb < C::kBlocks; ++kb) {
               uint4* rows = reinterpret_cast<uint4*>(sm + C::kOffV + st * C::kTileBytes + kb * kSwzBlockBytes);
@@ -744,7 +768,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!SHORT && cnt > 0 && guard) {
         // both halves must have read that O before P V overwrites it
         const int b = ~turn & 1;  // that unit's buffer: the one in front of the next
-        if (!(ok = mbar_wait_warp(&B.x_done[b], ((b ? x_uses[1] : x_uses[0]) - 1) & 1, status))) break;
+        if (!(ok = wait_warp<SHORT>(&B.x_done[b], ((b ? x_uses[1] : x_uses[0]) - 1) & 1, status))) break;
         guard = false;
       }
       // Key tiles [0, free) need no mask, the others come behind them: two loops, so
@@ -752,7 +776,7 @@ __global__ void __launch_bounds__(384, 1)
       const int free = min(cnt, max(0, ((lim0 + 1) >> 7) - jfirst + jshift) >> jshift);
       auto tiles = [&](auto nc, auto masked, int c0, int from, int to) {
         for (int i = from; i < to && ok; ++i) {
-          if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
+          if (!(ok = wait_warp<SHORT>(&B.s_full[t], scnt & 1, status))) break;
           ++scnt;
           tile(nc, masked, c0, i == 0, lim - (jfirst + (i << jshift)) * kTileRows - c0);
           mbar_arrive(&B.p_full[t]);
@@ -762,8 +786,12 @@ __global__ void __launch_bounds__(384, 1)
       constexpr std::true_type kMasked{};
       if (four) {
         constexpr std::integral_constant<int, 32> kQuarter{};
-        tiles(kQuarter, kFree, 32 * quarter, 0, free);
-        tiles(kQuarter, kMasked, 32 * quarter, free, cnt);
+        if constexpr (SHORT) {  // (one loop: less code, see wait_warp)
+          tiles(kQuarter, kMasked, 32 * quarter, 0, cnt);
+        } else {
+          tiles(kQuarter, kFree, 32 * quarter, 0, free);
+          tiles(kQuarter, kMasked, 32 * quarter, free, cnt);
+        }
       } else if constexpr (!SHORT) {
         constexpr std::integral_constant<int, 128> kAll{};
         if (busy) {
@@ -771,7 +799,7 @@ __global__ void __launch_bounds__(384, 1)
           tiles(kAll, kMasked, 0, free, cnt);
         } else {
           for (int i = 0; i < cnt && ok; ++i) {
-            if (!(ok = mbar_wait_warp(&B.s_full[t], scnt & 1, status))) break;
+            if (!(ok = wait_warp<SHORT>(&B.s_full[t], scnt & 1, status))) break;
             ++scnt;
             mbar_arrive(&B.p_half[t]);
             mbar_arrive(&B.p_full[t]);
@@ -779,7 +807,7 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (ok && cnt > 0) {
-        ok = mbar_wait_warp(&B.o_full[t], ocnt & 1, status);
+        ok = wait_warp<SHORT>(&B.o_full[t], ocnt & 1, status);
         ++ocnt;
       }
       if (!ok) break;
@@ -802,7 +830,7 @@ __global__ void __launch_bounds__(384, 1)
           if (cnt > 0) {
             const bool mine = lane >= r0 && lane < r0 + 8 && valid;
             const int rr = lane & 7;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(t_o + 32 * c, v);
@@ -818,7 +846,7 @@ __global__ void __launch_bounds__(384, 1)
             if (mine) ml[warp * 8 + rr] = make_float2(m_run, l_run);
           }
           mbar_arrive(B.x_full);
-          if (!(ok = mbar_wait_warp(B.x_full, fills & 1, status))) break;
+          if (!(ok = wait_warp<SHORT>(B.x_full, fills & 1, status))) break;
           ++fills;
           guard = false;  // everyone is past the last unit
           const int rr = threadIdx.x / kChunks, c = threadIdx.x % kChunks, q_row = r0 + rr;
@@ -854,7 +882,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (r0 + 8 < tile_rows) {
             mbar_arrive(B.x_next);
-            if (!(ok = mbar_wait_warp(B.x_next, nexts & 1, status))) break;
+            if (!(ok = wait_warp<SHORT>(B.x_next, nexts & 1, status))) break;
             ++nexts;
           }
         }
@@ -875,7 +903,7 @@ __global__ void __launch_bounds__(384, 1)
           float2* ml = reinterpret_cast<float2*>(sm + C::kOffQ + b * C::kTileBytes);
           ml[t * 128 + r] = make_float2(m_run, l_run);
           mbar_arrive(B.x_full);
-          if (!(ok = mbar_wait_warp(B.x_full, fills & 1, status))) break;
+          if (!(ok = wait_warp<SHORT>(B.x_full, fills & 1, status))) break;
           ++fills;
           const float2 other = ml[(1 - t) * 128 + r];
           m_out = fmaxf(m_run, other.x);

@@ -80,8 +80,10 @@ struct PagedCfg {
   static constexpr int kOffMl = kOffV + kVSlots * kTileBytes;  // [2 buffers][8 warps][8 rows] (m, l)
   static constexpr int kOffPlan = kOffMl + 2 * 64 * 8;
   static constexpr int kPlanBytes = 192;
-  static constexpr int kOffBar = kOffPlan + kPlanBytes;
-  static constexpr int kNumBars = 4 + 4 + 2 * kKSlots + 3 * kVSlots + 8 + 1;
+  static constexpr int kOffSegs = kOffPlan + kPlanBytes;  // (short chunks) [kSegs] segments
+  static constexpr int kSegs = 4;
+  static constexpr int kOffBar = kOffSegs + kSegs * 48;
+  static constexpr int kNumBars = 4 + 4 + 2 * kKSlots + 3 * kVSlots + 8 + 1 + 2 * kSegs;
   static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kSmemBytes = kOffAbort + 4;
@@ -232,6 +234,8 @@ struct PagedBars {
   uint64_t* p_half;   // [2] (not with four copies) P of the first 64 keys is there
   uint64_t* o_full;   // [2]
   uint64_t* mma_done;
+  uint64_t* seg_full;   // [segments] (short chunks) warp 11 has written it
+  uint64_t* seg_empty;  // every warp that walks has read it
 };
 
 // 32 bytes of a row.
@@ -297,6 +301,8 @@ __global__ void __launch_bounds__(384, 1)
   B.p_half = B.p_full + 2;
   B.o_full = B.p_half + 2;
   B.mma_done = B.o_full + 2;
+  B.seg_full = B.mma_done + 1;
+  B.seg_empty = B.seg_full + C::kSegs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
   Plan* plan = reinterpret_cast<Plan*>(sm + C::kOffPlan);
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(384, 1)
       const bool merge = bar == B.x_full || bar == B.x_next || bar == B.x_done || bar == B.x_done + 1;
       const bool p_full = bar >= B.p_full && bar < B.p_full + 4;  // p_half too
       const bool v_empty = bar >= B.v_empty && bar < B.v_empty + C::kVSlots;  // the MMA issuer and warp 10
-      mbar_init(bar, merge ? 256 : p_full ? 128 : v_empty ? 2 : 1);
+      mbar_init(bar, merge ? 256 : p_full ? 128 : bar >= B.seg_empty ? 11 : v_empty ? 2 : 1);
     }
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
@@ -337,14 +343,48 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tbase = *tmem_slot;
   const Work work(p);
   auto form_of = [&](const Segment& g) { return SHORT ? kFourCopies : sh.form(g.ntok); };
-  auto start = [&] { return walk_start(work, plan->at[0], plan->at[1], plan->q[0], sh); };
+  // The roles' walk through the run: `step` goes to the next segment, the first one
+  // included.  With short chunks warp 11 walks for all and the others read what it
+  // wrote: one copy of that code instead of five, and out of the chain between one
+  // unit's outputs and the next one's scores.
+  struct Place {
+    Walk w;
+    Segment g;
+    uint32_t count;
+  };
+  auto start = [&] {
+    Place a;
+    a.count = 0;
+    if constexpr (!SHORT) a.w = walk_start(work, plan->at[0], plan->at[1], plan->q[0], sh);
+    return a;
+  };
+  auto step = [&](Place& a, bool& ok) {
+    if (!ok) return false;
+    if constexpr (SHORT) {
+      const int slot = a.count % C::kSegs;
+      ok = wait_warp<SHORT>(&B.seg_full[slot], (a.count / C::kSegs) & 1, status);
+      if (!ok) return false;
+      ++a.count;
+      const int4* e = reinterpret_cast<const int4*>(sm + C::kOffSegs) + 3 * slot;
+      const int4 x = e[0], y = e[1], z = e[2];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.seg_empty[slot]);
+      a.w = {{x.x, x.y, 0, 0}, {x.z, x.w, y.x}};
+      a.g = {y.y, y.z, y.w, z.x, z.y};
+      return z.z != 0;
+    } else {
+      if (a.count++ > 0) walk_next(work, a.w, plan->at[1], sh, a.g);
+      return walk_get(work, a.w, plan->at[1], sh, a.g);
+    }
+  };
 
   if (warp >= 8) {
     regs_dec<C::kAuxRegs>();
     if (warp == 8) {
       // ------------------------------------------------------------ producer --
-      Walk w = start();
-      Segment g;
+      Place place = start();
+      const Walk& w = place.w;
+      const Segment& g = place.g;
       const int box_rows = min(1 << p.page_log2, kTileRows);
       const int per_tile = kTileRows / box_rows;  // pages of a key tile (1 if pages are longer)
       const uint32_t box_bytes = box_rows * 128;
@@ -359,7 +399,7 @@ __global__ void __launch_bounds__(384, 1)
         if (merged[b]) return wait_warp<SHORT>(&B.x_done[b], (by_merge[b] - 1) & 1, status);
         return by_mma[b] == 0 || wait_warp<SHORT>(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
       };
-      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
+      while (step(place, ok)) {
         const Form form = form_of(g);
         const int* table = p.page_table + (size_t)w.at.s * p.max_pages;
         const int pages = (w.q.kv + (1 << p.page_log2) - 1) >> p.page_log2;
@@ -445,7 +485,6 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
         }
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
       if (lost) atomicExch(status, FA_ERR_DEVICE_INDEX);
@@ -459,8 +498,9 @@ __global__ void __launch_bounds__(384, 1)
         wait_warp<SHORT>(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer --
-      Walk w = start();
-      Segment g;
+      Place place = start();
+      const Walk& w = place.w;
+      const Segment& g = place.g;
       const uint32_t idS = idesc_bf16(128, 128, 0, 0) | s_negate;  // S = (+/-) Q K^T, both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);            // O += P V, V is MN-major
       const uint32_t q_s = smem_addr(sm + C::kOffQ);
@@ -494,7 +534,7 @@ __global__ void __launch_bounds__(384, 1)
                                 sdesc(v_s + (it % C::kVSlots) * C::kTileBytes, kSwzBlockBytes, 1024), kIdO,
                                 accumulate);
       };
-      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
+      while (step(place, ok)) {
         const Form form = form_of(g);
         const int nt = g.j1 - g.j0;
         const int last = last_tile(w.q.kv);
@@ -612,7 +652,6 @@ __global__ void __launch_bounds__(384, 1)
         }
         kv_it += nt;
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
       mma_commit_w(B.mma_done);
@@ -621,11 +660,12 @@ __global__ void __launch_bounds__(384, 1)
       // ------------------------------------------- rows behind a sequence's end --
       // Follows every V tile (a parity wait must not run ahead of the ring, nor
       // the ring ahead of it: a slot is released by this warp as well).
-      Walk w = start();
-      Segment g;
+      Place place = start();
+      const Walk& w = place.w;
+      const Segment& g = place.g;
       uint32_t kv_it = 0;
       bool ok = true;
-      while (ok && walk_get(work, w, plan->at[1], sh, g)) {
+      while (step(place, ok)) {
         const int last = last_tile(w.q.kv), used = w.q.kv - (last << 7);
         for (int j = g.j0; j < g.j1; ++j, ++kv_it) {
           const int st = kv_it % C::kVSlots;
@@ -643,9 +683,27 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
         }
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
-        if (ok) walk_next(work, w, plan->at[1], sh, g);
       }
       if (!ok) *abort_flag = 1;
+    } else if constexpr (SHORT) {
+      // ------------------------------------------------------------ the walk --
+      Walk w = walk_start(work, plan->at[0], plan->at[1], plan->q[0], sh);
+      Segment g = {};
+      for (uint32_t i = 0;; ++i) {
+        const bool more = !__any_sync(0xffffffffu, aborted(abort_flag)) && walk_get(work, w, plan->at[1], sh, g);
+        const int slot = i % C::kSegs;
+        if (!wait_warp<SHORT>(&B.seg_empty[slot], ((i / C::kSegs) & 1) ^ 1, status)) break;
+        if (lane == 0) {
+          int4* e = reinterpret_cast<int4*>(sm + C::kOffSegs) + 3 * slot;
+          e[0] = make_int4(w.at.s, w.at.hk, w.q.q0, w.q.qn);
+          e[1] = make_int4(w.q.kv, g.tok0, g.ntok, g.n);
+          e[2] = make_int4(g.j0, g.j1, more, 0);
+          mbar_arrive(&B.seg_full[slot]);
+        }
+        __syncwarp();
+        if (!more) break;
+        walk_next(work, w, plan->at[1], sh, g);
+      }
     }
   } else {
     regs_inc<C::kSoftmaxRegs>();
@@ -744,9 +802,10 @@ __global__ void __launch_bounds__(384, 1)
       tmem_wait_st();
       tc_fence_before();
     };
-    Walk w = start();
-    Segment g;
-    while (ok && walk_get(work, w, plan->at[1], sh, g)) {
+    Place place = start();
+    const Walk& w = place.w;
+    const Segment& g = place.g;
+    while (step(place, ok)) {
       const Form form = form_of(g);
       const bool two = form == kTwoTiles, four = form == kFourCopies;
       const int nt = g.j1 - g.j0;
@@ -991,8 +1050,7 @@ __global__ void __launch_bounds__(384, 1)
         tail_hk = w.at.hk;
       }
       tc_fence_before();
-      if (aborted(abort_flag)) ok = false;
-      if (ok) walk_next(work, w, plan->at[1], sh, g);
+      if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
     }
     if (!ok) *abort_flag = 1;
     if (threadIdx.x == 0) {

@@ -245,13 +245,15 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// mbar_wait_warp in fewer instructions.  The kernels of short chunks pass through
-// all of their code for every small unit, and wait for instructions a good part of
-// their time: what is shorter there is faster (64 sequences of 8 tokens, d = 64:
-// 43.5 -> 42.7 us); the softmax of long chunks came out slower with it (468 -> 480).
-template <bool SHORT>
+// A warp's bounded wait.  SMALL: mbar_wait_warp in fewer instructions.  Small units
+// pass through all code of their roles and wait for instructions a good part of
+// their time, so what is shorter is faster: 64 sequences of 8 tokens, d = 64, took
+// 43.5 us and 42.7 with it; 2 chunks of 509 tokens among 14 single ones 60.3 and
+// 57.8, with d = 64 49.4 and 42.8.  The softmax of long chunks comes out slower with
+// it (2 x 2048 tokens: 468 -> 480 us) and has the other one.
+template <bool SMALL>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status) {
-  if constexpr (!SHORT) return mbar_wait_warp(bar, parity, status);
+  if constexpr (!SMALL) return mbar_wait_warp(bar, parity, status);
   const uint32_t a = smem_addr(bar);
   uint32_t t0 = 0;
 #pragma unroll 1
@@ -396,8 +398,8 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t turn = 0, kv_it = 0;
       bool ok = true, lost = false;
       auto wait_q = [&](int b) {
-        if (merged[b]) return wait_warp<SHORT>(&B.x_done[b], (by_merge[b] - 1) & 1, status);
-        return by_mma[b] == 0 || wait_warp<SHORT>(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
+        if (merged[b]) return wait_warp<true>(&B.x_done[b], (by_merge[b] - 1) & 1, status);
+        return by_mma[b] == 0 || wait_warp<true>(&B.q_empty[b], (by_mma[b] - 1) & 1, status);
       };
       while (step(place, ok)) {
         const Form form = form_of(g);
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           const int ks = kv_it % C::kKSlots, vs = kv_it % C::kVSlots;
           const uint32_t kph = (kv_it / C::kKSlots) & 1, vph = (kv_it / C::kVSlots) & 1;
-          if (!(ok = wait_warp<SHORT>(&B.k_empty[ks], kph ^ 1, status))) break;
+          if (!(ok = wait_warp<true>(&B.k_empty[ks], kph ^ 1, status))) break;
           if (lane == 0) mbar_expect_tx(&B.k_full[ks], boxes * box_bytes * C::kBlocks);
           __syncwarp();
           if (lane < boxes) {
@@ -470,9 +472,9 @@ __global__ void __launch_bounds__(384, 1)
               tma_load_4d(dst + kb * kSwzBlockBytes, &tm_k, &B.k_full[ks], 64 * kb, row, w.at.hk, page);
           }
           __syncwarp();
-          if (!(ok = wait_warp<SHORT>(&B.v_empty[vs], vph ^ 1, status))) {
+          if (!(ok = wait_warp<true>(&B.v_empty[vs], vph ^ 1, status))) {
             // the K copy of this tile is in flight: it lands before the block ends
-            wait_warp<SHORT>(&B.k_full[ks], kph, status);
+            wait_warp<true>(&B.k_full[ks], kph, status);
             break;
           }
           if (lane == 0) mbar_expect_tx(&B.v_full[vs], boxes * box_bytes * C::kBlocks);
@@ -491,11 +493,11 @@ __global__ void __launch_bounds__(384, 1)
       // Drain: every copy this warp started lands before the block ends.
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        if (q_uses[b] > 0) wait_warp<SHORT>(&B.q_full[b], (q_uses[b] - 1) & 1, status);
+        if (q_uses[b] > 0) wait_warp<true>(&B.q_full[b], (q_uses[b] - 1) & 1, status);
       for (uint32_t i = kv_it > (uint32_t)C::kKSlots ? kv_it - C::kKSlots : 0; i < kv_it; ++i)
-        wait_warp<SHORT>(&B.k_full[i % C::kKSlots], (i / C::kKSlots) & 1, status);
+        wait_warp<true>(&B.k_full[i % C::kKSlots], (i / C::kKSlots) & 1, status);
       for (uint32_t i = kv_it > (uint32_t)C::kVSlots ? kv_it - C::kVSlots : 0; i < kv_it; ++i)
-        wait_warp<SHORT>(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
+        wait_warp<true>(&B.v_full[i % C::kVSlots], (i / C::kVSlots) & 1, status);
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer --
       Place place = start();
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(384, 1)
         mma_commit_w(&B.s_full[t]);
       };
       auto wait_k = [&](uint32_t it) {
-        if (!wait_warp<SHORT>(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
+        if (!wait_warp<true>(&B.k_full[it % C::kKSlots], (it / C::kKSlots) & 1, status)) return false;
         tc_fence_after();
         return true;
       };
@@ -546,15 +548,15 @@ __global__ void __launch_bounds__(384, 1)
           if (i == tail) {
             const uint32_t parity = (clears >> st) & 1;
             clears ^= 1u << st;
-            return wait_warp<SHORT>(&B.v_clear[st], parity, status);
+            return wait_warp<true>(&B.v_clear[st], parity, status);
           }
-          return wait_warp<SHORT>(&B.v_full[st], (it / C::kVSlots) & 1, status);
+          return wait_warp<true>(&B.v_full[st], (it / C::kVSlots) & 1, status);
         };
         if (form != kTwoTiles) {
           const int b = turn & 1;
           ++turn;
           const uint32_t qa = q_s + b * C::kTileBytes;
-          ok = wait_warp<SHORT>(&B.q_full[b], (b ? q_uses[1] : q_uses[0]) & 1, status);
+          ok = wait_warp<true>(&B.q_full[b], (b ? q_uses[1] : q_uses[0]) & 1, status);
           if (b)
             ++q_uses[1];
           else
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(384, 1)
             const int t = i & 1;
             const bool halves = !SHORT && form == kOneTile;
             if (halves) {
-              ok = wait_warp<SHORT>(&B.p_half[t], (t ? hcnt[1] : hcnt[0]) & 1, status);
+              ok = wait_warp<true>(&B.p_half[t], (t ? hcnt[1] : hcnt[0]) & 1, status);
               if (t)
                 ++hcnt[1];
               else
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__(384, 1)
               tc_fence_after();
               issue_pv_half(t, kv_it + i, 0, i >= 2);
             }
-            ok = wait_warp<SHORT>(&B.p_full[t], (t ? pcnt[1] : pcnt[0]) & 1, status);
+            ok = wait_warp<true>(&B.p_full[t], (t ? pcnt[1] : pcnt[0]) & 1, status);
             if (t)
               ++pcnt[1];
             else
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || cnt[t] == 0) continue;
-            ok = wait_warp<SHORT>(&B.q_full[t], q_uses[t] & 1, status);
+            ok = wait_warp<true>(&B.q_full[t], q_uses[t] & 1, status);
             ++q_uses[t];
           }
           if (ok) ok = wait_k(kv_it);
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (!ok || i >= cnt[t]) continue;
-              ok = wait_warp<SHORT>(&B.p_half[t], hcnt[t] & 1, status);
+              ok = wait_warp<true>(&B.p_half[t], hcnt[t] & 1, status);
               ++hcnt[t];
               if (ok && !v_ready) {
                 ok = wait_v(i);
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(384, 1)
               if (!ok) break;
               tc_fence_after();
               issue_pv_half(t, kv_it + i, 0, i > 0);
-              ok = wait_warp<SHORT>(&B.p_full[t], pcnt[t] & 1, status);
+              ok = wait_warp<true>(&B.p_full[t], pcnt[t] & 1, status);
               ++pcnt[t];
               if (!ok) break;
               tc_fence_after();
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) *abort_flag = 1;
       mma_commit_w(B.mma_done);
-      wait_warp<SHORT>(B.mma_done, 0, status);
+      wait_warp<true>(B.mma_done, 0, status);
     } else if (warp == 10) {
       // ------------------------------------------- rows behind a sequence's end --
       // Follows every V tile (a parity wait must not run ahead of the ring, nor
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(384, 1)
         const int last = last_tile(w.q.kv), used = w.q.kv - (last << 7);
         for (int j = g.j0; j < g.j1; ++j, ++kv_it) {
           const int st = kv_it % C::kVSlots;
-          if (!(ok = wait_warp<SHORT>(&B.v_full[st], (kv_it / C::kVSlots) & 1, status))) break;
+          if (!(ok = wait_warp<true>(&B.v_full[st], (kv_it / C::kVSlots) & 1, status))) break;
           if (j == last && used < kTileRows) {
             for (int kb = 0; kb < C::kBlocks; ++kb) {
               uint4* rows = reinterpret_cast<uint4*>(sm + C::kOffV + st * C::kTileBytes + kb * kSwzBlockBytes);
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(384, 1)
       for (uint32_t i = 0;; ++i) {
         const bool more = !__any_sync(0xffffffffu, aborted(abort_flag)) && walk_get(work, w, plan->at[1], sh, g);
         const int slot = i % C::kSegs;
-        if (!wait_warp<SHORT>(&B.seg_empty[slot], ((i / C::kSegs) & 1) ^ 1, status)) break;
+        if (!wait_warp<true>(&B.seg_empty[slot], ((i / C::kSegs) & 1) ^ 1, status)) break;
         if (lane == 0) {
           int4* e = reinterpret_cast<int4*>(sm + C::kOffSegs) + 3 * slot;
           e[0] = make_int4(w.at.s, w.at.hk, w.q.q0, w.q.qn);

@@ -328,6 +328,13 @@ __global__ void __launch_bounds__(384, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  // Rows of a query tile that no copy fills (G does not divide 32): zero, as they
+  // have a part in their warp's votes on rescaling, which must be the same on every run.
+  if (tt * p.G < kTileRows || t4 * p.G < kTileRows / 4) {
+    for (int i = threadIdx.x; i < 2 * C::kTileBytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(sm + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_q4);
@@ -1071,23 +1078,40 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-// Merges the units that were cut: block (c, y) takes rows of the unit that CTA
-// c began and did not end.  Its parts are CTA c's second slot and the first
-// slots of the CTAs behind it up to the one that ended it, added in that order.
-// D / 8 lanes a row, AHEAD parts asked for at once: two where the rows are many
-// (40 MB in all where every CTA cut a unit of 256 rows), eight for the few
-// rows of short chunks, whose keys may be spread over many CTAs.
+// Merges the units that were cut: blocks (c, y) take rows of the unit that CTA c
+// began and did not end.  Its parts are CTA c's second slot and the first slots
+// of the CTAs behind it up to the one that ended it, added in a fixed order.
+// D / 8 lanes a row.  Of few parts a warp adds up all, AHEAD of them asked for at
+// once: two where the rows are many (40 MB in all where every CTA cut a unit of 256
+// rows), eight for the few rows of short chunks.  More parts (a long cache and few
+// heads) are shared by a block's warps, eight parts at a time, and the rows by the
+// blocks of all CTAs that worked on the unit: one warp after 46 parts of a unit
+// (267 tokens, one head, 5885 keys, d = 64) took most of that call's 39 us.
 template <int D, int AHEAD>
 __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(const PagedParams p, int ctas) {
   constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kRowsABlock = 8 * kRowsAWarp;
-  const int c = blockIdx.x;
   const int lane = threadIdx.x & 31, l8 = lane % kLanes;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  int c = blockIdx.x;  // the CTA that began the unit
   auto slot = [&](int i) { return ((size_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * kPagedRows; };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 h = *reinterpret_cast<const int4*>(p.hdr + (size_t)c * kPagedHdr);
+  int4 h = *reinterpret_cast<const int4*>(p.hdr + (size_t)c * kPagedHdr);
+  const int inside = p.hdr[(size_t)c * kPagedHdr + 4];
   int ends = c + 1 + lane < ctas ? p.hdr[(size_t)(c + 1 + lane) * kPagedHdr + 4] : 2;
-  if (!h.x) return;
+  if (!h.x) {
+    if (inside != 1) return;
+    // this CTA's run lies within a unit: the nearest one in front that began one
+    for (int at = c - 1;; at -= 32) {
+      const unsigned found = __ballot_sync(0xffffffffu, at >= lane && p.hdr[(size_t)(at - lane) * kPagedHdr] != 0);
+      if (found) {
+        c = at - (__ffs(found) - 1);
+        break;
+      }
+      if (at < 32) return;
+    }
+    h = *reinterpret_cast<const int4*>(p.hdr + (size_t)c * kPagedHdr);
+    ends = c + 1 + lane < ctas ? p.hdr[(size_t)(c + 1 + lane) * kPagedHdr + 4] : 2;
+  }
   // the first CTA behind c whose first slot ends its unit
   int last = ctas - 1;
   for (int at = c + 1;; at += 32) {
@@ -1101,6 +1125,71 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
   const int parts = last - c + 1;
   const int tile = p.tile_tokens * p.G;
   const int rows = h.z * p.G;  // valid rows, densely numbered
+  auto put = [&](int n, float m, float l, const float (&acc)[8]) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int tok = token_of(p, n);
+    const size_t row = (size_t)(h.y + tok) * (p.Hk * p.G) + h.w * p.G + (n - tok * p.G);
+    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[l8] =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (l8 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  };
+  auto add = [](float (&acc)[8], float w, const float4& a, const float4& b) {
+    acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]), acc[2] = fmaf(w, a.z, acc[2]);
+    acc[3] = fmaf(w, a.w, acc[3]), acc[4] = fmaf(w, b.x, acc[4]), acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]), acc[7] = fmaf(w, b.w, acc[7]);
+  };
+  if (parts > (AHEAD == 2 ? 4 : 8)) {
+    __shared__ float4 sum[8][32][2];
+    __shared__ float2 stat[8][32];
+    const int wp = threadIdx.x / 32, blocks = (last - c) * gridDim.y;
+    for (int q = (blockIdx.x - c) * gridDim.y + blockIdx.y; q * kRowsAWarp < rows; q += blocks) {
+      const int n = min(q * kRowsAWarp + lane / kLanes, rows - 1);  // (rows past the end repeat the last one)
+      const int prow = n < tile ? n : 128 + n - tile;
+      float m = -INFINITY, l = 0.f, acc[8] = {};
+      float4 v0 = {}, v1 = {};
+      float2 x = {-INFINITY, 0.f};
+      auto load = [&](int i) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot(i) + prow) * D) + 2 * l8;
+        v0 = src[0], v1 = src[1], x = ml[slot(i) + prow];
+      };
+      if (wp < parts) load(wp);
+      for (int i = wp; i < parts; i += 8) {
+        const float4 u0 = v0, u1 = v1;
+        const float2 y = x;
+        if (i + 8 < parts) load(i + 8);
+        if (y.y == 0.f) continue;  // saw no key
+        const float m_new = fmaxf(m, y.x);
+        const float old = m == -INFINITY ? 0.f : ex2(m - m_new), w = ex2(y.x - m_new);
+        l = fmaf(w, y.y, l * old);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= old;
+        add(acc, w, u0, u1);
+        m = m_new;
+      }
+      sum[wp][lane][0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      sum[wp][lane][1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      stat[wp][lane] = make_float2(m, l);
+      __syncthreads();
+      if (wp == 0) {
+        for (int k = 1; k < 8; ++k) m = fmaxf(m, stat[k][lane].x);
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int k = 0; k < 8; ++k) {
+          const float2 y = stat[k][lane];
+          if (y.y == 0.f) continue;
+          const float w = ex2(y.x - m);
+          l = fmaf(w, y.y, l);
+          add(acc, w, sum[k][lane][0], sum[k][lane][1]);
+        }
+        if (q * kRowsAWarp + lane / kLanes < rows) put(n, m, l, acc);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  if (c != (int)blockIdx.x) return;
   for (int n0 = blockIdx.y * kRowsABlock + threadIdx.x / 32 * kRowsAWarp; n0 < rows; n0 += gridDim.y * kRowsABlock) {
     const int n = min(n0 + lane / kLanes, rows - 1);  // (rows past the end repeat the last one)
     const int prow = n < tile ? n : 128 + n - tile;
@@ -1119,7 +1208,7 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
       if (k < 2 || k < parts) m = fmaxf(m, x[k].x);
-    if (parts > AHEAD) {
+    if (AHEAD < 4 && parts > AHEAD) {
       for (int i = AHEAD + l8; i < parts; i += kLanes) m = fmaxf(m, ml[slot(i) + prow].x);
 #pragma unroll
       for (int off = kLanes / 2; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -1131,24 +1220,11 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
         if (i + k >= parts) continue;
         const float w = x[k].y == 0.f ? 0.f : ex2(x[k].x - m);
         l = fmaf(w, x[k].y, l);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          acc[4 * e + 0] = fmaf(w, v[k][e].x, acc[4 * e + 0]);
-          acc[4 * e + 1] = fmaf(w, v[k][e].y, acc[4 * e + 1]);
-          acc[4 * e + 2] = fmaf(w, v[k][e].z, acc[4 * e + 2]);
-          acc[4 * e + 3] = fmaf(w, v[k][e].w, acc[4 * e + 3]);
-        }
+        add(acc, w, v[k][0], v[k][1]);
         if (i + k + AHEAD < parts) load(i + k + AHEAD, k);
       }
     }
-    if (n0 + lane / kLanes >= rows) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int tok = token_of(p, n);
-    const size_t row = (size_t)(h.y + tok) * (p.Hk * p.G) + h.w * p.G + (n - tok * p.G);
-    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[l8] =
-        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-    if (l8 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+    if (n0 + lane / kLanes < rows) put(n, m, l, acc);
   }
 }
 

@@ -166,6 +166,30 @@ def test_long_caches_are_cut(q_lens, kv_lens, Hq, Hk, d, hint):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hk,d", [
+    ([267], [5885], 1, 1, 64),                   # a row group's rows in two tiles, 46 parts
+    ([31, 57], [9001, 3000], 5, 1, 128),         # units of each form
+    ([3, 300, 2], [70, 2500, 5000], 6, 2, 64),
+    ([7], [30000], 4, 1, 128),
+])
+def test_parts_shared_by_warps(q_lens, kv_lens, Hq, Hk, d, hint):
+    """Units cut into many parts, some rows of NaN among the others; the same bits on every run."""
+    case = (q_lens, kv_lens, Hq, Hk, d, 32, True, True)
+    q, pages, table, cu, lens = batch(case, seed=29)
+    o, lse, reach = reference(q, pages, table, cu, lens, 0.09, True)
+    q[1::5, 0] = float("nan")
+    lse[1::5, 0] = np.nan
+    args = (q, *pages, table.cuda(), cu.cuda(), lens.cuda())
+    got, got_lse = fa.paged_forward(*args, scale=0.09, max_q=hint)
+    assert status() == fa.FA_OK
+    check(got, got_lse, (o, lse, reach))
+    assert np.isnan(f64(got)[1::5, 0]).all() and np.isnan(f64(got_lse)[1::5, 0]).all()
+    again, again_lse = fa.paged_forward(*args, scale=0.09, max_q=hint)
+    assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+    assert torch.equal(got_lse.view(torch.int32), again_lse.view(torch.int32))
+
+
 @pytest.mark.parametrize("d,page,q,hint", [(128, 16, 1, 1), (64, 32, 5, 5), (128, 64, 1, 200), (64, 128, 40, 200)])
 def test_runs_of_many_tiles_and_units(d, page, q, hint):
     """Several units of several key tiles in each CTA's run, sequences that end inside a tile among them."""

@@ -854,12 +854,7 @@ __global__ void __launch_bounds__(384, 1)
       constexpr std::true_type kMasked{};
       if (four) {
         constexpr std::integral_constant<int, 32> kQuarter{};
-        if constexpr (SHORT) {  // (one loop: less code, see wait_warp)
-          tiles(kQuarter, kMasked, 32 * quarter, 0, cnt);
-        } else {
-          tiles(kQuarter, kFree, 32 * quarter, 0, free);
-          tiles(kQuarter, kMasked, 32 * quarter, free, cnt);
-        }
+        tiles(kQuarter, kMasked, 32 * quarter, 0, cnt);  // (one loop: less code, see wait_warp)
       } else if constexpr (!SHORT) {
         constexpr std::integral_constant<int, 128> kAll{};
         if (busy) {

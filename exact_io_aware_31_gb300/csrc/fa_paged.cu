@@ -14,11 +14,12 @@
 //
 // Work: a unit is one key head's block of one or two 128-row query tiles and all
 // key tiles (128 keys) it sees.  The units, one after the other, are cut into
-// runs of equal cost, one per CTA, whatever mix of lengths a step brings; lengths are read on the device, so the host knows none of them and one
-// captured graph serves every step.  A cut that falls near a unit's border moves
-// there.  A unit that is cut leaves unnormalised partial outputs (fp32) with
-// their maxima and sums in the workspace, at most two a CTA, and a second kernel
-// (a programmatic dependent) merges them in a fixed order: no atomics on results.
+// runs of equal cost, one per CTA, whatever mix of lengths a step brings; lengths
+// are read on the device, so the host knows none of them and one captured graph
+// serves every step.  A cut that falls near a unit's border moves there.  A unit
+// that is cut leaves unnormalised partial outputs (fp32) with their maxima and
+// sums in the workspace, at most two a CTA, and a second kernel (a programmatic
+// dependent) merges them in a fixed order: no atomics on results.
 //
 // Three forms of a unit, by its query rows; warpgroups t = 0, 1:
 //   two tiles   up to 256 rows against each key tile: warpgroup t owns tile t
@@ -29,16 +30,23 @@
 //               of the columns (its P is zero in the others).  A warp that had
 //               32 rows to itself spent about 2000 cycles a key tile on one
 //               lane's 128 exponentials while three warps idled: 64 sequences
-//               of 256 to 1024 keys, 8 tokens each, 16 heads, d = 64 ran in 68 us.
-//               The eight partial rows are merged through the unit's own query
-//               buffer, which is dead by then.
+//               of 256 to 1024 keys, 8 tokens each, 16 heads, d = 64 ran in 68 us
+//               (42 now).  The eight partial rows are merged through the unit's
+//               own query buffer, which is dead by then.
 // SHORT kernels hold only the last form: the host takes them where it was told
 // that chunks are short; a longer chunk is then a row of small units.
+//
+// Measured (GB300, d = 128, 32 query and 8 key heads): 2 x 2048 tokens against 16384
+// and 8789 keys 465 us, 1.67 PFLOP/s (87% of the dense rate; the softmax between
+// the MMAs); 64 single tokens against up to 8192 keys 220 us, 6.1 TB/s (90% of the
+// copy rate); one token, 16 heads, 16384 keys 32 us (7 us until the first tile,
+// 4 us of merge).  Small units are bound by the chain from one unit's last tile to
+// the next one's first scores (2 us) and by instruction fetch.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax warpgroups, 8 producer, 9 MMA issuer,
 // 10 clears the rows of V behind a sequence's end (what lies there in a page is
 // not the sequence's, and 0 * NaN is NaN; K needs none of it, its scores are
-// masked), 11 idle.
+// masked), 11 (short chunks) walks the run for the others.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -199,7 +199,7 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
       before = run + block_scan<THREADS>(per_head * p.Hk, plan->scan, &part);
       run += part;
     }
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       const long long x = border(total, share, blockIdx.x + e, ctas);
       if ((int)blockIdx.x + e > ctas || x < before || x >= before + per_head * p.Hk) continue;
@@ -211,7 +211,7 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
   }
   __syncthreads();
   // Their blocks: every thread tries some.
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     if (plan->at[e].s >= p.S) continue;
     const Seq sq = plan->q[e];

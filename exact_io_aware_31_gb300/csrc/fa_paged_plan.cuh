@@ -31,14 +31,15 @@ struct Shape {
 // The units' share was then moved until mixed batches took least: with too little
 // for two tiles and too much for four copies, the CTAs of single tokens ended 15 us
 // before the others (d = 128: 45, 35, 24 -> 75, 35, 15 took a step of 2 chunks of
-// 509 among 14 single tokens from 64 to 60 us, 3 chunks of 200 among 97 from 208 to 197).
+// 509 among 14 single tokens from 64 to 60 us, 3 chunks of 200 among 97 from 208 to 197;
+// 15 -> 10 when the kernels' small units had got shorter: 57.6 -> 57.2).
 template <int D>
 __host__ __device__ inline int tile_cost(Form f) {
   return D == 128 ? (f == kTwoTiles ? 15 : f == kOneTile ? 10 : 12) : (f == kTwoTiles ? 12 : f == kOneTile ? 7 : 6);
 }
 template <int D>
 __host__ __device__ inline int unit_cost(Form f) {
-  return D == 128 ? (f == kTwoTiles ? 75 : f == kOneTile ? 35 : 15) : (f == kTwoTiles ? 60 : f == kOneTile ? 30 : 17);
+  return D == 128 ? (f == kTwoTiles ? 75 : f == kOneTile ? 35 : 10) : (f == kTwoTiles ? 60 : f == kOneTile ? 30 : 12);
 }
 
 struct Seq {

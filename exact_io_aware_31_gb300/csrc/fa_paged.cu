@@ -966,21 +966,25 @@ __global__ void __launch_bounds__(384, 1)
           ++x_uses[0];
       } else if constexpr (!SHORT) {
         // One-tile unit of two or more key tiles: both halves' (m, l) through the dead query
-        // buffer, then each half writes half of the columns from both outputs.
+        // buffer, then each half writes half of the columns from both outputs.  With one
+        // key tile half 1 has nothing to add, but waits as well: it must not run ahead, and
+        // arrive on x_done for the unit after the next in half 0's place.
         const bool merge = !two && nt > 1;
         float w0 = 1.f, w1 = 0.f, m_out = m_run, l_out = l_run;  // weights of this half's and the other's output
         const int b = turn & 1;
-        if (merge) {
+        if (!two) {
           float2* ml = reinterpret_cast<float2*>(sm + C::kOffQ + b * C::kTileBytes);
-          ml[t * 128 + r] = make_float2(m_run, l_run);
+          if (merge) ml[t * 128 + r] = make_float2(m_run, l_run);
           mbar_arrive(B.x_full);
           if (!(ok = wait_warp<SHORT>(B.x_full, fills & 1, status))) break;
           ++fills;
-          const float2 other = ml[(1 - t) * 128 + r];
-          m_out = fmaxf(m_run, other.x);
-          w0 = l_run == 0.f ? 0.f : ex2(m_run - m_out);
-          w1 = other.y == 0.f ? 0.f : ex2(other.x - m_out);
-          l_out = l_run * w0 + other.y * w1;
+          if (merge) {
+            const float2 other = ml[(1 - t) * 128 + r];
+            m_out = fmaxf(m_run, other.x);
+            w0 = l_run == 0.f ? 0.f : ex2(m_run - m_out);
+            w1 = other.y == 0.f ? 0.f : ex2(other.x - m_out);
+            l_out = l_run * w0 + other.y * w1;
+          }
         }
         if (busy && (two || merge || t == 0)) {  // (a single key tile: half 0 alone)
           const bool empty = l_out == 0.f;       // saw no key: zero, whatever O holds

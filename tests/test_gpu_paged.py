@@ -166,6 +166,29 @@ def test_long_caches_are_cut(q_lens, kv_lens, Hq, Hk, d, hint):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("hint", [0, 200])
+@pytest.mark.parametrize("q,kv,Hq,Hk,d,long", [
+    (6, 110, 64, 8, 64, 1),      # every unit one query tile, most of one key tile
+    (7, 300, 64, 8, 128, 1),     # 1 to 3 key tiles
+    (82, 200, 4, 4, 128, 7),     # among single tokens
+    (120, 128, 2, 2, 64, 3),
+])
+def test_rows_of_small_units(q, kv, Hq, Hk, d, long, hint):
+    """Runs of units of one query tile and one key tile or a few: the half of a CTA that has no key tile must not get
+    ahead of the other."""
+    g = torch.Generator().manual_seed(5)
+    q_lens = [int(torch.randint(max(1, q - 30), q + 1, (1,), generator=g)) if s % long == 0 else 1 for s in range(72)]
+    kv_lens = [max(n, int(torch.randint(n, kv + 1, (1,), generator=g))) for n in q_lens]
+    case = (q_lens, kv_lens, Hq, Hk, d, 32, False, True)
+    q, pages, table, cu, lens = batch(case)
+    ref = reference(q, pages, table, cu, lens, 0.11, True)
+    args = (q, *pages, table.cuda(), cu.cuda(), lens.cuda())
+    for _ in range(3):
+        o, lse = fa.paged_forward(*args, scale=0.11, max_q=hint)
+        assert status() == fa.FA_OK
+        check(o, lse, ref)
+
+
 @pytest.mark.parametrize("hint", [0, 1])
 @pytest.mark.parametrize("q_lens,kv_lens,Hq,Hk,d", [
     ([267], [5885], 1, 1, 64),                   # a row group's rows in two tiles, 46 parts

@@ -31,14 +31,14 @@
 //               32 rows to itself spent about 2000 cycles a key tile on one
 //               lane's 128 exponentials while three warps idled: 64 sequences
 //               of 256 to 1024 keys, 8 tokens each, 16 heads, d = 64 ran in 68 us
-//               (42 now).  The eight partial rows are merged through the unit's
+//               (41 now).  The eight partial rows are merged through the unit's
 //               own query buffer, which is dead by then.
 // SHORT kernels hold only the last form: the host takes them where it was told
 // that chunks are short; a longer chunk is then a row of small units.
 //
 // Measured (GB300, d = 128, 32 query and 8 key heads): 2 x 2048 tokens against 16384
-// and 8789 keys 465 us, 1.67 PFLOP/s (87% of the dense rate; the softmax between
-// the MMAs); 64 single tokens against up to 8192 keys 220 us, 6.1 TB/s (90% of the
+// and 8789 keys 461 us, 1.68 PFLOP/s (88% of the dense rate; the softmax between
+// the MMAs); 64 single tokens against up to 8192 keys 219 us, 6.1 TB/s (91% of the
 // copy rate); one token, 16 heads, 16384 keys 32 us (7 us until the first tile,
 // 4 us of merge).  Small units are bound by the chain from one unit's last tile to
 // the next one's first scores (2 us) and by instruction fetch.

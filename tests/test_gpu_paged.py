@@ -7,6 +7,8 @@ most 2^-18 sum_c |q_c k_c| scale (d <= 128 products, accumulated in fp32 by the 
 lse: the forward tests' 1e-3 covers the same score error (2^-18 * 80 = 3e-4).
 """
 
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -393,6 +395,34 @@ def test_a_served_sequence_equals_the_whole_attention(Hq, Hk, d, page, inter):
                                     d ** -0.5, True)
         check(torch.cat(out[s]), torch.cat(lses[s]), ref)
         check(o[0].transpose(0, 1), lse[0].T, ref)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_any_mix_of_lengths(seed):
+    """Batches drawn at random: every form, groups that divide nothing, empty sequences, chunks longer than their keys,
+    lengths at tile borders; any hint; rows behind the batch untouched."""
+    r = random.Random(seed)
+    while True:
+        d, G, S = r.choice([64, 128]), r.choice([1, 2, 3, 5, 8, 12, 20, 33, 100]), int(2 ** r.uniform(0, 7))
+        Hk = r.choice([1, 2, 4, 16]) if G < 16 else 1
+        long_q, long_kv = r.choice([1, 2, 6, 40, 150, 400]), r.choice([10, 130, 300, 1500])
+        if S * long_kv < 30000 and S * long_q * (long_q + long_kv) * Hk * G < 6e6:
+            break
+    q_lens = [r.randint(0, long_q) if r.random() < 0.6 else 1 for _ in range(S)] + [1]
+    kv_lens = [n + r.randint(0, long_kv) if r.random() < 0.9 else r.randint(0, long_kv) for n in q_lens]
+    kv_lens = [n // 128 * 128 if r.random() < 0.1 else n for n in kv_lens]
+    case = (q_lens, kv_lens, Hk * G, Hk, d, r.choice([16, 32, 128, 256]), r.random() < 0.5, r.random() < 0.8)
+    q, pages, table, cu, lens = batch(case, seed=seed)
+    T = q.shape[0]
+    ref = reference(q, pages, table, cu, lens, 0.1, case[7])
+    q = torch.cat([q, q[:1].expand(3, -1, -1)])
+    for hint in (0, max(q_lens), r.choice([1, 3, 50, 10 ** 6])):
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        fa.paged_forward(q, *pages, table.cuda(), cu.cuda(), lens.cuda(), scale=0.1, causal=case[7], max_q=hint, out=o,
+                         lse=lse)
+        assert status() == fa.FA_OK
+        check(o[:T], lse[:T], ref)
+        assert (o[T:] == 7).all() and (lse[T:] == 7).all()
 
 
 def test_strides_of_single_elements_mean_nothing():

@@ -14,14 +14,14 @@ namespace fa {
 namespace paged {
 
 // Which form a unit takes (fa_paged.cu).
-enum Form { kTwoTiles, kOneTile, kFourCopies };
+enum Form { kTwoTiles, kOneTile, kFourCopies, kShortCopies };  // (the last: four copies, and no other form there)
 
 // The launch's division: tokens of a unit, of a query tile, of a quarter tile.
 struct Shape {
   int ut, tt, t4;
   int causal;
   __host__ __device__ Form form(int tokens) const {
-    return tokens <= t4 ? kFourCopies : tokens <= tt ? kOneTile : kTwoTiles;
+    return tokens <= t4 ? (ut <= t4 ? kShortCopies : kFourCopies) : tokens <= tt ? kOneTile : kTwoTiles;
   }
 };
 
@@ -31,15 +31,18 @@ struct Shape {
 // The units' share was then moved until mixed batches took least: with too little
 // for two tiles and too much for four copies, the CTAs of single tokens ended 15 us
 // before the others (d = 128: 45, 35, 24 -> 75, 35, 15 took a step of 2 chunks of
-// 509 among 14 single tokens from 64 to 60 us, 3 chunks of 200 among 97 from 208 to 197;
-// 15 -> 10 when the kernels' small units had got shorter: 57.6 -> 57.2).
+// 509 among 14 single tokens from 64 to 60 us, 3 chunks of 200 among 97 from 208 to
+// 197).  The kernels that hold four copies alone have shorter units: 10 and 12 there
+// take 64 x 8 tokens, d = 64, from 41.8 to 41.2 us, and in the others 4 chunks of up
+// to 225 among 25 single tokens, d = 64, from 31.6 to 35.8.
 template <int D>
 __host__ __device__ inline int tile_cost(Form f) {
   return D == 128 ? (f == kTwoTiles ? 15 : f == kOneTile ? 10 : 12) : (f == kTwoTiles ? 12 : f == kOneTile ? 7 : 6);
 }
 template <int D>
 __host__ __device__ inline int unit_cost(Form f) {
-  return D == 128 ? (f == kTwoTiles ? 75 : f == kOneTile ? 35 : 10) : (f == kTwoTiles ? 60 : f == kOneTile ? 30 : 12);
+  return D == 128 ? (f == kTwoTiles ? 75 : f == kOneTile ? 35 : f == kFourCopies ? 15 : 10)
+                  : (f == kTwoTiles ? 60 : f == kOneTile ? 30 : f == kFourCopies ? 17 : 12);
 }
 
 struct Seq {

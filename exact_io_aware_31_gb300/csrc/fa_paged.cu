@@ -246,7 +246,8 @@ struct PagedBars {
   uint64_t* seg_empty;  // every warp that walks has read it
 };
 
-// 32 bytes of a row.
+// 32 bytes of a row, 32-byte aligned: rows of the workspace (an output of the caller's
+// is only 16-byte aligned).
 __device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -1021,12 +1022,13 @@ __global__ void __launch_bounds__(384, 1)
             if (!valid) continue;
             if (whole) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t y[8];
+              for (int h = 0; h < 4; ++h) {
+                uint32_t y[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  y[k] = pack_bf16x2(__uint_as_float(v[16 * h + 2 * k]), __uint_as_float(v[16 * h + 2 * k + 1]));
-                store32(static_cast<__nv_bfloat16*>(p.o) + out_row * D + c + 16 * h, y);
+                for (int k = 0; k < 4; ++k)
+                  y[k] = pack_bf16x2(__uint_as_float(v[8 * h + 2 * k]), __uint_as_float(v[8 * h + 2 * k + 1]));
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D + c + 8 * h) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
               }
             } else {
 #pragma unroll

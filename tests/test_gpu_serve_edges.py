@@ -1,0 +1,90 @@
+"""Norm, rotation and paged cache at the edges of what their calls allow (needs a GB300).
+
+Tolerances are those of the tests of each operator (tests/test_gpu_norm_rope.py, tests/test_gpu_paged.py).
+"""
+
+import pytest
+import torch
+
+import exact_io_aware_31_gb300 as fa
+from tests.gpu_util import require_gpu
+from tests.test_gpu_norm_rope import pool, ragged, status
+from tests.test_gpu_paged import CASES, IDS, batch, check, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def aside(t, behind=16):
+    """A contiguous copy of ``t`` that starts ``behind`` bytes past a 256-byte border (and no nearer to one)."""
+    n = behind // t.element_size()
+    room = torch.zeros(t.numel() + 2 * n, dtype=t.dtype, device="cuda")
+    assert room.data_ptr() % 256 == 0
+    out = room[n:n + t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("hint", [None, 0, 1, 10 ** 6])
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_attention_at_16_byte_addresses(case, hint):
+    """16 bytes are the alignment that every tensor is promised to need; each form of a unit writes rows of its own."""
+    q, pages, table, cu, lens = batch(case)
+    if case[6]:
+        pages = [aside(p.transpose(1, 2)).transpose(1, 2) for p in pages]
+    else:
+        pages = [aside(p) for p in pages]
+    ref = reference(q, pages, table, cu, lens, 0.11, case[7])
+    room = torch.full((q.numel() + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    stats = torch.full((q.shape[0] * q.shape[1] + 2,), 4.0, device="cuda")
+    o, lse = room[8:-8].view(q.shape), stats[1:-1].view(q.shape[:2])
+    assert o.data_ptr() % 32 == 16
+    fa.paged_forward(aside(q), *pages, *(aside(t, 4) for t in (table, cu, lens)), scale=0.11, causal=case[7],
+                     max_q=max(case[0]) if hint is None else hint, out=o, lse=lse)
+    assert status() == fa.FA_OK
+    check(o, lse, ref)
+    assert bool((room[:8] == 3).all()) and bool((room[-8:] == 3).all()) and stats[0] == 4 and stats[-1] == 4
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hk,d", [
+    ([267], [5885], 1, 1, 64),
+    ([1, 140], [9000, 6000], 2, 1, 128),
+])
+def test_merged_rows_at_16_byte_addresses(q_lens, kv_lens, Hq, Hk, d):
+    """Units that were cut: the merge writes them."""
+    q, pages, table, cu, lens = batch((q_lens, kv_lens, Hq, Hk, d, 64, False, True))
+    args = (*pages, table.cuda(), cu.cuda(), lens.cuda())
+    want = fa.paged_forward(q, *args)
+    out = aside(torch.zeros_like(q))
+    got = fa.paged_forward(aside(q), *args, out=out)
+    assert status() == fa.FA_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("Hq,Hk,N,d", [(1, 1, 37, 64), (5, 2, 70, 128), (17, 9, 33, 64)])
+def test_norm_and_append_at_16_byte_addresses(Hq, Hk, N, d):
+    g = torch.Generator().manual_seed(8)
+    new = lambda *n: torch.randn(n, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, v = new(1, Hq, N, d), new(1, Hk, N, d), new(N, Hk, d)
+    w = [(1 + 0.2 * torch.randn(d, generator=g)).cuda() for _ in "qk"]
+    rope = fa.rope_table(N, d)
+    dz = [torch.randn_like(x) for x in (q, k)]
+    want = *fa.qk_norm_rope(q, k, *w, rope=rope), *fa.qk_norm_rope_backward(*dz, q, k, *w, rope=rope)
+    w2, rope2 = [aside(t) for t in w], aside(rope)
+    outs, grads = ([aside(torch.zeros_like(x)) for x in (q, k)] for _ in range(2))
+    got = (*fa.qk_norm_rope(aside(q), aside(k), *w2, rope=rope2, out=outs),
+           *fa.qk_norm_rope_backward(*(aside(x) for x in dz), aside(q), aside(k), *w2, rope=rope2, grads=grads))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    (kp, vp), table = pool([N], Hk, d, 16, False, 3)
+    meta = table.cuda(), ragged([N]).cuda(), torch.tensor([N], dtype=torch.int32).cuda()
+    rows = [x[0].transpose(0, 1).contiguous() for x in (q, k)]
+    kp2, vp2 = aside(kp), aside(vp)
+    out = fa.paged_append(*rows, v, kp, vp, *meta, *w, rope=rope)
+    out2 = fa.paged_append(*(aside(x) for x in (*rows, v)), kp2, vp2, *(aside(t, 4) for t in meta), *w2, rope=rope2,
+                           out=aside(torch.zeros_like(out)))
+    assert status() == fa.FA_OK
+    assert torch.equal(out, out2) and torch.equal(kp, kp2) and torch.equal(vp, vp2)

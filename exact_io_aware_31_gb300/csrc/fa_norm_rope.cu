@@ -236,7 +236,8 @@ __device__ __forceinline__ uint4 turn_row(const NormRopeParams& p, const Lane<D,
 }
 
 // The gradient of a row's 8 columns: dz -> dx (c and s of minus the angle), and its part of dw added to `dw` if it
-// counts (a row without a position has no gradient; one that is not there may have no finite 1 / rms).
+// counts.  One that does not, without a position or not there at all, comes with zeros for x and dz: then only its
+// 1 / rms may be infinite (eps = 0), and is left out.
 template <int D, bool INTER>
 __device__ __forceinline__ uint4 turn_row_back(const NormRopeParams& p, const Lane<D, INTER>& ln, const Row& c,
                                                const Row& s, const Row& w, const uint4& raw, const uint4& dz,
@@ -402,6 +403,10 @@ __global__ void __launch_bounds__(kThreads, STEPS == 4 ? 2 : 3) norm_rope_bwd_ke
     Row c, s;
     load_angles<D, INTER>(a.p, ln, bad ? 0 : pos, c, s);
     signed_row<D, INTER, true>(ln, s);
+    if (bad) {  // whatever these rows hold (NaN, if nothing was written there) is not part of any sum
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) raw[i] = dz[i] = make_uint4(0, 0, 0, 0);
+    }
     __nv_bfloat16* dst = out + b * dx.sb + n * dx.sn;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i, dst += out_hop) {
@@ -527,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_rows_bwd_kernel(const N
       Row c, s;
       load_angles<D, INTER>(a.p, ln, bad ? 0 : pos[i], c, s);
       signed_row<D, INTER, true>(ln, s);
+      if (bad) raw[i] = dz[i] = make_uint4(0, 0, 0, 0);  // as in norm_rope_bwd_kernel
       const uint4 g = turn_row_back<D, INTER>(a.p, ln, c, s, w, raw[i], dz[i], !bad && there[i], dw);
       if (!there[i]) continue;
       *reinterpret_cast<uint4*>(to[i]) = bad ? make_uint4(0, 0, 0, 0) : g;

@@ -3,12 +3,14 @@
 Tolerances are those of the tests of each operator (tests/test_gpu_norm_rope.py, tests/test_gpu_paged.py).
 """
 
+import numpy as np
 import pytest
 import torch
 
 import exact_io_aware_31_gb300 as fa
-from tests.gpu_util import require_gpu
-from tests.test_gpu_norm_rope import pool, ragged, status
+from oracle import serve
+from tests.gpu_util import f64, require_gpu
+from tests.test_gpu_norm_rope import F32, pool, ragged, status
 from tests.test_gpu_paged import CASES, IDS, batch, check, reference
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +90,39 @@ def test_norm_and_append_at_16_byte_addresses(Hq, Hk, N, d):
                            out=aside(torch.zeros_like(out)))
     assert status() == fa.FA_OK
     assert torch.equal(out, out2) and torch.equal(kp, kp2) and torch.equal(vp, vp2)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("eps", [1e-5, 0.0])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,Hk,d", [(17, 9, 64), (9, 16, 128), (8, 8, 64), (4, 2, 128), (1, 1, 64), (1, 2, 128)])
+def test_rows_without_a_position_are_in_no_gradient(Hq, Hk, d, fill, eps, interleaved):
+    """Padding rows (position -1, or past the table) hold NaN or infinities, in x, in dz or in both: their dq and dk
+    are zero, and the weights' gradients are those of the other rows.  Each kernel variant of the gradient."""
+    B, N = 2, 41
+    g = torch.Generator().manual_seed(13)
+    x = [torch.randn(B, h, N, d, generator=g).bfloat16().cuda() for h in (Hq, Hk)]
+    dz = [torch.randn(t.shape, generator=g).bfloat16().cuda() for t in x]
+    w = [(1 + 0.3 * torch.randn(d, generator=g)).cuda() for _ in "qk"]
+    pos = torch.arange(N, dtype=torch.int32).repeat(B, 1)
+    pos[0, 5:9], pos[1, ::7], pos[1, 40] = -1, N, 2 ** 31 - 1
+    gone = ((pos < 0) | (pos >= N))
+    at = torch.where(gone, 0, pos).numpy()
+    kw = dict(rope=fa.rope_table(N, d), positions=pos.cuda(), eps=eps, interleaved=interleaved)
+    refs = []
+    for t, z, wi in zip(x, dz, w):
+        z = f64(z) * ~gone.numpy()[:, None, :, None]
+        size = np.abs(z).max(-1, keepdims=True) * 2 * np.abs(f64(t)) / np.sqrt((f64(t) ** 2).mean(-1, keepdims=True) + eps)
+        bound = ((size[..., 0].size + 16) * 2.0 ** -24 + F32) * size.reshape(-1, d).sum(0)
+        refs.append((serve.norm_rope_grad(z, f64(t), f64(wi), eps, f64(kw["rope"]), at, interleaved)[1], bound))
+    clean = fa.qk_norm_rope_backward(*dz, *x, *w, **kw)
+    for in_x, in_dz in ((True, True), (True, False), (False, True)):
+        mask = gone.cuda()[:, None, :, None]
+        x2 = [t.masked_fill(mask, fill) if in_x else t for t in x]
+        dz2 = [t.masked_fill(mask, fill) if in_dz else t for t in dz]
+        got = fa.qk_norm_rope_backward(*dz2, *x2, *w, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, clean))
+        for dx, dw, (ref, bound) in zip(got[:2], got[2:], refs):
+            assert bool((dx.masked_select(mask) == 0).all())
+            assert (np.abs(f64(dw) - ref) <= bound).all()
+    assert status() == fa.FA_ERR_DEVICE_INDEX

@@ -337,13 +337,6 @@ __global__ void __launch_bounds__(384, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  // Rows of a query tile that no copy fills (G does not divide 32): zero, as they
-  // have a part in their warp's votes on rescaling, which must be the same on every run.
-  if (tt * p.G < kTileRows || t4 * p.G < kTileRows / 4) {
-    for (int i = threadIdx.x; i < 2 * C::kTileBytes / 16; i += C::kThreads)
-      reinterpret_cast<uint4*>(sm + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_map(&tm_q);
     tma_prefetch_map(&tm_q4);
@@ -737,6 +730,10 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     int tail_row0 = 0, tail_tok = 0, tail_hk = 0, has_tail = 0, has_head = 0;  // for the header
     float m_run = -INFINITY, l_run = 0.f;  // running maximum (log2 units) and sum of this row, in this warp's columns
+    // Of rescaling (log2 units).  Infinite for a row that is no token's: what such rows
+    // hold (neighbours' queries, leftovers where G does not divide 32) must not decide
+    // when the warp rescales, as that is seen in the last bits of the others.
+    float threshold = kRescaleThreshold;
     // One key tile: NC columns from c0 on; MASK: column c is seen iff c <= cut.
     auto tile = [&](auto nc, auto masked, int c0, bool first, int cut) {
       constexpr int NC = decltype(nc)::value;
@@ -759,7 +756,7 @@ __global__ void __launch_bounds__(384, 1)
       if (first) {
         m_run = mx2;
       } else {
-        const bool need = mx2 > m_run + kRescaleThreshold;
+        const bool need = mx2 > m_run + threshold;
         if (__any_sync(0xffffffffu, need)) {
           // O_t is quiescent: this S was committed after P V of this half's last tile
           const float m_new = fmaxf(m_run, mx2);
@@ -840,6 +837,7 @@ __global__ void __launch_bounds__(384, 1)
       const int lim = !valid ? -1 : p.causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
       // the tile's first row's: up to it no key tile needs a mask
       const int lim0 = p.causal ? min(past + g.tok0 + tile0, w.q.kv - 1) : w.q.kv - 1;
+      threshold = valid ? kRescaleThreshold : INFINITY;
       m_run = -INFINITY;
       l_run = 0.f;
       if (!SHORT && cnt > 0 && guard) {

@@ -126,3 +126,37 @@ def test_rows_without_a_position_are_in_no_gradient(Hq, Hk, d, fill, eps, interl
             assert bool((dx.masked_select(mask) == 0).all())
             assert (np.abs(f64(dw) - ref) <= bound).all()
     assert status() == fa.FA_ERR_DEVICE_INDEX
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hk,d", [
+    ([40, 70, 9], [700, 900, 800], 1, 1, 64),        # one query tile, partly filled
+    ([14, 3, 25], [1000, 600, 1500], 15, 3, 128),    # groups of 5: rows that no copy fills
+    ([150, 200, 1], [900, 1100, 500], 3, 1, 128),    # two tiles, the second partly filled
+    ([60, 12, 7], [700, 2000, 640], 20, 1, 64),
+    ([5, 2, 9], [640, 1000, 1300], 12, 1, 64),       # four copies
+])
+def test_a_sequence_is_the_same_bits_whatever_others_hold(q_lens, kv_lens, Hq, Hk, d, hint):
+    """Queries, keys and values of another sequence, or queries behind the last one, change no bit of a sequence's
+    rows: tiles hold rows of neighbours and leftovers, which must have no part in when a row is rescaled."""
+    q, pages, table, cu, lens = batch((q_lens, kv_lens, Hq, Hk, d, 32, False, True))
+    T = q.shape[0]
+    rows = torch.cat([q, torch.zeros(140, Hq, d, dtype=q.dtype, device="cuda")])
+    args = table.cuda(), cu.cuda(), lens.cuda()
+    run = lambda x, p: [t[:T] for t in fa.paged_forward(x, *p, *args, scale=0.11, max_q=hint)]  # noqa: E731
+    want = run(rows, pages)
+    g = torch.Generator().manual_seed(6)
+    noise = lambda *n: (100 * torch.randn(n, generator=g)).bfloat16().cuda()  # noqa: E731
+    for s in (*range(len(q_lens)), None):
+        x, p = rows.clone(), [t.clone() for t in pages]
+        x[T:] = noise(140, Hq, d)
+        keep = torch.ones(T, dtype=torch.bool)
+        if s is not None:
+            keep[cu[s]:cu[s + 1]] = False
+            x[cu[s]:cu[s + 1]] = noise(q_lens[s], Hq, d)
+            used = table[s, :-(-kv_lens[s] // 32)].long()
+            for t in p:
+                t[used.cuda()] = noise(len(used), *t.shape[1:])
+        for a, b in zip(run(x, p), want):
+            assert torch.equal(a[keep.cuda()], b[keep.cuda()])
+    assert status() == fa.FA_OK

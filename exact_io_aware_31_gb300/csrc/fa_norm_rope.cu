@@ -29,7 +29,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "../../include/fa.h"
 #include "fa_norm_rope.cuh"
 #include "sm103_ptx.cuh"
 
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const Nor
       const uint4 z = turn_row<D, INTER>(a.p, ln, c, s, raw[i], a.p.norm ? r[i] : 1.f);
       if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : z;
     }
-    if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+    if (bad && lane == 0) record_index(a.p.status);
   }
 }
 
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, STEPS == 4 ? 2 : 3) norm_rope_bwd_ke
                                                          !bad && h0 + i * I::RPW < H, dw);
       if (h0 + i * I::RPW < H) *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0, 0, 0, 0) : g;
     }
-    if (bad && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+    if (bad && lane == 0) record_index(a.p.status);
   }
   if (a.partial != nullptr) store_partial<D>(dw, ln.l, sub, a.partial);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_rows_kernel(const NormR
       if (!there[i]) continue;
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out[which]) + to[i]) =
           bad[i] ? make_uint4(0, 0, 0, 0) : z;
-      if (bad[i] && ln.l == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+      if (bad[i] && ln.l == 0) record_index(a.p.status);
     }
   }
 }
@@ -536,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_rows_bwd_kernel(const N
       const uint4 g = turn_row_back<D, INTER>(a.p, ln, c, s, w, raw[i], dz[i], !bad && there[i], dw);
       if (!there[i]) continue;
       *reinterpret_cast<uint4*>(to[i]) = bad ? make_uint4(0, 0, 0, 0) : g;
-      if (bad && ln.l == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+      if (bad && ln.l == 0) record_index(a.p.status);
     }
   }
   if (a.partial != nullptr) store_partial<D>(dw, ln.l, sub, a.partial);
@@ -629,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendL
   const int at = bad ? 0 : (int)pos;
   const int page = bad || end <= cq ? -1 : __ldg(a.page_table + (size_t)sq * a.max_pages + (at >> a.page_log2));
   const bool lost = page < 0 || page >= a.num_pages;  // no slot
-  if ((bad || (lost && end > cq)) && lane == 0) atomicExch(a.p.status, FA_ERR_DEVICE_INDEX);
+  if ((bad || (lost && end > cq)) && lane == 0) record_index(a.p.status);
 #pragma unroll 1
   while (true) {
     const int which = chunk < cq ? 0 : chunk < cq + ck ? 1 : 2;

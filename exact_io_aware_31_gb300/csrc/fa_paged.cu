@@ -53,7 +53,6 @@
 
 #include <type_traits>
 
-#include "../../include/fa.h"
 #include "fa_common.cuh"
 #include "fa_paged.cuh"
 #include "fa_paged_plan.cuh"
@@ -182,7 +181,7 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
     before = total + block_scan<THREADS>(per_head * p.Hk, plan->scan, &part);
     total += part;
   }
-  if (bad) atomicExch(p.status, FA_ERR_DEVICE_INDEX);
+  if (bad) record_index(p.status);
   // The sequences that the borders lie in.
   const int ctas = ctas_for<D>(total, gridDim.x);
   const long long share = ctas > 0 ? div_long(total, ctas) : 0;
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(384, 1)
         if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
       }
       if (!ok) *abort_flag = 1;
-      if (lost) atomicExch(status, FA_ERR_DEVICE_INDEX);
+      if (lost) record_index(status);
       // Drain: every copy this warp started lands before the block ends.
 #pragma unroll
       for (int b = 0; b < 2; ++b)

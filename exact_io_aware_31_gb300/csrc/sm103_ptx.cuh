@@ -17,7 +17,12 @@ enum : int {
   kDevOk = 0,
   kDevTimeout = 5,   // FA_ERR_DEVICE_TIMEOUT
   kDevInternal = 6,  // FA_ERR_INTERNAL
+  kDevIndex = 7,     // FA_ERR_DEVICE_INDEX
 };
+
+// An index outside its table: recorded where nothing else is.  The call's other
+// results hold, so it must not hide a kernel that gave up.
+__device__ __forceinline__ void record_index(int* status) { atomicCAS(status, kDevOk, kDevIndex); }
 
 // Shared-memory tiles are laid out from the dynamic shared memory base, which
 // must be 1024-byte aligned for the 128-byte swizzle atoms.  On sm_103 the

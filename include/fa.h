@@ -427,9 +427,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device: FA_OK, or FA_ERR_DEVICE_TIMEOUT if any kernel of this
  * library gave up on a bounded wait since the last call (FA_ERR_INTERNAL for
- * a violated layout assumption, FA_ERR_DEVICE_INDEX for a position, page or
- * length outside its table); FA_ERR_CUDA if the
- * synchronisation itself failed.
+ * a violated layout assumption; FA_ERR_DEVICE_INDEX for a position, page or
+ * length outside its table, where neither of those was met); FA_ERR_CUDA if
+ * the synchronisation itself failed.
  */
 int fa_get_device_status(cudaStream_t stream);
 

@@ -63,6 +63,12 @@ namespace {
 
 using namespace paged;
 
+#ifdef FA_TEST_HOOKS
+// Test builds only (-DFA_TEST_HOOKS, never the default library).  2: every CTA
+// takes its shared memory for misaligned.
+static __device__ int g_fa_test_paged;
+#endif
+
 template <int D>
 struct PagedCfg {
   static constexpr int kTileBytes = kTileRows * D * 2;
@@ -288,7 +294,17 @@ __global__ void __launch_bounds__(384, 1)
   const float c2 = fabsf(p.c2);
   int* status = p.status;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (!smem_base_ok(smem_raw, status)) return;
+  bool start_ok = smem_base_ok(smem_raw, status);
+#ifdef FA_TEST_HOOKS
+  if (*reinterpret_cast<volatile int*>(&g_fa_test_paged) == 2) {
+    if (threadIdx.x == 0) atomicExch(status, kDevInternal);
+    start_ok = false;
+  }
+#endif
+  if (!start_ok) {  // nothing for the merge kernel, whatever the workspace holds
+    if (threadIdx.x < kPagedHdr) p.hdr[(size_t)blockIdx.x * kPagedHdr + threadIdx.x] = 0;
+    return;
+  }
   uint8_t* sm = smem_raw;
   // The merge kernel (a programmatic dependent) may start launching: its blocks
   // take the room of CTAs that are done, and wait for this grid's results.
@@ -1271,3 +1287,10 @@ cudaError_t launch_paged(const PagedLaunch& a, cudaStream_t stream) {
 }
 
 }  // namespace fa
+
+#ifdef FA_TEST_HOOKS
+// Test builds only: sets what g_fa_test_paged says (0: nothing).
+extern "C" int fa_test_paged(int mode) {
+  return cudaMemcpyToSymbol(fa::g_fa_test_paged, &mode, sizeof(int)) == cudaSuccess ? 0 : 4;
+}
+#endif

@@ -64,8 +64,9 @@ namespace {
 using namespace paged;
 
 #ifdef FA_TEST_HOOKS
-// Test builds only (-DFA_TEST_HOOKS, never the default library).  2: every CTA
-// takes its shared memory for misaligned.
+// Test builds only (-DFA_TEST_HOOKS, never the default library).  1: softmax
+// warpgroup 0 withholds its first "P ready" arrival of every unit, so that the
+// waits behind it run out.  2: every CTA takes its shared memory for misaligned.
 static __device__ int g_fa_test_paged;
 #endif
 
@@ -869,6 +870,9 @@ __global__ void __launch_bounds__(384, 1)
           if (!(ok = wait_warp<SHORT>(&B.s_full[t], scnt & 1, status))) break;
           ++scnt;
           tile(nc, masked, c0, i == 0, lim - (jfirst + (i << jshift)) * kTileRows - c0);
+#ifdef FA_TEST_HOOKS
+          if (t == 0 && i == 0 && *reinterpret_cast<volatile int*>(&g_fa_test_paged) == 1) continue;
+#endif
           mbar_arrive(&B.p_full[t]);
         }
       };

@@ -6,6 +6,7 @@ Nothing here traps, asserts on the device or spins without a limit.
 """
 
 import ctypes
+import time
 
 import pytest
 import torch
@@ -93,6 +94,25 @@ FORMS = [
     ([200, 300], [4000, 900], 2, 1, 64, 0),   # two
     ([300, 1, 40], [2500, 900, 41], 4, 2, 128, 0),
 ]
+
+
+@pytest.mark.parametrize("form", FORMS, ids=["split", "short", "copies", "one_tile", "two_tiles", "mix"])
+def test_paged_attention_gives_up_and_the_next_call_is_clean(hooks, form):
+    """An arrival withheld in every CTA with work: the roles' waits run out, the merge launch behind them ends."""
+    call, o, lse, ref = paged_call(hooks, *form)
+    assert call() == fa.FA_OK
+    check(o, lse, ref)
+    assert hooks.fa_test_paged(1) == 0
+    try:
+        t0 = time.time()
+        st = call()
+        took = time.time() - t0
+    finally:
+        assert hooks.fa_test_paged(0) == 0
+    assert st == fa.FA_ERR_DEVICE_TIMEOUT, fa.fa_status_string(st)
+    assert took < 30.0
+    assert call() == fa.FA_OK
+    check(o, lse, ref)
 
 
 @pytest.mark.parametrize("form", FORMS, ids=["split", "short", "copies", "one_tile", "two_tiles", "mix"])

@@ -395,18 +395,24 @@ def _elsewhere(first, stream):
 
 def _rows(t, name, shape, dtype, device):
     """Check rows of any layout; their strides without the last (where a size is 1 a stride may be anything)."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device or (steps := t.stride())[-1] != 1):
-        _refuse(t, name, shape, dtype, device)
-    return steps[:-1]
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and (steps := t.stride())[-1] == 1:
+            return steps[:-1]
+    except AttributeError:  # not a tensor
+        pass
+    _refuse(t, name, shape, dtype, device)
 
 
 def _flat(t, name, shape, dtype, device):
     """Check a contiguous tensor (None passes); its address."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        _refuse(t, name, shape, dtype, device)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _refuse(t, name, shape, dtype, device)
 
 
 _rooms = {}
@@ -426,9 +432,12 @@ def _room(workspace, device):
     """Address and bytes of a workspace (None: no room)."""
     if workspace is None:
         return None, 0
-    if workspace.get_device() != device or not workspace.is_contiguous():
-        _refuse(workspace, "workspace", workspace.shape, workspace.dtype, device)
-    return workspace.data_ptr(), workspace.nbytes
+    try:
+        if workspace.get_device() == device and workspace.is_contiguous():
+            return workspace.data_ptr(), workspace.nbytes
+    except AttributeError:  # not a tensor
+        pass
+    _refuse(workspace, "workspace", getattr(workspace, "shape", ()), getattr(workspace, "dtype", None), device)
 
 
 def _shape(t, name, n):
@@ -443,7 +452,7 @@ def _norm_rope_args(d, norm, q_weight, k_weight, eps, rope, interleaved, device)
     """The shared trailing arguments of the norm-and-rotation calls, checked."""
     import torch
     first = q_weight if q_weight is not None else k_weight
-    wt = torch.float32 if first is not None and first.dtype == torch.float32 else torch.bfloat16
+    wt = torch.float32 if getattr(first, "dtype", None) == torch.float32 else torch.bfloat16
     qw, kw = _flat(q_weight, "q_weight", (d,), wt, device), _flat(k_weight, "k_weight", (d,), wt, device)
     rope_len, rope_dim = (0, 0) if rope is None else _shape(rope, "rope", 2)
     return (1 if norm else 0, qw, kw, 1 if wt == torch.float32 else 0, eps,

@@ -160,3 +160,33 @@ def test_a_sequence_is_the_same_bits_whatever_others_hold(q_lens, kv_lens, Hq, H
         for a, b in zip(run(x, p), want):
             assert torch.equal(a[keep.cuda()], b[keep.cuda()])
     assert status() == fa.FA_OK
+
+
+def test_helpers_refuse_what_is_no_tensor():
+    """With the ValueError of a CPU tensor, whichever argument it is."""
+    Hq, Hk, d, page = 2, 1, 64, 16
+    (kp, vp), table = pool([20], Hk, d, page, False, 1)
+    x = torch.randn(3, Hq + 2 * Hk, d, device="cuda").bfloat16()
+    meta = dict(page_table=table.cuda(), cu_seqlens=ragged([3]).cuda(), kv_lens=torch.tensor([20]).int().cuda())
+    append = dict(q=x[:, :Hq], k=x[:, Hq:Hq + Hk], v=x[:, Hq + Hk:], k_pages=kp, v_pages=vp, **meta)
+    attend = dict(q=fa.paged_append(**append), k_pages=kp, v_pages=vp, **meta)
+    turn = dict(q=x[None, :, :Hq].transpose(1, 2), k=x[None, :, Hq:Hq + Hk].transpose(1, 2))
+    z = fa.qk_norm_rope(**turn)
+    back = dict(dq_out=z[0], dk_out=z[1], **turn)
+    extra = dict(q_weight=None, k_weight=None, rope=None)
+    room = dict(workspace=None)
+    for f, args, more in ((fa.paged_append, append, dict(extra, out=None)), (fa.paged_forward, attend, dict(room, out=None, lse=None)),
+                          (fa.qk_norm_rope, turn, dict(extra, positions=None)),
+                          (fa.qk_norm_rope_backward, back, dict(extra, positions=None, **room))):
+        f(**args)
+        for name in (*args, *more):
+            for bad in ([1.0] * 64, np.zeros((3, 2, 64), dtype=np.float32)):
+                with pytest.raises(ValueError):
+                    f(**args | {name: bad})
+    for f, args, names in ((fa.paged_append, append, ("q", "k", "v", "k_pages", "v_pages", "page_table")),
+                           (fa.paged_forward, attend, ("q", "k_pages", "v_pages", "page_table")),
+                           (fa.qk_norm_rope, turn, ("q", "k")), (fa.qk_norm_rope_backward, back, ("q", "k", "dq_out"))):
+        for name in names:
+            with pytest.raises(ValueError):
+                f(**args | {name: None})
+    assert status() == fa.FA_OK

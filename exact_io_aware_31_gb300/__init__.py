@@ -475,8 +475,9 @@ def rope_table(length, rope_dim, base=10000.0, device="cuda"):
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, rope=None, positions=None, eps=1e-6, interleaved=False,
                  norm=True, out=None, stream=None):
     """Norm of queries and keys for each head, then rotation: ``q [B, Hq, N, d]``, ``k [B, Hk, N, d]`` bf16 of any
-    strides (``x.transpose(1, 2)`` of a token-major projection, a slice of a wider row) -> contiguous
-    ``(q_out, k_out)``, what :func:`forward` takes.  ``rope`` is a :func:`rope_table` (None: no rotation),
+    strides that are multiples of 8 (``x.transpose(1, 2)`` of a token-major projection, a slice of a wider row, an
+    ``expand``) -> contiguous ``(q_out, k_out)``, what :func:`forward` takes (where Hk < Hq with keys and values
+    repeated for the query heads of their group).  ``rope`` is a :func:`rope_table` (None: no rotation),
     ``positions`` int32 ``[B, N]`` (None: 0 .. N-1), ``norm=False`` rotates only."""
     where = _elsewhere(q, stream)
     if where is not None:
@@ -563,8 +564,9 @@ def _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens, d, device):
 def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_weight=None, k_weight=None, rope=None,
                  eps=1e-6, interleaved=False, norm=True, out=None, stream=None):
     """Norm and rotate the new tokens' ``q [T, Hq, d]`` and ``k [T, Hk, d]`` at their positions, write keys and values
-    into the cache ``k_pages, v_pages [num_pages, Hk, page_size, d]`` (any strides: a token-major pool is a
-    ``transpose(1, 2)`` view), and return the queries ``[T, Hq, d]`` for :func:`paged_forward`.
+    into the cache ``k_pages, v_pages [num_pages, Hk, page_size, d]`` (strides of whole rows, multiples of 8: a
+    token-major pool is a ``transpose(1, 2)`` view), and return the queries ``[T, Hq, d]`` for :func:`paged_forward`
+    (rows of no sequence are not written).
     ``page_table [S, max_pages]``, ``cu_seqlens [S + 1]`` and ``kv_lens [S]`` (new tokens included) are int32 on
     the device.  ``rope=None, norm=False`` caches k and v as they are."""
     where = _elsewhere(q, stream)
@@ -595,9 +597,9 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
 
 def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,
                   lse=None, workspace=None, stream=None):
-    """Attention of the new tokens ``q [T, Hq, d]`` (any strides) over the paged cache that :func:`paged_append` wrote;
-    returns ``(o [T, Hq, d], lse [T, Hq])``.  ``max_q`` is the longest chunk of the step (0: not known; a hint that
-    selects the kernel variant)."""
+    """Attention of the new tokens ``q [T, Hq, d]`` (strides of whole rows: multiples of 8, at least d) over the paged
+    cache that :func:`paged_append` wrote; returns ``(o [T, Hq, d], lse [T, Hq])``, in which rows of no sequence are
+    not written.  ``max_q`` is the longest chunk of the step (0: not known; a hint that selects the kernel variant)."""
     where = _elsewhere(q, stream)
     if where is not None:
         with where:

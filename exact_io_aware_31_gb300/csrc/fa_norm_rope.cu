@@ -83,13 +83,6 @@ __device__ __forceinline__ float pair_sum(uint64_t v) {
   return lo + hi;
 }
 
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int off = LPR / 2; off > 0; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
 // Where a lane stands in its row.  The rotation is z = y * c + other * s:
 // `other` is the partner column's element (dr / 16 lanes away for split pairs
 // (i, i + dr / 2), the neighbour within the pair for (2i, 2i + 1): INTER), and
@@ -311,7 +304,8 @@ struct Chunk {
   static constexpr int kRows = RPW * STEPS;   // heads a chunk
   __host__ __device__ static int of(int H) { return (H + kRows - 1) / kRows; }
 };
-// CTAs an SM of the forward: at three (80 registers) nothing spills; four and
+// CTAs an SM of the forward: 80 registers at three, in which the kernels of split
+// pairs do not spill (those of neighbouring pairs 4 to 12 bytes a thread); four and
 // five measured 89 and 110 us against 85 (B = 64, N = 1024, 16 + 16 heads, d = 64).
 constexpr int kFwdCtas = 3;
 
@@ -360,9 +354,10 @@ __global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const Nor
 }
 
 // ---------------------------------------------------------------- backward ---
-// Bound by the loads in flight: the rows of x and dz of four steps take 118 registers
-// a thread, two CTAs an SM (B = 64, N = 1024, 16 + 16 heads, d = 64: 152 us, 5.3 of
-// 6.8 TB/s; two steps and three CTAs an SM are slower for many heads, steps_for()).
+// Bound by the loads in flight: the rows of x and dz of four steps take 119 registers
+// a thread, two CTAs an SM (B = 64, N = 1024, 16 + 16 heads, d = 64: 153 us, 5.3 of
+// 6.8 TB/s; two steps and three CTAs an SM, which spill 28 to 40 bytes a thread, are
+// slower for many heads, steps_for()).
 // The weights' gradients of a thread's 8 columns stay in registers over all its
 // tokens; a CTA adds up its warps and writes one row of partial sums, and a
 // second kernel adds those in a fixed order: no atomics, the same bits on every
@@ -593,9 +588,12 @@ __device__ __forceinline__ int find_sequence(const int* cu, int S, int t) {
 // rotation table, or in a page outside the pool) is not cached, and its query
 // row is zero where it has no position.
 // A warp takes one token: one chunk of its heads, or (`span`) all of them, so
-// that the search for its sequence and slot is made once.  Bound by issue slots and
-// load latency (8207 tokens, 32 + 8 heads, d = 128, pages of 16: 39 us, 5.2 TB/s); 64
-// single tokens take 3.9 us, the chain search - page entry - row.
+// that the search for its sequence and slot is made once.  8207 tokens, 32 + 8 heads,
+// d = 128, pages of 16 take 39 us (5.2 TB/s; the copy rate allows 30): issue slots,
+// part of them for what is done again for each chunk of a token's heads (angles and
+// weights loaded and folded; at four steps 60 to 68 bytes a thread spilled at the 64
+// registers of four CTAs an SM), and a chunk's rows are asked for only behind the
+// stores of the last.  64 single tokens take 3.9 us, the chain search - page entry - row.
 template <int D, bool INTER, int STEPS>
 __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendLaunch a) {
   using I = Chunk<D, STEPS>;

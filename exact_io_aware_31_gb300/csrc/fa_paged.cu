@@ -36,12 +36,19 @@
 // SHORT kernels hold only the last form: the host takes them where it was told
 // that chunks are short; a longer chunk is then a row of small units.
 //
+// Rounding: scores, maxima, sums and O are fp32.  P is rounded to bf16 once, as the
+// MMA takes it (its sum takes the fp32 values), for single tokens, too, which run the
+// same MMAs: outputs are 2.0e-3 to 2.3e-3 off (norm of the error by the norm) where
+// the rounding of the output alone makes 1.65e-3.  MMAs that take more of P (tf32)
+// want V in 32 bits as well: twice its shared memory at half the rate.
+//
 // Measured (GB300, d = 128, 32 query and 8 key heads): 2 x 2048 tokens against 16384
-// and 8789 keys 461 us, 1.68 PFLOP/s (88% of the dense rate; the softmax between
-// the MMAs); 64 single tokens against up to 8192 keys 219 us, 6.1 TB/s (91% of the
-// copy rate); one token, 16 heads, 16384 keys 32 us (7 us until the first tile,
-// 4 us of merge).  Small units are bound by the chain from one unit's last tile to
-// the next one's first scores (2 us) and by instruction fetch.
+// and 8789 keys 458 to 471 us, 1.66 PFLOP/s (86% of the dense rate; the softmax between
+// the MMAs), and 508 in a loop of seconds, when the power limit holds the clock near
+// 1.8 of 2.07 GHz (89% of the rate then); 64 single tokens against up to 8192 keys
+// 219 us, 6.1 TB/s (91% of the copy rate); one token, 16 heads, 16384 keys 32 us (7 us
+// until the first tile, 4 us of merge).  Small units are bound by the chain from one
+// unit's last tile to the next one's first scores (2 us) and by instruction fetch.
 //
 // Roles (12 warps): 0-3 and 4-7 softmax warpgroups, 8 producer, 9 MMA issuer,
 // 10 clears the rows of V behind a sequence's end (what lies there in a page is

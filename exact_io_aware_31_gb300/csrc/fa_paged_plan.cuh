@@ -160,6 +160,10 @@ struct Segment {
 __host__ __device__ inline bool same_unit(const Spot& a, const Spot& b) { return a.s == b.s && a.hk == b.hk && a.b == b.b; }
 
 // To the next unit.  P tells what a walk needs to know: `seq(s)` gives a sequence; S, Hk.
+// Empty sequences are passed one by one: four chunks of 75 tokens against 300 keys
+// (32 + 8 heads, d = 128) take 18 us, and 49 among 1020 empty ones.  Passing 32 at a
+// time gained a quarter of that, but batches without empty ones took 3% more, or long
+// chunks 5%: code of the softmax loop.
 template <class P>
 __host__ __device__ inline void walk_skip(const P& p, Walk& w, const Shape& sh) {
   w.at.j = 0;

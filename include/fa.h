@@ -231,7 +231,10 @@ int fa_bwd_dq_convert(void* dq, int B, int H, int N, int d, float scale, const v
 /*
  * Norm of queries and keys for each head with the position rotation in the
  * same pass: from a projection's output to the operands fa_fwd reads, in one
- * launch.  For a head row x at position p, with r = 1 / sqrt(mean(x^2) + eps):
+ * launch.  (fa_fwd and fa_bwd take one number of heads: with Hq != Hk the
+ * caller repeats keys and values for the query heads of their group, and sums
+ * dk and dv over them.  fa_fwd_paged takes grouped heads as they are.)
+ * For a head row x at position p, with r = 1 / sqrt(mean(x^2) + eps):
  *
  *     y = w * x * r                                (norm = 1; y = x for norm = 0)
  *     z_a = y_a c - y_b s,  z_b = y_b c + y_a s    for each pair (a, b) of columns
@@ -256,8 +259,9 @@ int fa_bwd_dq_convert(void* dq, int B, int H, int N, int d, float scale, const v
  *   rope_dim  multiple of 16, 0 <= rope_dim <= d
  *   positions in   [B, N] int32, or NULL for 0 .. N-1 (then N <= rope_len)
  *
- * A position outside [0, rope_len) gives a zero row (and a zero gradient row)
- * and records FA_ERR_DEVICE_INDEX in the device status word.  Head counts may
+ * A position outside [0, rope_len) gives a zero row, and a zero gradient row
+ * that has no part in the weights' gradients whatever the row holds, and
+ * records FA_ERR_DEVICE_INDEX in the device status word.  Head counts may
  * differ (grouped key heads), up to 2048 each.  Tensors are not limited to 2^31
  * elements here; B*N < 2^31 and B*N*(Hq+Hk) < 2^34.
  */
@@ -280,7 +284,9 @@ int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int 
  *                   (the same bits on every run); NULL where not wanted;
  *                   both must be NULL with norm = 0
  *   workspace  fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned;
- *              may be NULL when no weight gradient is wanted
+ *              may be NULL when no weight gradient is wanted.  Its contents on
+ *              entry do not matter; calls that may overlap need one each, and a
+ *              captured graph's must live as long as the graph
  *
  * One launch, or two with weight gradients.
  */
@@ -305,7 +311,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *  in elements, multiples of 8, >= d (of no meaning where the size is 1); both
  *  head-major ([pages, Hk, page_size, d])
  *  and token-major ([pages, page_size, Hk, d]) pools are covered.  page_size is
- *  a power of two, 16 to 65536.
+ *  a power of two, 16 to 65536.  Strides are below 2^38, and max_pages *
+ *  page_size is at most 2^30.
  *  page_table [S, max_pages] int32 (contiguous): key j of sequence s is row
  *  j mod page_size of page page_table[s][j / page_size].  Entries behind a
  *  sequence's end are not read.  Sequences may share pages that they only read.
@@ -330,7 +337,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  * A token with no position in [0, min(rope_len, max_pages*page_size)) gets a
  * zero q_out row and is not cached; one whose page lies outside the pool is
  * not cached; each records FA_ERR_DEVICE_INDEX.  Two tokens of one call must
- * not share a slot (then either may win).
+ * not share a slot (then either may win).  Up to 2048 heads of each kind;
+ * T*(Hq+2Hk) < 2^34.
  */
 int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_pages, void* v_pages,
                     const int* page_table, const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq, int Hk,
@@ -348,7 +356,7 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  * h / (Hq / Hk)).
  *
  *   q         in   bf16 [T, Hq, d]: element (t, h, c) at t*stride_t + h*stride_h
- *                  + c (multiples of 8, >= d)
+ *                  + c (multiples of 8, >= d, below 2^31)
  *   o         out  contiguous [T, Hq, d] bf16
  *   lse       out  contiguous [T, Hq] fp32, natural-log logsumexp of each row;
  *                  may be NULL
@@ -368,8 +376,14 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  * outside the pool count as zeros with zero values, lengths outside their
  * range are cut to it; both record FA_ERR_DEVICE_INDEX.  Two launches.  Results
  * are the same bits on every run.
+ * A sequence's rows depend on no other's contents, nor on rows behind the last
+ * one.
+ * Probabilities are rounded to bf16 before P V for single tokens, too, as in
+ * fa_fwd (fa_fwd_splitkv keeps them in fp32 for one or two queries): outputs
+ * are within 2^-8 |o| + 2^-8 sum_j p_j |v_j| of exact ones, and the errors of
+ * the scores.
  * Hq must be a multiple of Hk with Hq / Hk <= 128 (FA_ERR_UNSUPPORTED above);
- * T < 2^30.
+ * Hq < 2^15, T < 2^30.
  */
 int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse, const int* page_table,
                  const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq, int Hk, int d, int num_pages,

@@ -190,3 +190,23 @@ def test_helpers_refuse_what_is_no_tensor():
             with pytest.raises(ValueError):
                 f(**args | {name: None})
     assert status() == fa.FA_OK
+
+
+def test_nothing_to_do():
+    """No token, no sequence, sequences without a token: nothing is written and nothing recorded."""
+    Hq, Hk, d, page = 4, 2, 64, 16
+    (kp, vp), table = pool([20, 40], Hk, d, page, False, 1)
+    kept = kp.clone(), vp.clone()
+    lens = torch.tensor([20, 40], dtype=torch.int32).cuda()
+    rope = fa.rope_table(64, d)
+    for T, meta in ((0, (table.cuda(), ragged([0, 0]).cuda(), lens)), (5, (table.cuda(), ragged([0, 0]).cuda(), lens)),
+                    (5, (table[:0].cuda(), ragged([]).cuda(), lens[:0])), (0, (table[:0, :0].cuda(), ragged([]).cuda(), lens[:0]))):
+        x = torch.randn(T, Hq + 2 * Hk, d, device="cuda").bfloat16()
+        out = torch.full((T, Hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+        o, lse = torch.full_like(out, 6.0), torch.full((T, Hq), 7.0, device="cuda")
+        fa.paged_append(x[:, :Hq], x[:, Hq:Hq + Hk], x[:, Hq + Hk:], kp, vp, *meta, rope=rope, out=out)
+        for hint in (0, 1):
+            fa.paged_forward(x[:, :Hq], kp, vp, *meta, max_q=hint, out=o, lse=lse)
+        assert status() == fa.FA_OK
+        assert bool((out == 5).all()) and bool((o == 6).all()) and bool((lse == 7).all())
+    assert torch.equal(kp, kept[0]) and torch.equal(vp, kept[1])

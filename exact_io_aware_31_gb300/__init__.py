@@ -12,11 +12,12 @@ the split-KV decode forward (``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_size``), the norm and rotation of queries and keys
 (``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
 ``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``,
-``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``),
+``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``, ``fa_fwd_paged_shared``,
+``fa_fwd_paged_shared_workspace_size``),
 ``fa_get_device_status``, ``fa_status_string``.
 Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`,
 :func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`,
-:func:`paged_forward`.
+:func:`paged_forward`, :func:`paged_forward_shared`.
 """
 
 from __future__ import annotations
@@ -30,8 +31,9 @@ __all__ = [
     "fa_bwd_preprocess", "fa_bwd_dkdv", "fa_bwd_dq_convert", "fa_bwd_noalloc", "NOALLOC_SCRATCH_BYTES",
     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "decode_forward",
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
-    "fa_fwd_paged", "fa_fwd_paged_workspace_size",
+    "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_fwd_paged_shared", "fa_fwd_paged_shared_workspace_size",
     "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "paged_append", "paged_forward",
+    "paged_forward_shared",
     "fa_get_device_status", "fa_status_string", "forward", "backward", "EXPORTED_SYMBOLS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_WORKSPACE", "FA_ERR_CUDA",
     "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INTERNAL", "FA_ERR_DEVICE_INDEX",
@@ -53,7 +55,8 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_fp8", "fa_bwd", "fa_bwd_workspace_size", "
                     "fa_bwd_dkdv",
                     "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size",
                     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
-                    "fa_fwd_paged", "fa_fwd_paged_workspace_size",
+                    "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_fwd_paged_shared",
+                    "fa_fwd_paged_shared_workspace_size",
                     "fa_get_device_status", "fa_status_string")
 
 # Size of the library-owned scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES).
@@ -117,6 +120,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_paged_append.argtypes = [vp] * 9 + [i] * 8 + [ll] * 12 + [i, vp, vp, i, f, vp, i, i, i, vp]
     lib.fa_fwd_paged.restype = i
     lib.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [ll] * 8 + [f, i, i, vp, sz, vp]
+    lib.fa_fwd_paged_shared.restype = i
+    lib.fa_fwd_paged_shared.argtypes = [vp] * 10 + [i] * 9 + [ll] * 8 + [f, i, i, vp, sz, vp]
+    lib.fa_fwd_paged_shared_workspace_size.restype = sz
+    lib.fa_fwd_paged_shared_workspace_size.argtypes = [i] * 5
     lib.fa_fwd_paged_workspace_size.restype = sz
     lib.fa_fwd_paged_workspace_size.argtypes = [i]
     lib.fa_get_device_status.restype = i
@@ -235,6 +242,21 @@ def fa_fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, T
 
 def fa_fwd_paged_workspace_size(d) -> int:
     return load_library().fa_fwd_paged_workspace_size(d)
+
+
+def fa_fwd_paged_shared(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, groups, prefix_lens, T, S,
+                        num_groups, Hq, Hk, d, num_pages, page_size, max_pages, q_stride_t, q_stride_h, kp_stride_p,
+                        kp_stride_h, kp_stride_r, vp_stride_p, vp_stride_h, vp_stride_r, scale, causal, max_q,
+                        workspace, workspace_bytes, stream) -> int:
+    return load_library().fa_fwd_paged_shared(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, groups,
+                                              prefix_lens, T, S, num_groups, Hq, Hk, d, num_pages, page_size,
+                                              max_pages, q_stride_t, q_stride_h, kp_stride_p, kp_stride_h,
+                                              kp_stride_r, vp_stride_p, vp_stride_h, vp_stride_r, scale, causal,
+                                              max_q, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_shared_workspace_size(T, S, num_groups, Hq, d) -> int:
+    return load_library().fa_fwd_paged_shared_workspace_size(T, S, num_groups, Hq, d)
 
 
 def fa_get_device_status(stream) -> int:
@@ -629,4 +651,46 @@ def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=No
                                      ws, wbytes, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged")
+    return out, lse
+
+
+def paged_forward_shared(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, groups, prefix_lens, scale=None,
+                         causal=True, max_q=0, out=None, lse=None, workspace=None, stream=None):
+    """:func:`paged_forward` for a batch whose sequences share their first keys, which are read and multiplied once for
+    each group: ``groups [n + 1]`` int32 on the device holds each group's first sequence and the last one's end,
+    ``prefix_lens [n]`` how many keys its sequences share (any number that is true: what is not worth computing once
+    is not).  Same results up to rounding."""
+    where = _elsewhere(q, stream)
+    if where is not None:
+        with where:
+            return paged_forward_shared(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, groups, prefix_lens,
+                                        scale, causal, max_q, out, lse, workspace)
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    T, Hq, d = _shape(q, "q", 3)
+    dev = q.get_device()
+    meta, S, Hk, num_pages, page_size, max_pages, steps = _cache_args(k_pages, v_pages, page_table, cu_seqlens, kv_lens,
+                                                                      d, dev)
+    n = _shape(prefix_lens, "prefix_lens", 1)[0]
+    shared = _flat(groups, "groups", (n + 1,), i32, dev), _flat(prefix_lens, "prefix_lens", (n,), i32, dev)
+    sq = _rows(q, "q", (T, Hq, d), bf16, dev)
+    if out is None:
+        out = torch.empty(T, Hq, d, dtype=bf16, device=q.device)
+    else:
+        _flat(out, "out", (T, Hq, d), bf16, dev)
+    if lse is None:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    else:
+        _flat(lse, "lse", (T, Hq), torch.float32, dev)
+    if workspace is None:
+        need = load_library().fa_fwd_paged_shared_workspace_size(T, S, n, Hq, d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws, wbytes = _room(workspace, dev)
+    st = load_library().fa_fwd_paged_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                            lse.data_ptr(), *meta, *shared, T, S, n, Hq, Hk, d, num_pages, page_size,
+                                            max_pages, *sq, *steps, d ** -0.5 if scale is None else scale,
+                                            1 if causal else 0, max_q, ws, wbytes,
+                                            torch._C._cuda_getCurrentRawStream(dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_paged_shared")
     return out, lse

@@ -113,6 +113,7 @@ struct PagedCfg {
 
 // ------------------------------------------------------------------- the plan --
 // The kernel's arguments as a walk (fa_paged_plan.cuh) sees them.
+template <bool SHARED>
 struct Work {
   const int* cu;
   const int* lens;
@@ -128,14 +129,35 @@ struct Work {
   }
 };
 
+// Where sequences share keys: the entries that shared_plan_kernel wrote.
+template <>
+struct Work<true> {
+  const SharedEntry* list;
+  int S, Hk;
+  __device__ __forceinline__ explicit Work(const PagedParams& p)
+      : list(reinterpret_cast<const SharedEntry*>(costs(p) + shared_plan_costs(p.S + p.num_groups))),
+        S(__ldcg(&p.plan->entries)),
+        Hk(p.Hk) {}
+  static __device__ __forceinline__ const long long* costs(const PagedParams& p) {
+    return reinterpret_cast<const long long*>(p.plan + 1);
+  }
+  __device__ __forceinline__ SharedSeq seq(int s) const {
+    const int4 a = __ldcg(&list[s].seq), b = __ldcg(&list[s].how);
+    SharedSeq q;
+    q.q0 = a.x, q.qn = a.y, q.kv = a.z, q.row = a.w, q.page0 = b.x, q.kind = b.y;
+    return q;
+  }
+};
+
 // The CTA's run in shared memory.
+template <class Q>
 struct Plan {
   Spot at[2];      // its borders
-  Seq q[2];        // the sequences they lie in
+  Q q[2];          // the sequences they lie in
   long long y[2];  // while it is made: places in the cost of their key heads
   long long scan[12];
 };
-static_assert(sizeof(Plan) <= 192, "plan size");
+static_assert(sizeof(Plan<SharedSeq>) <= 192, "plan size");
 
 // Token of a row: row / G for rows up to 256 and G up to 128.  With m = 65536 / G + 1
 // the product is row / G + row * e / (65536 G) for an e of 1 .. G: too little to
@@ -173,11 +195,29 @@ __device__ long long block_scan(long long v, long long* warps, long long* total)
   return before + inc - v;
 }
 
+// The borders' blocks: every thread tries some.
+template <int D, int THREADS, class Q>
+__device__ __forceinline__ void place_borders(int S, const Shape& sh, Plan<Q>* plan) {
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (plan->at[e].s >= S) continue;
+    const Q sq = plan->q[e];
+    for (int b = threadIdx.x; b * sh.ut < sq.qn; b += THREADS) {
+      int j;
+      if (place<D>(sq, plan->y[e], b, sh, j)) {
+        plan->at[e].b = b;
+        plan->at[e].j = j;
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // Every thread of the CTA.  Fills *plan: the run of this CTA.  The borders are
 // computed alike by the CTAs on both sides of them.
 template <int D, int THREADS>
-__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
-  const Work work(p);
+__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<Seq>* plan) {
+  const Work<false> work(p);
   const int tid = threadIdx.x;
   bool bad = false;
   Seq q = {0, 0, 0};
@@ -223,20 +263,35 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan* plan) {
     }
   }
   __syncthreads();
-  // Their blocks: every thread tries some.
+  place_borders<D, THREADS>(p.S, sh, plan);
+}
+
+// The same where the entries' costs have been added up before.
+template <int D, int THREADS>
+__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<SharedSeq>* plan) {
+  const Work<true> work(p);
+  const long long* cost = Work<true>::costs(p);
+  const long long total = __ldcg(cost + work.S);
+  const int ctas = ctas_for<D>(total, gridDim.x);
+  const long long share = ctas > 0 ? div_long(total, ctas) : 0;
+  const long long x[2] = {border(total, share, blockIdx.x, ctas), border(total, share, blockIdx.x + 1, ctas)};
+  if (threadIdx.x < 2) plan->at[threadIdx.x] = {work.S, 0, 0, 0};  // a border at the end
+  __syncthreads();
+  for (int s = threadIdx.x; s < work.S; s += THREADS) {
+    const long long before = __ldcg(cost + s), behind = __ldcg(cost + s + 1);
 #pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    if (plan->at[e].s >= p.S) continue;
-    const Seq sq = plan->q[e];
-    for (int b = tid; b * sh.ut < sq.qn; b += THREADS) {
-      int j;
-      if (place<D>(sq, plan->y[e], b, sh, j)) {
-        plan->at[e].b = b;
-        plan->at[e].j = j;
-      }
+    for (int e = 0; e < 2; ++e) {
+      const long long at = e ? x[1] : x[0];
+      if ((int)blockIdx.x + e > ctas || at < before || at >= behind) continue;
+      const long long per_head = div_long(behind - before, p.Hk);
+      const int hk = (int)div_long(at - before, per_head);
+      plan->at[e] = {s, hk, 0, 0};
+      plan->y[e] = at - before - hk * per_head;
+      plan->q[e] = work.seq(s);
     }
   }
   __syncthreads();
+  place_borders<D, THREADS>(work.S, sh, plan);
 }
 
 struct PagedBars {
@@ -291,12 +346,17 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
-template <int D, bool SHORT>
+// SHARED: the batch's sequences share keys (fa_paged_shared.cu): the units are those of a
+// list of entries, and rows whose group shares keys are partial rows in any case.
+template <int D, bool SHORT, bool SHARED>
 __global__ void __launch_bounds__(384, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q4,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ PagedParams p) {
   using C = PagedCfg<D>;
+  using Q = std::conditional_t<SHARED, SharedSeq, Seq>;
+  using Walk = WalkOf<Q>;
+  static_assert(!(SHORT && SHARED), "no such form");
   // A negative scale: S is computed negated and the softmax uses |c2|.
   const uint32_t s_negate = p.c2 < 0.f ? kIdescNegateA : 0u;
   const float c2 = fabsf(p.c2);
@@ -339,7 +399,7 @@ __global__ void __launch_bounds__(384, 1)
   B.seg_empty = B.seg_full + C::kSegs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
-  Plan* plan = reinterpret_cast<Plan*>(sm + C::kOffPlan);
+  Plan<Q>* plan = reinterpret_cast<Plan<Q>*>(sm + C::kOffPlan);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int tt = p.tile_tokens, t4 = p.copy_tokens;
@@ -369,13 +429,14 @@ __global__ void __launch_bounds__(384, 1)
   // Short chunks: the plan behind the barrier (64 sequences of 8 tokens against up to
   // 1024 keys, d = 64: 47.3 -> 45.4 us).  The other way round with the other forms,
   // whose softmax loops come out slower so (2 x 2048 tokens: 458 -> 463 us).
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // the list of entries
   if constexpr (!SHORT) make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_before();
   __syncthreads();
   if constexpr (SHORT) make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const Work work(p);
+  const Work<SHARED> work(p);
   auto form_of = [&](const Segment& g) { return SHORT ? kFourCopies : sh.form(g.ntok); };
   // The roles' walk through the run: `step` goes to the next segment, the first one
   // included.  With short chunks warp 11 walks for all and the others read what it
@@ -435,7 +496,11 @@ __global__ void __launch_bounds__(384, 1)
       };
       while (step(place, ok)) {
         const Form form = form_of(g);
-        const int* table = p.page_table + (size_t)w.at.s * p.max_pages;
+        const int* table;
+        if constexpr (SHARED)
+          table = p.page_table + (size_t)w.q.row * p.max_pages + w.q.page0;
+        else
+          table = p.page_table + (size_t)w.at.s * p.max_pages;
         const int pages = (w.q.kv + (1 << p.page_log2) - 1) >> p.page_log2;
         // this lane's page of key tile j, asked for a tile ahead
         auto page_at = [&](int j) {
@@ -857,9 +922,10 @@ __global__ void __launch_bounds__(384, 1)
       const int cnt = two ? (t ? nt : tile0_count(w.q, g, sh)) : (nt + 1 - t) / 2;
       const int jfirst = g.j0 + (two ? 0 : t), jshift = two ? 0 : 1;  // every second key tile
       const int past = w.q.kv - w.q.qn;
-      const int lim = !valid ? -1 : p.causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
+      const bool causal = causal_in(w.q, p.causal);
+      const int lim = !valid ? -1 : causal ? min(past + tok, w.q.kv - 1) : w.q.kv - 1;  // last key it sees
       // the tile's first row's: up to it no key tile needs a mask
-      const int lim0 = p.causal ? min(past + g.tok0 + tile0, w.q.kv - 1) : w.q.kv - 1;
+      const int lim0 = causal ? min(past + g.tok0 + tile0, w.q.kv - 1) : w.q.kv - 1;
       threshold = valid ? kRescaleThreshold : INFINITY;
       m_run = -INFINITY;
       l_run = 0.f;
@@ -908,7 +974,26 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
       tc_fence_after();
+      // Rows of a whole unit go to the output, those of others (and, where keys are shared,
+      // all of its group's) to the workspace.
       const bool whole = g.j0 == 0 && g.j1 == g.n;
+      bool direct = whole;
+      size_t apart = 0;  // the output rows' partial ones
+      if constexpr (SHARED) {
+        direct = whole && w.q.kind == kAlone;
+        apart = (size_t)gridDim.x * (2 * kPagedRows) + (w.q.kind == kPrefix ? 0 : (size_t)p.T * p.Hk * p.G);
+      }
+      // ... says where the merge finds a row that is not there (r_unit: row of the unit)
+      auto mark = [&](size_t out, int r_unit) {
+        if constexpr (SHARED) {
+          float2* at = reinterpret_cast<float2*>(p.part_ml) + apart + out;
+          if (direct)
+            *at = make_float2(0.f, kRowDone);
+          else if (!whole && g.j0 == 0)
+            *at = make_float2(__int_as_float((int)blockIdx.x * kPagedRows + r_unit),
+                              w.q.kind == kRest ? kRowCutOfRest : kRowCut);
+        }
+      };
       const size_t out_row = (size_t)(w.q.q0 + tok) * (p.Hk * p.G) + w.at.hk * p.G + rhead;
       const size_t slot = ((size_t)blockIdx.x * 2 + (g.j0 > 0 ? 0 : 1)) * kPagedRows;
       if (four) {
@@ -964,16 +1049,18 @@ __global__ void __launch_bounds__(384, 1)
               l = fmaf(wt, part[i].y, l);
               o.x = fmaf(wt, x.x, o.x), o.y = fmaf(wt, x.y, o.y), o.z = fmaf(wt, x.z, o.z), o.w = fmaf(wt, x.w, o.w);
             }
-            if (whole) {
-              const int qt = token_of(p, q_row);
-              const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.at.hk * p.G + (q_row - qt * p.G);
+            const int qt = token_of(p, q_row);
+            const size_t at = (size_t)(w.q.q0 + g.tok0 + qt) * (p.Hk * p.G) + w.at.hk * p.G + (q_row - qt * p.G);
+            if (c == 0) mark(at, q_row);
+            if (direct) {
               const float inv = l == 0.f ? 0.f : 1.f / l;
               reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D)[c] =
                   make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
               if (c == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
             } else {
-              reinterpret_cast<float4*>(p.part_o + (slot + q_row) * D)[c] = o;
-              if (c == 0) reinterpret_cast<float2*>(p.part_ml)[slot + q_row] = make_float2(m, l);
+              const size_t part_row = SHARED && whole ? apart + at : slot + q_row;
+              reinterpret_cast<float4*>(p.part_o + part_row * D)[c] = o;
+              if (c == 0) reinterpret_cast<float2*>(p.part_ml)[part_row] = make_float2(m, l);
             }
           }
           if (r0 + 8 < tile_rows) {
@@ -1013,10 +1100,11 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (busy && (two || merge || t == 0)) {  // (a single key tile: half 0 alone)
           const bool empty = l_out == 0.f;       // saw no key: zero, whatever O holds
-          const float scale_o = whole ? (empty ? 0.f : 1.f / l_out) : 1.f;
+          const float scale_o = direct ? (empty ? 0.f : 1.f / l_out) : 1.f;
           w0 *= scale_o;
           w1 *= scale_o;
-          const size_t part = slot + (two ? t * 128 : 0) + r;
+          const int unit_row = (two ? t * 128 : 0) + r;
+          const size_t part = SHARED && whole ? apart + out_row : slot + unit_row;
           const int c_lo = merge ? t * (D / 2) : 0, c_hi = merge ? c_lo + D / 2 : D;
           const uint32_t t_o1 = tmem_lane_col(tbase, quarter * 32, C::kColO + 128 * (1 - t));
 #pragma unroll 1
@@ -1044,7 +1132,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int k = 0; k < 32; ++k) v[k] = 0u;
             }
             if (!valid) continue;
-            if (whole) {
+            if (direct) {
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
                 uint32_t y[4];
@@ -1065,7 +1153,8 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           if (valid && (!merge || t == 0)) {
-            if (!whole)
+            mark(out_row, unit_row);
+            if (!direct)
               reinterpret_cast<float2*>(p.part_ml)[part] = make_float2(m_out, l_out);
             else if (p.lse)
               p.lse[out_row] = empty ? -INFINITY : (m_out + __log2f(l_out)) * kLn2;
@@ -1104,6 +1193,8 @@ __global__ void __launch_bounds__(384, 1)
 
   tc_fence_before();
   __syncthreads();
+  // Rows of the workspace are only good if every CTA went through to its end.
+  if (SHARED && threadIdx.x == 0) p.hdr[(size_t)blockIdx.x * kPagedHdr + kPagedEnded] = !aborted(abort_flag);
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
@@ -1261,10 +1352,10 @@ __global__ void __launch_bounds__(256, AHEAD == 2 ? 4 : 2) paged_merge_kernel(co
   }
 }
 
-template <int D, bool SHORT>
+template <int D, bool SHORT, bool SHARED>
 cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   using C = PagedCfg<D>;
-  auto kern = paged_kernel<D, SHORT>;
+  auto kern = paged_kernel<D, SHORT, SHARED>;
   // The register split inside the kernel assumes it was built with exactly
   // kLaunchRegs registers a thread: refuse to launch any other build.
   static const bool regs_ok = [&] {
@@ -1274,17 +1365,27 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   if (!regs_ok) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  if constexpr (SHARED) {  // between the plan and the merge, each launched while the one in front runs
+    if ((e = launch_shared_plan(a, stream)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess) return e;
+    return launch_shared_merge(a, stream);
+  }
   kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // Units of up to three key tiles are never cut (fa_paged_plan.cuh, place()).
   if (((long long)a.p.max_pages << a.p.page_log2) <= kNeverCut * kTileRows) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid, SHORT ? 2 : 4);
   cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, SHORT ? 8 : 2>, a.p, a.grid);
@@ -1293,8 +1394,11 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged(const PagedLaunch& a, cudaStream_t stream) {
-  if (a.d == 64) return a.is_short ? launch_paged_t<64, true>(a, stream) : launch_paged_t<64, false>(a, stream);
-  return a.is_short ? launch_paged_t<128, true>(a, stream) : launch_paged_t<128, false>(a, stream);
+  if (a.is_shared)
+    return a.d == 64 ? launch_paged_t<64, false, true>(a, stream) : launch_paged_t<128, false, true>(a, stream);
+  if (a.d == 64)
+    return a.is_short ? launch_paged_t<64, true, false>(a, stream) : launch_paged_t<64, false, false>(a, stream);
+  return a.is_short ? launch_paged_t<128, true, false>(a, stream) : launch_paged_t<128, false, false>(a, stream);
 }
 
 }  // namespace fa

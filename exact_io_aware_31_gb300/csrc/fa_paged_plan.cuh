@@ -6,6 +6,10 @@
 // sequence by sequence, key head by key head, block by block.  Each has a cost,
 // and the row of all costs is cut into equal runs, one per CTA.  A role of a CTA
 // walks its run as segments, each the part of one unit that lies in the run.
+//
+// Where sequences share their first keys (fa_paged_shared.cu), the shared keys of
+// a group are an entry of their own in front: all of the group's tokens, one after
+// the other, against those keys.  The group's sequences then begin behind them.
 #pragma once
 
 #include "fa_common.cuh"
@@ -49,6 +53,17 @@ struct Seq {
   int q0, qn, kv;  // first row, new tokens, keys
 };
 
+// An entry of a batch whose sequences share keys.
+enum Kind { kAlone, kPrefix, kRest };  // a whole sequence; a group's shared keys; a sequence behind them
+struct SharedSeq : Seq {
+  int row, page0;  // its pages: entries of this row of the table from page0 on
+  int kind;
+};
+
+// Whether tokens see only the keys up to their own.
+__host__ __device__ inline int causal_in(const Seq&, int causal) { return causal; }
+__host__ __device__ inline int causal_in(const SharedSeq& q, int causal) { return causal && q.kind != kPrefix; }
+
 __host__ __device__ inline int imin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ inline int imax(int a, int b) { return a > b ? a : b; }
 
@@ -66,12 +81,14 @@ __host__ __device__ inline Seq make_seq(int begin, int end, int kv, int T, int c
 __host__ __device__ inline int blocks_of(const Seq& q, int ut) { return (q.qn + ut - 1) / ut; }
 
 // Keys that tokens [.., hi) of the sequence see.
-__host__ __device__ inline int keys_upto(const Seq& q, int hi, int causal) {
-  return imax(0, causal ? q.kv - q.qn + hi : q.kv);
+template <class Q>
+__host__ __device__ inline int keys_upto(const Q& q, int hi, int causal) {
+  return imax(0, causal_in(q, causal) ? q.kv - q.qn + hi : q.kv);
 }
 
 // Key tiles of block b, at least one (so that rows that see no key are written as well).
-__host__ __device__ inline int unit_tiles(const Seq& q, int b, const Shape& sh) {
+template <class Q>
+__host__ __device__ inline int unit_tiles(const Q& q, int b, const Shape& sh) {
   return imax(1, (keys_upto(q, imin(q.qn, (b + 1) * sh.ut), sh.causal) + kTileRows - 1) >> 7);
 }
 
@@ -83,25 +100,25 @@ __host__ __device__ inline long long cost_of(long long blocks, long long keys, F
 }
 
 // Cost of blocks [0, b) of one key head, all of them full.
-template <int D>
-__host__ __device__ inline long long cost_before(const Seq& q, int b, const Shape& sh) {
+template <int D, class Q>
+__host__ __device__ inline long long cost_before(const Q& q, int b, const Shape& sh) {
   const Form f = sh.form(sh.ut);
-  if (!sh.causal) return cost_of<D>(b, (long long)b * q.kv, f);
+  if (!causal_in(q, sh.causal)) return cost_of<D>(b, (long long)b * q.kv, f);
   const int c = q.kv - q.qn;  // block i sees c + (i + 1) ut keys, or none
   const int z = c >= 0 ? 0 : imin(b, -c / sh.ut);
   const long long keys = (long long)(b - z) * c + (long long)sh.ut * ((long long)b * (b + 1) - (long long)z * (z + 1)) / 2;
   return cost_of<D>(b, keys, f);
 }
 
-template <int D>
-__host__ __device__ inline long long cost_of_block(const Seq& q, int b, const Shape& sh) {
+template <int D, class Q>
+__host__ __device__ inline long long cost_of_block(const Q& q, int b, const Shape& sh) {
   const int hi = imin(q.qn, (b + 1) * sh.ut);
   return cost_of<D>(1, keys_upto(q, hi, sh.causal), sh.form(hi - b * sh.ut));
 }
 
 // Of one key head.
-template <int D>
-__host__ __device__ inline long long cost_of_seq(const Seq& q, const Shape& sh) {
+template <int D, class Q>
+__host__ __device__ inline long long cost_of_seq(const Q& q, const Shape& sh) {
   const int nb = blocks_of(q, sh.ut);
   return nb == 0 ? 0 : cost_before<D>(q, nb - 1, sh) + cost_of_block<D>(q, nb - 1, sh);
 }
@@ -126,8 +143,8 @@ constexpr int kNeverCut = 3;
 // Whether position y of a key head's cost lies in block b.  Then j is the key
 // tile at which the unit is cut: 0 or its number of tiles (no cut) where that is
 // a tile away, which costs less than a unit's other beginning and its partial outputs.
-template <int D>
-__host__ __device__ inline bool place(const Seq& q, long long y, int b, const Shape& sh, int& j) {
+template <int D, class Q>
+__host__ __device__ inline bool place(const Q& q, long long y, int b, const Shape& sh, int& j) {
   const long long at = y - cost_before<D>(q, b, sh);
   if (at < 0 || at >= cost_of_block<D>(q, b, sh)) return false;
   const Form f = sh.form(imin(q.qn, (b + 1) * sh.ut) - b * sh.ut);
@@ -147,10 +164,12 @@ struct Spot {
 };
 
 // Where a role stands in its walk through the run.
-struct Walk {
+template <class Q>
+struct WalkOf {
   Spot at;
-  Seq q;
+  Q q;
 };
+using Walk = WalkOf<Seq>;
 
 struct Segment {
   int tok0, ntok;  // first token (in the sequence), tokens
@@ -164,8 +183,8 @@ __host__ __device__ inline bool same_unit(const Spot& a, const Spot& b) { return
 // (32 + 8 heads, d = 128) take 18 us, and 49 among 1020 empty ones.  Passing 32 at a
 // time gained a quarter of that, but batches without empty ones took 3% more, or long
 // chunks 5%: code of the softmax loop.
-template <class P>
-__host__ __device__ inline void walk_skip(const P& p, Walk& w, const Shape& sh) {
+template <class P, class Q>
+__host__ __device__ inline void walk_skip(const P& p, WalkOf<Q>& w, const Shape& sh) {
   w.at.j = 0;
   if (++w.at.b * sh.ut < w.q.qn) return;
   w.at.b = 0;
@@ -178,8 +197,8 @@ __host__ __device__ inline void walk_skip(const P& p, Walk& w, const Shape& sh) 
 }
 
 // The current segment of a run up to `end`; false at its end.
-template <class P>
-__host__ __device__ inline bool walk_get(const P& p, const Walk& w, const Spot& end, const Shape& sh, Segment& g) {
+template <class P, class Q>
+__host__ __device__ inline bool walk_get(const P& p, const WalkOf<Q>& w, const Spot& end, const Shape& sh, Segment& g) {
   if (w.at.s >= p.S) return false;
   const bool last = same_unit(w.at, end);
   if (last && w.at.j >= end.j) return false;
@@ -191,8 +210,8 @@ __host__ __device__ inline bool walk_get(const P& p, const Walk& w, const Spot& 
   return true;
 }
 
-template <class P>
-__host__ __device__ inline void walk_next(const P& p, Walk& w, const Spot& end, const Shape& sh, const Segment& g) {
+template <class P, class Q>
+__host__ __device__ inline void walk_next(const P& p, WalkOf<Q>& w, const Spot& end, const Shape& sh, const Segment& g) {
   if (same_unit(w.at, end))
     w.at.j = g.j1;  // the run's last segment
   else
@@ -200,16 +219,18 @@ __host__ __device__ inline void walk_next(const P& p, Walk& w, const Spot& end, 
 }
 
 // `q` is sequence at.s (anything for at.s >= S).
-template <class P>
-__host__ __device__ inline Walk walk_start(const P& p, const Spot& at, const Spot& end, const Seq& q, const Shape& sh) {
-  Walk w = {at, q};
+template <class P, class Q>
+__host__ __device__ inline WalkOf<Q> walk_start(const P& p, const Spot& at, const Spot& end, const Q& q,
+                                                const Shape& sh) {
+  WalkOf<Q> w = {at, q};
   if (at.s < p.S && !same_unit(at, end) && at.j >= unit_tiles(q, at.b, sh)) walk_skip(p, w, sh);
   return w;
 }
 
 // Key tiles of query tile 0 of a two-tile unit within the segment (tile 1
 // sees every one of the unit's).
-__host__ __device__ inline int tile0_count(const Seq& q, const Segment& g, const Shape& sh) {
+template <class Q>
+__host__ __device__ inline int tile0_count(const Q& q, const Segment& g, const Shape& sh) {
   const int vis = keys_upto(q, g.tok0 + sh.tt, sh.causal);
   const int n0 = imin((vis + kTileRows - 1) >> 7, g.n);
   return imax(0, imin(g.j1, n0) - g.j0);

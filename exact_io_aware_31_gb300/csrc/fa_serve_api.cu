@@ -245,17 +245,25 @@ namespace fa {
 namespace {
 
 struct PagedWorkspace {
-  size_t ml, o, total;
+  size_t ml, o, plan, total;
 };
 
-PagedWorkspace paged_workspace(int sms, int d) {
-  const size_t rows = (size_t)sms * 2 * kPagedRows;
+// `rows`: partial rows behind the CTAs' slots; `entries`: of a list of them (0: no list).
+PagedWorkspace paged_workspace(int sms, int d, size_t rows = 0, size_t entries = 0) {
+  rows += (size_t)sms * 2 * kPagedRows;
   PagedWorkspace w;
   w.ml = round256((size_t)sms * kPagedHdr * sizeof(int));
   w.o = w.ml + round256(rows * 2 * sizeof(float));
-  w.total = w.o + round256(rows * d * sizeof(float));
+  w.plan = w.o + round256(rows * d * sizeof(float));
+  w.total = w.plan;
+  if (entries > 0)
+    w.total += round256(sizeof(SharedPlan) + shared_plan_costs(entries) * sizeof(long long) +
+                        entries * sizeof(SharedEntry));
   return w;
 }
+
+// Partial rows of a batch whose sequences share keys: of the shared keys and of the rest.
+size_t shared_rows(int T, int Hq) { return 2 * (size_t)T * Hq; }
 
 // A pool [pages, Hk, page_size, d] of any strides: boxes of 64 columns by the
 // rows of a page, at most a key tile's 128 (128-byte swizzle).
@@ -296,18 +304,31 @@ extern "C" size_t fa_fwd_paged_workspace_size(int d) {
   return paged_workspace(dev.sms, d).total;
 }
 
-extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
-                            const int* page_table, const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq,
-                            int Hk, int d, int num_pages, int page_size, int max_pages, long long q_stride_t,
-                            long long q_stride_h, long long kp_stride_p, long long kp_stride_h, long long kp_stride_r,
-                            long long vp_stride_p, long long vp_stride_h, long long vp_stride_r, float scale,
-                            int causal, int max_q, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+namespace fa {
+namespace {
+
+// The groups of a batch whose sequences share keys.
+struct Groups {
+  const int* starts;
+  const int* prefix_lens;
+  int n;
+};
+
+// `groups` null: fa_fwd_paged.
+int fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse, const int* page_table,
+              const int* cu_seqlens, const int* kv_lens, const Groups* groups, int T, int S, int Hq, int Hk, int d,
+              int num_pages, int page_size, int max_pages, long long q_stride_t, long long q_stride_h,
+              long long kp_stride_p, long long kp_stride_h, long long kp_stride_r, long long vp_stride_p,
+              long long vp_stride_h, long long vp_stride_r, float scale, int causal, int max_q, void* workspace,
+              size_t workspace_bytes, cudaStream_t stream) {
   if (T < 0 || S < 0 || T >= (1 << 30) || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_q < 0 || !flag(causal) ||
       !std::isfinite(scale))
     return FA_ERR_INVALID_ARG;
   if (Hq >= (1 << 15)) return FA_ERR_INVALID_ARG;
   const int G = Hq / Hk;
   if ((d != 64 && d != 128) || G > 128) return FA_ERR_UNSUPPORTED;
+  if (groups && groups->n < 0) return FA_ERR_INVALID_ARG;
+  if (groups && groups->n > kMaxGroups) return FA_ERR_UNSUPPORTED;
   if (T == 0 || S == 0) return FA_OK;
   if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
   if (!stride_map(&q_stride_t, T, d, 1ll << 31) || !stride_map(&q_stride_h, Hq, d, 1ll << 31))
@@ -317,10 +338,14 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   int st = check_cache(k_pages, v_pages, page_table, cu_seqlens, kv_lens, Hk, d, num_pages, page_size, max_pages, sp,
                        sh, sr);
   if (st != FA_OK) return st;
+  if (groups && groups->n > 0 &&
+      (!groups->starts || !groups->prefix_lens || !aligned4(groups->starts) || !aligned4(groups->prefix_lens)))
+    return FA_ERR_INVALID_ARG;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_WORKSPACE;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != FA_OK) return st;
-  const PagedWorkspace w = paged_workspace(dev.sms, d);
+  const PagedWorkspace w = groups ? paged_workspace(dev.sms, d, shared_rows(T, Hq), (size_t)S + groups->n)
+                                  : paged_workspace(dev.sms, d);
   if (workspace_bytes < w.total) return FA_ERR_WORKSPACE;
   PagedLaunch a = {};
   a.d = d;
@@ -352,10 +377,54 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   p.part_ml = reinterpret_cast<float*>(ws + w.ml);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.status = dev.status;
+  if (groups) {
+    a.is_shared = 1;
+    p.groups = groups->starts;
+    p.prefix_lens = groups->prefix_lens;
+    p.num_groups = groups->n;
+    p.plan = reinterpret_cast<SharedPlan*>(ws + w.plan);
+  }
   if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||
       make_ragged_map(&a.tm_q4, q, T, Hk, G, d, p.copy_tokens > 0 ? p.copy_tokens : 1, q_stride_t, q_stride_h) ||
       make_pool_map(&a.tm_k, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0]) ||
       make_pool_map(&a.tm_v, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1]))
     return FA_ERR_CUDA;
   return cuda_status(launch_paged(a, stream));
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                            const int* page_table, const int* cu_seqlens, const int* kv_lens, int T, int S, int Hq,
+                            int Hk, int d, int num_pages, int page_size, int max_pages, long long q_stride_t,
+                            long long q_stride_h, long long kp_stride_p, long long kp_stride_h, long long kp_stride_r,
+                            long long vp_stride_p, long long vp_stride_h, long long vp_stride_r, float scale,
+                            int causal, int max_q, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, nullptr, T, S, Hq, Hk, d, num_pages,
+                   page_size, max_pages, q_stride_t, q_stride_h, kp_stride_p, kp_stride_h, kp_stride_r, vp_stride_p,
+                   vp_stride_h, vp_stride_r, scale, causal, max_q, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t fa_fwd_paged_shared_workspace_size(int T, int S, int num_groups, int Hq, int d) {
+  if ((d != 64 && d != 128) || T < 1 || T >= (1 << 30) || S < 1 || num_groups < 0 || num_groups > kMaxGroups ||
+      Hq < 1 || Hq >= (1 << 15))
+    return 0;
+  DeviceInfo dev;
+  if (device_info(&dev) != FA_OK) return 0;
+  return paged_workspace(dev.sms, d, shared_rows(T, Hq), (size_t)S + num_groups).total;
+}
+
+extern "C" int fa_fwd_paged_shared(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                                   const int* page_table, const int* cu_seqlens, const int* kv_lens,
+                                   const int* groups, const int* prefix_lens, int T, int S, int num_groups, int Hq,
+                                   int Hk, int d, int num_pages, int page_size, int max_pages, long long q_stride_t,
+                                   long long q_stride_h, long long kp_stride_p, long long kp_stride_h,
+                                   long long kp_stride_r, long long vp_stride_p, long long vp_stride_h,
+                                   long long vp_stride_r, float scale, int causal, int max_q, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  const Groups g = {groups, prefix_lens, num_groups};
+  return fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, &g, T, S, Hq, Hk, d, num_pages,
+                   page_size, max_pages, q_stride_t, q_stride_h, kp_stride_p, kp_stride_h, kp_stride_r, vp_stride_p,
+                   vp_stride_h, vp_stride_r, scale, causal, max_q, workspace, workspace_bytes, stream);
 }

@@ -400,6 +400,51 @@ int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* 
 size_t fa_fwd_paged_workspace_size(int d);
 
 /*
+ * fa_fwd_paged for a batch whose sequences share their first keys (a system
+ * prompt, samples of one prompt, questions about one document): the shared keys
+ * are read and multiplied once for all sequences of a group.  Results equal
+ * fa_fwd_paged's up to rounding.
+ *
+ *   groups    in   [num_groups + 1] int32, not decreasing: group g holds sequences
+ *                  groups[g] .. groups[g+1] - 1.  Sequences outside of all
+ *                  groups, and groups of none or one, are as in fa_fwd_paged
+ *   prefix_lens in [num_groups] int32, >= 0: the first prefix_lens[g] keys and
+ *                  values are the same for all sequences of group g (the same
+ *                  pages, or copies).  They are read from the pages of the first
+ *                  one that has new tokens
+ *   others    as in fa_fwd_paged, which see
+ *   workspace fa_fwd_paged_shared_workspace_size(T, S, num_groups, Hq, d) bytes,
+ *             256-byte aligned, under fa_fwd_paged's rules: two fp32 rows for each
+ *             row of the output, and the work's list
+ *
+ * Any prefix_lens[g] that is true is right: what is computed once is cut to the
+ * keys that every sequence of the group has in front of its new tokens (with
+ * causal = 0: has), and to whole tiles of 128 keys and whole pages, and is
+ * nothing where that costs no less (a group of few rows, long chunks that fill
+ * the tensor cores by themselves); the other keys are each sequence's own.
+ * groups and prefix_lens live on the device as the lengths do, so that one
+ * captured graph serves every step of the same T, S and num_groups.  Values of
+ * groups outside of 0 .. S or decreasing, and prefix_lens outside of
+ * 0 .. max_pages * page_size, are cut to their range and record
+ * FA_ERR_DEVICE_INDEX; rows of sequences that two groups then hold are not
+ * specified.
+ *
+ * Three launches.  Results are the same bits on every run.  In the last bits a
+ * row depends on the other sequences of its group.  num_groups <= 4096
+ * (FA_ERR_UNSUPPORTED above); 0 with groups and prefix_lens NULL is allowed.
+ */
+int fa_fwd_paged_shared(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                        const int* page_table, const int* cu_seqlens, const int* kv_lens, const int* groups,
+                        const int* prefix_lens, int T, int S, int num_groups, int Hq, int Hk, int d, int num_pages,
+                        int page_size, int max_pages, long long q_stride_t, long long q_stride_h,
+                        long long kp_stride_p, long long kp_stride_h, long long kp_stride_r, long long vp_stride_p,
+                        long long vp_stride_h, long long vp_stride_r, float scale, int causal, int max_q,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of fa_fwd_paged_shared on the current device; 0 for invalid sizes or without an sm_103 device. */
+size_t fa_fwd_paged_shared_workspace_size(int T, int S, int num_groups, int Hq, int d);
+
+/*
  * Size of the library-owned scratch fa_bwd_noalloc uses: 64 MiB, held on every
  * GPU that loads the library until the process exits.
  */

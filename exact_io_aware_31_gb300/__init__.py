@@ -11,13 +11,13 @@ of ``fa_bwd`` (``fa_bwd_preprocess``, ``fa_bwd_dkdv``, ``fa_bwd_dq_convert``),
 the split-KV decode forward (``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_size``), the norm and rotation of queries and keys
 (``fa_qk_norm_rope``, ``fa_qk_norm_rope_bwd``,
-``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``,
+``fa_qk_norm_rope_bwd_workspace_size``), the paged cache (``fa_paged_append``, ``fa_paged_extend``, ``fa_paged_release``,
 ``fa_fwd_paged``, ``fa_fwd_paged_workspace_size``, ``fa_fwd_paged_shared``,
 ``fa_fwd_paged_shared_workspace_size``),
 ``fa_get_device_status``, ``fa_status_string``.
 Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`decode_forward`,
 :func:`rope_table`, :func:`qk_norm_rope`, :func:`qk_norm_rope_backward`, :func:`paged_append`,
-:func:`paged_forward`, :func:`paged_forward_shared`.
+:func:`paged_pool`, :func:`paged_extend`, :func:`paged_release`, :func:`paged_forward`, :func:`paged_forward_shared`.
 """
 
 from __future__ import annotations
@@ -33,7 +33,7 @@ __all__ = [
     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
     "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_fwd_paged_shared", "fa_fwd_paged_shared_workspace_size",
     "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "paged_append", "paged_forward",
-    "paged_forward_shared",
+    "paged_forward_shared", "fa_paged_extend", "fa_paged_release", "paged_pool", "paged_extend", "paged_release",
     "fa_get_device_status", "fa_status_string", "forward", "backward", "EXPORTED_SYMBOLS",
     "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_WORKSPACE", "FA_ERR_CUDA",
     "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INTERNAL", "FA_ERR_DEVICE_INDEX",
@@ -56,7 +56,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_fp8", "fa_bwd", "fa_bwd_workspace_size", "
                     "fa_bwd_dq_convert", "fa_bwd_noalloc", "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size",
                     "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size", "fa_paged_append",
                     "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_fwd_paged_shared",
-                    "fa_fwd_paged_shared_workspace_size",
+                    "fa_fwd_paged_shared_workspace_size", "fa_paged_extend", "fa_paged_release",
                     "fa_get_device_status", "fa_status_string")
 
 # Size of the library-owned scratch behind fa_bwd_noalloc (FA_NOALLOC_SCRATCH_BYTES).
@@ -120,6 +120,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_paged_append.argtypes = [vp] * 9 + [i] * 8 + [ll] * 12 + [i, vp, vp, i, f, vp, i, i, i, vp]
     lib.fa_fwd_paged.restype = i
     lib.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [ll] * 8 + [f, i, i, vp, sz, vp]
+    lib.fa_paged_extend.restype = i
+    lib.fa_paged_extend.argtypes = [vp] * 10 + [i] * 6 + [vp]
+    lib.fa_paged_release.restype = i
+    lib.fa_paged_release.argtypes = [vp] * 6 + [i] * 5 + [vp]
     lib.fa_fwd_paged_shared.restype = i
     lib.fa_fwd_paged_shared.argtypes = [vp] * 10 + [i] * 9 + [ll] * 8 + [f, i, i, vp, sz, vp]
     lib.fa_fwd_paged_shared_workspace_size.restype = sz
@@ -229,6 +233,19 @@ def fa_paged_append(q, k, v, q_out, k_pages, v_pages, page_table, cu_seqlens, kv
                                           k_stride_h, v_stride_t, v_stride_h, kp_stride_p, kp_stride_h, kp_stride_r,
                                           vp_stride_p, vp_stride_h, vp_stride_r, norm, q_weight, k_weight,
                                           weights_f32, eps, rope, rope_len, rope_dim, interleaved, stream)
+
+
+def fa_paged_extend(requests, new_lens, request_lens, request_table, pool, cu_seqlens, kv_lens, page_table, positions,
+                    slots, T, S, R, num_pages, page_size, max_pages, stream) -> int:
+    return load_library().fa_paged_extend(requests, new_lens, request_lens, request_table, pool, cu_seqlens, kv_lens,
+                                          page_table, positions, slots, T, S, R, num_pages, page_size, max_pages,
+                                          stream)
+
+
+def fa_paged_release(requests, keep_lens, kept_pages, request_lens, request_table, pool, S, R, num_pages, page_size,
+                     max_pages, stream) -> int:
+    return load_library().fa_paged_release(requests, keep_lens, kept_pages, request_lens, request_table, pool, S, R,
+                                           num_pages, page_size, max_pages, stream)
 
 
 def fa_fwd_paged(q, k_pages, v_pages, o, lse, page_table, cu_seqlens, kv_lens, T, S, Hq, Hk, d, num_pages, page_size,
@@ -615,6 +632,86 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_seqlens, kv_lens, q_w
     if st != FA_OK:
         raise FaError(st, "fa_paged_append")
     return out
+
+
+def paged_pool(num_pages, device="cuda"):
+    """A pool ``[num_pages + 2]`` int32 of free pages, page 0 the first to be taken."""
+    import torch
+    if num_pages < 1:
+        raise ValueError("num_pages must be >= 1")
+    pool = torch.zeros(num_pages + 2, dtype=torch.int32, device=device)
+    pool[0] = num_pages
+    pool[2:] = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+    return pool
+
+
+def _tables_args(requests, request_lens, request_table, pool, device):
+    """Checks of the tensors that hold the requests: their addresses, ``(S, R, num_pages, max_pages)``."""
+    import torch
+    i32 = torch.int32
+    S, (R, max_pages), room = (_shape(requests, "requests", 1)[0], _shape(request_table, "request_table", 2),
+                               _shape(pool, "pool", 1)[0])
+    if room < 3:
+        raise ValueError("pool must hold at least one page")
+    return (_flat(requests, "requests", (S,), i32, device), _flat(request_lens, "request_lens", (R,), i32, device),
+            _flat(request_table, "request_table", (R, max_pages), i32, device),
+            _flat(pool, "pool", (room,), i32, device), S, R, room - 2, max_pages)
+
+
+def paged_extend(requests, new_lens, request_lens, request_table, pool, page_size, tokens, out=None, stream=None):
+    """Room in a paged cache for the new tokens of a step, and the step's tables: ``requests [S]`` says which request
+    each sequence is (negative: a place without one), ``new_lens [S]`` how many tokens it brings; all int32 on the
+    device.  ``request_lens [R]``, ``request_table [R, max_pages]`` and ``pool`` (:func:`paged_pool`) are the
+    requests' state and brought up to date.  Returns ``(cu_seqlens [S + 1], kv_lens [S], page_table [S, max_pages],
+    positions [tokens], slots [tokens] int64)`` for the other calls; ``out`` gives tensors to write to (any of the
+    last two may be None: not wanted), as a captured step does.  Of ``page_table`` only entries in use are written.
+    A sequence that finds no room has ``kv_lens`` 0 and leaves its request as it was."""
+    where = _elsewhere(requests, stream)
+    if where is not None:
+        with where:
+            return paged_extend(requests, new_lens, request_lens, request_table, pool, page_size, tokens, out)
+    import torch
+    i32 = torch.int32
+    dev = requests.get_device()
+    req, lens, table, pool_at, S, R, num_pages, max_pages = _tables_args(requests, request_lens, request_table, pool, dev)
+    new = _flat(new_lens, "new_lens", (S,), i32, dev)
+    if out is None:
+        out = (torch.empty(S + 1, dtype=i32, device=requests.device), torch.empty(S, dtype=i32, device=requests.device),
+               torch.empty(S, max_pages, dtype=i32, device=requests.device),
+               torch.empty(tokens, dtype=i32, device=requests.device),
+               torch.empty(tokens, dtype=torch.int64, device=requests.device))
+    if not 0 <= tokens < 1 << 31:
+        raise ValueError("tokens must be in 0 .. 2^31 - 1")
+    cu, kv, pages, positions, slots = out
+    st = load_library().fa_paged_extend(req, new, lens, table, pool_at, _flat(cu, "cu_seqlens", (S + 1,), i32, dev),
+                                        _flat(kv, "kv_lens", (S,), i32, dev),
+                                        _flat(pages, "page_table", (S, max_pages), i32, dev),
+                                        _flat(positions, "positions", (tokens,), i32, dev),
+                                        _flat(slots, "slots", (tokens,), torch.int64, dev), tokens, S, R, num_pages,
+                                        page_size, max_pages, torch._C._cuda_getCurrentRawStream(dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_extend")
+    return cu, kv, pages, positions, slots
+
+
+def paged_release(requests, request_lens, request_table, pool, page_size, keep_lens=None, kept_pages=None,
+                  stream=None):
+    """The requests ``requests [S]`` (negative: none) give pages back to the pool and keep their first ``keep_lens
+    [S]`` keys (None: none).  ``kept_pages [R]`` counts the pages at the front of each request that it shares and
+    does not own (None: it owns all)."""
+    where = _elsewhere(requests, stream)
+    if where is not None:
+        with where:
+            return paged_release(requests, request_lens, request_table, pool, page_size, keep_lens, kept_pages)
+    import torch
+    dev = requests.get_device()
+    req, lens, table, pool_at, S, R, num_pages, max_pages = _tables_args(requests, request_lens, request_table, pool, dev)
+    st = load_library().fa_paged_release(req, _flat(keep_lens, "keep_lens", (S,), torch.int32, dev),
+                                         _flat(kept_pages, "kept_pages", (R,), torch.int32, dev), lens, table, pool_at,
+                                         S, R, num_pages, page_size, max_pages,
+                                         torch._C._cuda_getCurrentRawStream(dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_release")
 
 
 def paged_forward(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, scale=None, causal=True, max_q=0, out=None,

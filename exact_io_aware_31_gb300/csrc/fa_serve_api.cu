@@ -12,6 +12,7 @@
 #include "fa_host.h"
 #include "fa_norm_rope.cuh"
 #include "fa_paged.cuh"
+#include "fa_paged_tables.cuh"
 
 namespace fa {
 namespace {
@@ -239,6 +240,76 @@ extern "C" int fa_paged_append(const void* q, const void* k, const void* v, void
   a.max_pages = max_pages;
   a.sms = dev.sms;
   return cuda_status(launch_paged_append(a, stream));
+}
+
+namespace fa {
+namespace {
+
+// The arguments that the calls on a cache's tables share (S >= 1 here).
+int check_tables(TablesParams* p, const int* requests, const int* lens, int* request_lens, int* request_table,
+                 int* pool, int S, int R, int num_pages, int page_size, int max_pages) {
+  if (R < 1 || num_pages < 1 || num_pages > (1 << 30) || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
+  if ((long long)max_pages * page_size > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (S > kMaxSequences || R > kMaxRequests) return FA_ERR_UNSUPPORTED;
+  if (S == 0) return FA_OK;
+  if (!requests || !request_lens || !request_table || !pool || !aligned4(requests) || !aligned4(lens) ||
+      !aligned4(request_lens) || !aligned4(request_table) || !aligned4(pool))
+    return FA_ERR_INVALID_ARG;
+  p->requests = requests;
+  p->lens = lens;
+  p->request_lens = request_lens;
+  p->request_table = request_table;
+  p->pool = pool;
+  p->S = S;
+  p->R = R;
+  p->num_pages = num_pages;
+  while ((1 << p->page_log2) < page_size) ++p->page_log2;
+  p->max_pages = max_pages;
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" int fa_paged_extend(const int* requests, const int* new_lens, int* request_lens, int* request_table,
+                               int* pool, int* cu_seqlens, int* kv_lens, int* page_table, int* positions,
+                               long long* slots, int T, int S, int R, int num_pages, int page_size, int max_pages,
+                               cudaStream_t stream) {
+  if (T < 0 || S < 0) return FA_ERR_INVALID_ARG;
+  TablesParams p = {};
+  int st = check_tables(&p, requests, new_lens, request_lens, request_table, pool, S, R, num_pages, page_size,
+                        max_pages);
+  if (st != FA_OK || S == 0) return st;
+  if (!new_lens || !cu_seqlens || !kv_lens || !page_table || !aligned4(cu_seqlens) || !aligned4(kv_lens) ||
+      !aligned4(page_table) || !aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return FA_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != FA_OK) return st;
+  p.status = dev.status;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.page_table = page_table;
+  p.positions = positions;
+  p.slots = slots;
+  p.T = T;
+  return cuda_status(launch_paged_extend(p, dev.sms, stream));
+}
+
+extern "C" int fa_paged_release(const int* requests, const int* keep_lens, const int* kept_pages, int* request_lens,
+                                const int* request_table, int* pool, int S, int R, int num_pages, int page_size,
+                                int max_pages, cudaStream_t stream) {
+  if (S < 0) return FA_ERR_INVALID_ARG;
+  TablesParams p = {};
+  int st = check_tables(&p, requests, keep_lens, request_lens, const_cast<int*>(request_table), pool, S, R, num_pages,
+                        page_size, max_pages);
+  if (st != FA_OK || S == 0) return st;
+  if (!aligned4(kept_pages)) return FA_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != FA_OK) return st;
+  p.status = dev.status;
+  p.kept_pages = kept_pages;
+  return cuda_status(launch_paged_release(p, dev.sms, stream));
 }
 
 namespace fa {

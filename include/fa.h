@@ -350,6 +350,72 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
                     int interleaved, cudaStream_t stream);
 
 /*
+ * A paged cache's tables, kept on the device
+ * ------------------------------------------
+ *  A server's requests have places 0 .. R-1: request_lens [R] int32 holds the
+ *  keys that each has cached, request_table [R, max_pages] int32 their pages.
+ *  pool [num_pages + 2] int32 holds the free pages: pool[0] how many there are,
+ *  pool[1] a word that belongs to the library and is zero between calls,
+ *  pool[2 .. 2 + pool[0]) their numbers, the next one to be taken last.  The
+ *  caller sets all of it up (every page free: pool[0] = num_pages, pool[1] = 0)
+ *  and may change it between calls.  Calls on the same requests or the same
+ *  pool must not overlap.
+ *
+ * fa_paged_extend: room for the new tokens of a step, and the step's tables for
+ * fa_paged_append and the attention over the cache.  One launch.
+ *
+ *   requests   in   [S] int32: the request of each sequence of the step; negative
+ *                   for a place of the batch without one
+ *   new_lens   in   [S] int32: its new tokens, >= 0 (of no meaning without a request)
+ *   request_lens    in, out  new_lens are added
+ *   request_table   in, out  entries of the pages taken are written
+ *   pool            in, out  pages are taken in the order of the batch
+ *   cu_seqlens out  [S + 1] int32
+ *   kv_lens    out  [S] int32, new tokens included
+ *   page_table out  [S, max_pages] int32: entries of the pages in use are written
+ *   positions  out  [T] int32, or NULL: each new token's position.  Rows behind
+ *                   the last sequence get 0
+ *   slots      out  [T] int64, or NULL: page * page_size + row of each new token,
+ *                   for caches of the caller's own.  Rows behind the last
+ *                   sequence get -1
+ *
+ * A sequence is left out where its request is not in 0 .. R-1 or stands in
+ * front in the batch already, has a length outside of its table (new tokens
+ * included), has rows past T, or needs pages that the pool, after those in front
+ * in the batch, does not have (those behind it that need some are left out,
+ * too): its request stays as it was, its kv_lens is 0, so that it attends to
+ * nothing and nothing of it is cached, the positions and slots of its rows are
+ * -1, and FA_ERR_DEVICE_INDEX is recorded.  The caller sees it in kv_lens and
+ * may bring it again.  cu_seqlens counts its rows (cut to T).
+ *
+ * fa_paged_release: requests give their pages back.  One launch.
+ *
+ *   requests   in   [S] int32, negative: none
+ *   keep_lens  in   [S] int32: keys that each keeps (a step whose tokens are not
+ *                   all accepted keeps those in front), or NULL: none
+ *   kept_pages in   [R] int32, or NULL: pages at the front of each request that are
+ *                   not its own (a shared prompt's) and stay out of the pool
+ *   request_lens    in, out  becomes keep_lens
+ *   request_table   in   [R, max_pages]
+ *   pool            in, out  the pages behind those kept, so that fa_paged_extend of
+ *                   the same batch would take them in the same order again
+ *
+ * A request that is not in 0 .. R-1, stands in front already or is to keep what
+ * it does not have stays as it is; where more pages come back than the pool has
+ * room for (some came back before) nothing is done.  Both, and a page outside of
+ * the pool in the table, record FA_ERR_DEVICE_INDEX.
+ *
+ * page_size and max_pages are the cache's; num_pages <= 2^30, S <= 4096 and R <=
+ * 16384 (FA_ERR_UNSUPPORTED above).  S = 0 does nothing.
+ */
+int fa_paged_extend(const int* requests, const int* new_lens, int* request_lens, int* request_table, int* pool,
+                    int* cu_seqlens, int* kv_lens, int* page_table, int* positions, long long* slots, int T, int S,
+                    int R, int num_pages, int page_size, int max_pages, cudaStream_t stream);
+int fa_paged_release(const int* requests, const int* keep_lens, const int* kept_pages, int* request_lens,
+                     const int* request_table, int* pool, int S, int R, int num_pages, int page_size, int max_pages,
+                     cudaStream_t stream);
+
+/*
  * Attention of the T new tokens of a step over the paged cache (their keys and
  * values appended before): a single token a sequence, a few, or chunks of a
  * prompt, in any mix; grouped key heads (query head h reads key head

@@ -1,4 +1,5 @@
-"""Plain fp64 forms of the operators around the attention kernels: norm with rotation, paged cache, paged attention.
+"""Plain forms of the operators around the attention kernels: norm with rotation, paged cache and its tables, paged
+attention (fp64; the tables in whole numbers).
 
 TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``): slow, obvious, CPU.
 
@@ -13,7 +14,7 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["rope_table", "norm_rope", "norm_rope_grad", "paged_append", "paged_attention"]
+__all__ = ["rope_table", "norm_rope", "norm_rope_grad", "paged_append", "paged_attention", "Tables"]
 
 
 def rope_table(length, dim, base=10000.0):
@@ -109,3 +110,71 @@ def paged_attention(q, k_pages, v_pages, page_table, cu, lens, scale, causal):
                     o[t, g] = (e / e.sum()) @ vals[:see]
                     reach[t, g] = (e / e.sum()) @ np.abs(vals[:see])
     return o, lse, reach
+
+
+class Tables:
+    """The requests of a paged cache: lengths [R], rows of pages [R, max_pages], the stack of free pages."""
+
+    def __init__(self, lens, table, free, num_pages, page_size):
+        self.lens, self.table, self.free = list(lens), np.array(table), list(free)
+        self.num_pages, self.page = num_pages, page_size
+        self.bad = False                       # something was refused
+
+    def pages(self, n):
+        return -(-n // self.page)
+
+    def extend(self, requests, new_lens, tokens, page_table):
+        """(cu_seqlens, kv_lens, page_table, positions, slots); ``page_table`` holds what is there before."""
+        S, most = len(requests), self.table.shape[1]
+        cu, kv, out = [0], [], np.array(page_table)
+        positions, slots = np.zeros(tokens, dtype=np.int64), np.full(tokens, -1, dtype=np.int64)
+        seen, row, asked, have = set(), 0, 0, len(self.free)
+        for s, r in enumerate(requests):
+            n = max(0, new_lens[s]) if r >= 0 else 0
+            first = row
+            row += n
+            cu.append(min(row, tokens))
+            kv.append(0)
+            if r < 0:
+                continue
+            self.bad |= new_lens[s] < 0
+            fine = r < len(self.lens) and r not in seen
+            seen.add(r)
+            fine = fine and 0 <= self.lens[r] and self.lens[r] + n <= most * self.page and (n == 0 or row <= tokens)
+            if fine:
+                held, need = self.pages(self.lens[r]), self.pages(self.lens[r] + n)
+                asked += need - held
+                fine = need == held or asked <= have
+            if not fine:
+                self.bad = True
+                positions[min(first, tokens):min(row, tokens)] = -1
+                continue
+            for j in range(held, need):
+                self.table[r, j] = self.free.pop()
+            at = np.arange(self.lens[r], self.lens[r] + n)
+            positions[first:row] = at
+            slots[first:row] = self.table[r, at // self.page].astype(np.int64) * self.page + at % self.page
+            self.lens[r] += n
+            kv[s] = self.lens[r]
+            out[s, :need] = self.table[r, :need]
+        return np.array(cu), np.array(kv), out, positions, slots
+
+    def release(self, requests, keep_lens=None, kept_pages=None):
+        back, lens, seen = [], list(self.lens), set()
+        for s, r in enumerate(requests):
+            if r < 0:
+                continue
+            keep = 0 if keep_lens is None else keep_lens[s]
+            if r >= len(lens) or r in seen or not 0 <= keep <= lens[r] <= self.table.shape[1] * self.page:
+                self.bad = True
+                seen.add(r)
+                continue
+            seen.add(r)
+            first = max(self.pages(keep), 0 if kept_pages is None else kept_pages[r])
+            back += [int(x) for x in self.table[r, first:self.pages(lens[r])]]
+            lens[r] = keep
+        self.bad |= any(not 0 <= x < self.num_pages for x in back)
+        if len(self.free) + len(back) > self.num_pages:
+            self.bad = True
+            return
+        self.lens, self.free = lens, self.free + back[::-1]

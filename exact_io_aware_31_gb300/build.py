@@ -34,7 +34,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfa.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_decode.cu", "fa_noalloc.cu",
-           "fa_norm_rope.cu", "fa_paged.cu", "fa_paged_shared.cu", "fa_paged_tables.cu",
+           "fa_norm_rope.cu", "fa_paged.cu", "fa_paged_rows.cu", "fa_paged_shared.cu", "fa_paged_tables.cu",
            "fa_serve_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

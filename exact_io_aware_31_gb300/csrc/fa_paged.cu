@@ -135,12 +135,10 @@ struct Work<true> {
   const SharedEntry* list;
   int S, Hk;
   __device__ __forceinline__ explicit Work(const PagedParams& p)
-      : list(reinterpret_cast<const SharedEntry*>(costs(p) + shared_plan_costs(p.S + p.num_groups))),
+      : list(reinterpret_cast<const SharedEntry*>(reinterpret_cast<const uint8_t*>(p.plan) +
+                                                  shared_lists(p.S, p.num_groups, p.sms).list)),
         S(__ldcg(&p.plan->entries)),
         Hk(p.Hk) {}
-  static __device__ __forceinline__ const long long* costs(const PagedParams& p) {
-    return reinterpret_cast<const long long*>(p.plan + 1);
-  }
   __device__ __forceinline__ SharedSeq seq(int s) const {
     const int4 a = __ldcg(&list[s].seq), b = __ldcg(&list[s].how);
     SharedSeq q;
@@ -270,9 +268,9 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<Seq>* plan
 template <int D, int THREADS>
 __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<SharedSeq>* plan) {
   const Work<true> work(p);
-  const long long* cost = Work<true>::costs(p);
+  const long long* cost = reinterpret_cast<const long long*>(p.plan + 1);
   const long long total = __ldcg(cost + work.S);
-  const int ctas = ctas_for<D>(total, gridDim.x);
+  const int ctas = __ldcg(&p.plan->ctas);
   const long long share = ctas > 0 ? div_long(total, ctas) : 0;
   const long long x[2] = {border(total, share, blockIdx.x, ctas), border(total, share, blockIdx.x + 1, ctas)};
   if (threadIdx.x < 2) plan->at[threadIdx.x] = {work.S, 0, 0, 0};  // a border at the end
@@ -362,6 +360,13 @@ __global__ void __launch_bounds__(384, 1)
   const float c2 = fabsf(p.c2);
   int* status = p.status;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // Where keys are shared the launch in front wrote the list of entries, and the one
+  // behind (rows_kernel) may begin once that is there; CTAs without work make room for it.
+  if constexpr (SHARED) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.x >= __ldcg(&p.plan->ctas)) return;
+  }
   bool start_ok = smem_base_ok(smem_raw, status);
 #ifdef FA_TEST_HOOKS
   if (*reinterpret_cast<volatile int*>(&g_fa_test_paged) == 2) {
@@ -371,12 +376,13 @@ __global__ void __launch_bounds__(384, 1)
 #endif
   if (!start_ok) {  // nothing for the merge kernel, whatever the workspace holds
     if (threadIdx.x < kPagedHdr) p.hdr[(size_t)blockIdx.x * kPagedHdr + threadIdx.x] = 0;
+    if (SHARED && threadIdx.x == 0) p.plan->failed = 1;
     return;
   }
   uint8_t* sm = smem_raw;
   // The merge kernel (a programmatic dependent) may start launching: its blocks
   // take the room of CTAs that are done, and wait for this grid's results.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   PagedBars B;
@@ -429,7 +435,6 @@ __global__ void __launch_bounds__(384, 1)
   // Short chunks: the plan behind the barrier (64 sequences of 8 tokens against up to
   // 1024 keys, d = 64: 47.3 -> 45.4 us).  The other way round with the other forms,
   // whose softmax loops come out slower so (2 x 2048 tokens: 458 -> 463 us).
-  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // the list of entries
   if constexpr (!SHORT) make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_before();
   __syncthreads();
@@ -1194,7 +1199,7 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   __syncthreads();
   // Rows of the workspace are only good if every CTA went through to its end.
-  if (SHARED && threadIdx.x == 0) p.hdr[(size_t)blockIdx.x * kPagedHdr + kPagedEnded] = !aborted(abort_flag);
+  if (SHARED && threadIdx.x == 0 && aborted(abort_flag)) p.plan->failed = 1;
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
@@ -1378,6 +1383,7 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess) return e;
+    if (a.p.few_rows > 0 && (e = launch_shared_rows(a, stream)) != cudaSuccess) return e;
     return launch_shared_merge(a, stream);
   }
   kern<<<a.grid, C::kThreads, C::kSmemBytes, stream>>>(a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p);

@@ -11,16 +11,46 @@ namespace fa {
 // The plan of a batch whose sequences share keys, in the workspace: what the work is, one
 // entry after the other, with the cost of all entries in front of each.
 struct SharedPlan {
-  int entries;        // how many there are
-  int row0, row1;     // tokens that belong to a sequence
+  int entries;      // of paged_kernel's list
+  int pieces;       // of rows_kernel's
+  int ctas;         // that paged_kernel's work is given to
+  unsigned next;    // rows_kernel: the next of its pieces' heads that no CTA has taken
+  int row0, row1;   // tokens that belong to a sequence
+  int failed;       // a CTA gave up: the workspace's rows are not this call's
   int pad;
-  // long long cost[S + num_groups + 1], then SharedEntry[S + num_groups] (16-byte aligned)
 };
 struct SharedEntry {
   int4 seq;  // first token, tokens, keys, row of the page table
   int4 how;  // its first entry there, kind
 };
-static_assert(sizeof(SharedPlan) == 16 && sizeof(SharedEntry) == 32, "16-byte reads");
+// Of an entry with few rows, or a part of its keys.
+struct SharedPiece {
+  int4 seq;   // as SharedEntry
+  int4 how;   // first entry of the page table, kind, keys [z, w) of the entry
+  int4 part;  // place of its partial rows (-1: not split), parts of the entry, which one
+};
+static_assert(sizeof(SharedPlan) == 32 && sizeof(SharedEntry) == 32 && sizeof(SharedPiece) == 48, "16-byte reads");
+
+// What rows_kernel's entries are split into in all: so many parts an SM or fewer, so that
+// the places of partial rows are twice as many at most (an entry of more than one part
+// has at most twice as many parts as its share).
+constexpr int kPartsASm = 8;
+inline __host__ __device__ int shared_parts(int sms) { return 2 * kPartsASm * sms; }
+constexpr int kPartRows = 32;  // rows of such an entry at most
+
+// Where the lists lie behind the head: costs in front of the entries, entries, pieces.
+struct SharedLists {
+  size_t cost, list, pieces, bytes;
+};
+inline __host__ __device__ SharedLists shared_lists(int S, int groups, int sms) {
+  const size_t n = (size_t)S + groups;
+  SharedLists w;
+  w.cost = sizeof(SharedPlan);
+  w.list = w.cost + (n + 2) / 2 * 2 * sizeof(long long);
+  w.pieces = w.list + n * sizeof(SharedEntry);
+  w.bytes = w.pieces + (n + shared_parts(sms)) * sizeof(SharedPiece);
+  return w;
+}
 
 struct PagedParams {
   void* o;                // [T, Hq, d] bf16
@@ -44,11 +74,12 @@ struct PagedParams {
   const int* prefix_lens;  // [num_groups] keys that its sequences share
   int num_groups;
   SharedPlan* plan;
+  int sms;
+  int few_rows;            // entries of at most so many rows of a key head go to rows_kernel (0: none)
 };
 
 // ints of a CTA's header in the workspace
 constexpr int kPagedHdr = 8;
-constexpr int kPagedEnded = 5;  // (shared keys) which of them says that the CTA did its work
 // query rows of a unit at most
 constexpr int kPagedRows = 256;
 
@@ -57,6 +88,9 @@ struct PagedLaunch {
   CUtensorMap tm_q4;  // ... x copy_tokens
   CUtensorMap tm_k;  // [pages, Hk, page_size, d]: boxes of 64 columns x min(page_size, 128) rows
   CUtensorMap tm_v;
+  CUtensorMap tm_qr;  // shared keys: queries in boxes of few_rows / G tokens, K and V in boxes of few rows
+  CUtensorMap tm_kr;
+  CUtensorMap tm_vr;
   PagedParams p;
   int d;
   int is_short;  // units of copy_tokens only
@@ -70,15 +104,24 @@ cudaError_t launch_paged(const PagedLaunch& a, cudaStream_t stream);
 constexpr int kMaxGroups = 4096;
 
 // Partial rows of a batch whose sequences share keys lie behind the CTAs' slots: first
-// those of the shared keys, one a row of the output, then those of the rest.  Where a
-// row's partial outputs are instead is said by a sum that no row can have:
-constexpr float kRowCut = -1.f;         // in the slots: the maximum holds the CTA that began the unit and the row there
-constexpr float kRowDone = -2.f;        // in the output already
-constexpr float kRowCutOfRest = -3.f;   // as kRowCut, and there are shared keys, too
+// those of the shared keys, one a row of the output, then those of the rest, then
+// kPartRows for each head of a part of rows_kernel.  Where a row's partial outputs are
+// instead is said by a sum that no row can have:
+constexpr float kRowDone = -1.f;         // in the output already
+constexpr float kRowCut = -2.f;          // in the slots: the maximum holds the CTA that began the unit and the row there
+constexpr float kRowCutOfRest = -3.f;    // as kRowCut, and there are shared keys, too
+constexpr float kRowParts = -4.f;        // in parts: the maximum holds their first place, their number and the row there
+constexpr float kRowPartsOfRest = -5.f;  // as kRowParts, and there are shared keys, too
 
-inline __host__ __device__ size_t shared_plan_costs(int entries) { return ((size_t)entries + 2) / 2 * 2; }
+// Rows of a 16-row matrix tile: what rows_kernel takes at a time, once (two CTAs an SM) or
+// twice (one: it has more in registers).
+constexpr int kFewRows = 16;
+inline __host__ __device__ int rows_ctas(int few_rows, int sms) { return few_rows <= kFewRows ? 2 * sms : sms; }
+// Keys of a stage of rows_kernel: 16 KB of K and V.
+inline constexpr int rows_keys(int d) { return d == 128 ? 32 : 64; }
 
 cudaError_t launch_shared_plan(const PagedLaunch& a, cudaStream_t stream);
+cudaError_t launch_shared_rows(const PagedLaunch& a, cudaStream_t stream);
 cudaError_t launch_shared_merge(const PagedLaunch& a, cudaStream_t stream);
 
 }  // namespace fa

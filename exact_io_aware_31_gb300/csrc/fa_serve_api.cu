@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/fa.h"
+#include "fa_common.cuh"
 #include "fa_host.h"
 #include "fa_norm_rope.cuh"
 #include "fa_paged.cuh"
@@ -319,30 +320,31 @@ struct PagedWorkspace {
   size_t ml, o, plan, total;
 };
 
-// `rows`: partial rows behind the CTAs' slots; `entries`: of a list of them (0: no list).
-PagedWorkspace paged_workspace(int sms, int d, size_t rows = 0, size_t entries = 0) {
-  rows += (size_t)sms * 2 * kPagedRows;
+// `apart`: partial rows behind the CTAs' slots; `lists`: bytes of the lists behind all.
+PagedWorkspace paged_workspace(int sms, int d, size_t apart = 0, size_t lists = 0) {
+  const size_t rows = (size_t)sms * 2 * kPagedRows + apart;
   PagedWorkspace w;
   w.ml = round256((size_t)sms * kPagedHdr * sizeof(int));
   w.o = w.ml + round256(rows * 2 * sizeof(float));
   w.plan = w.o + round256(rows * d * sizeof(float));
-  w.total = w.plan;
-  if (entries > 0)
-    w.total += round256(sizeof(SharedPlan) + shared_plan_costs(entries) * sizeof(long long) +
-                        entries * sizeof(SharedEntry));
+  w.total = w.plan + round256(lists);
   return w;
 }
 
-// Partial rows of a batch whose sequences share keys: of the shared keys and of the rest.
-size_t shared_rows(int T, int Hq) { return 2 * (size_t)T * Hq; }
+// The same for a batch whose sequences share keys: partial rows of the shared keys and of
+// the rest, and those of entries in parts.
+PagedWorkspace shared_workspace(int sms, int T, int S, int num_groups, int Hq, int d) {
+  return paged_workspace(sms, d, 2 * (size_t)T * Hq + (size_t)shared_parts(sms) * kPartRows,
+                         shared_lists(S, num_groups, sms).bytes);
+}
 
 // A pool [pages, Hk, page_size, d] of any strides: boxes of 64 columns by the
-// rows of a page, at most a key tile's 128 (128-byte swizzle).
+// rows of a page, at most `rows` (a key tile's 128; 128-byte swizzle).
 int make_pool_map(CUtensorMap* m, const void* base, int pages, int Hk, int page_size, int d, long long sp,
-                  long long sh, long long sr) {
+                  long long sh, long long sr, int rows = kTileRows) {
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)Hk, (cuuint64_t)pages};
   cuuint64_t strides[3] = {(cuuint64_t)sr * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)(page_size < 128 ? page_size : 128), 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)(page_size < rows ? page_size : rows), 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -415,8 +417,8 @@ int fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, 
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_WORKSPACE;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != FA_OK) return st;
-  const PagedWorkspace w = groups ? paged_workspace(dev.sms, d, shared_rows(T, Hq), (size_t)S + groups->n)
-                                  : paged_workspace(dev.sms, d);
+  const PagedWorkspace w =
+      groups ? shared_workspace(dev.sms, T, S, groups->n, Hq, d) : paged_workspace(dev.sms, d);
   if (workspace_bytes < w.total) return FA_ERR_WORKSPACE;
   PagedLaunch a = {};
   a.d = d;
@@ -454,6 +456,15 @@ int fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, 
     p.prefix_lens = groups->prefix_lens;
     p.num_groups = groups->n;
     p.plan = reinterpret_cast<SharedPlan*>(ws + w.plan);
+    p.sms = dev.sms;
+    // Rows that rows_kernel takes of a key head: a single token's group at least, and what a
+    // step of max_q tokens has where that is no more than its larger form's.
+    p.few_rows = G > 2 * kFewRows ? 0 : G > kFewRows || (max_q <= 2 * kFewRows / G && max_q * G > kFewRows) ? 2 * kFewRows : kFewRows;
+    if (p.few_rows > 0 &&
+        (make_ragged_map(&a.tm_qr, q, T, Hk, G, d, p.few_rows / G, q_stride_t, q_stride_h) ||
+         make_pool_map(&a.tm_kr, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0], rows_keys(d)) ||
+         make_pool_map(&a.tm_vr, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1], rows_keys(d))))
+      return FA_ERR_CUDA;
   }
   if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||
       make_ragged_map(&a.tm_q4, q, T, Hk, G, d, p.copy_tokens > 0 ? p.copy_tokens : 1, q_stride_t, q_stride_h) ||
@@ -483,7 +494,7 @@ extern "C" size_t fa_fwd_paged_shared_workspace_size(int T, int S, int num_group
     return 0;
   DeviceInfo dev;
   if (device_info(&dev) != FA_OK) return 0;
-  return paged_workspace(dev.sms, d, shared_rows(T, Hq), (size_t)S + num_groups).total;
+  return shared_workspace(dev.sms, T, S, num_groups, Hq, d).total;
 }
 
 extern "C" int fa_fwd_paged_shared(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,

@@ -31,12 +31,14 @@ struct SharedPiece {
 };
 static_assert(sizeof(SharedPlan) == 32 && sizeof(SharedEntry) == 32 && sizeof(SharedPiece) == 48, "16-byte reads");
 
-// What rows_kernel's entries are split into in all: so many parts an SM or fewer, so that
-// the places of partial rows are twice as many at most (an entry of more than one part
-// has at most twice as many parts as its share).
-constexpr int kPartsASm = 8;
-inline __host__ __device__ int shared_parts(int sms) { return 2 * kPartsASm * sms; }
-constexpr int kPartRows = 32;  // rows of such an entry at most
+// Partial rows of rows_kernel's entries in parts: of kMaxParts (16 rows) or half as many (32
+// rows) an SM.  An entry of n keys has at most 2 n / (L + 1) parts of L keys, if it has two;
+// with part_keys()' lengths and W keys times heads for 8 workers an SM these are, a worker,
+// 3 / W for each of the first W / 2, 6 / W for the next 3 W / 10 and 12 / W for the others at most:
+// 5.7 in all.
+constexpr int kMaxParts = 46;
+constexpr int kPartRows = 16;
+inline __host__ __device__ int shared_parts(int sms) { return kMaxParts * sms; }
 
 // Where the lists lie behind the head: costs in front of the entries, entries, pieces.
 struct SharedLists {
@@ -75,6 +77,7 @@ struct PagedParams {
   int num_groups;
   SharedPlan* plan;
   int sms;
+  unsigned hk_inverse;     // (2^32 - 1) / Hk
   int few_rows;            // entries of at most so many rows of a key head go to rows_kernel (0: none)
 };
 
@@ -88,9 +91,10 @@ struct PagedLaunch {
   CUtensorMap tm_q4;  // ... x copy_tokens
   CUtensorMap tm_k;  // [pages, Hk, page_size, d]: boxes of 64 columns x min(page_size, 128) rows
   CUtensorMap tm_v;
-  CUtensorMap tm_qr;  // shared keys: queries in boxes of few_rows / G tokens, K and V in boxes of few rows
-  CUtensorMap tm_kr;
+  CUtensorMap tm_kr;  // shared keys: boxes of rows_kernel's rows
   CUtensorMap tm_vr;
+  const void* q;
+  long long q_stride_t, q_stride_h;
   PagedParams p;
   int d;
   int is_short;  // units of copy_tokens only
@@ -105,7 +109,7 @@ constexpr int kMaxGroups = 4096;
 
 // Partial rows of a batch whose sequences share keys lie behind the CTAs' slots: first
 // those of the shared keys, one a row of the output, then those of the rest, then
-// kPartRows for each head of a part of rows_kernel.  Where a row's partial outputs are
+// few_rows for each head of a part of rows_kernel.  Where a row's partial outputs are
 // instead is said by a sum that no row can have:
 constexpr float kRowDone = -1.f;         // in the output already
 constexpr float kRowCut = -2.f;          // in the slots: the maximum holds the CTA that began the unit and the row there
@@ -113,12 +117,12 @@ constexpr float kRowCutOfRest = -3.f;    // as kRowCut, and there are shared key
 constexpr float kRowParts = -4.f;        // in parts: the maximum holds their first place, their number and the row there
 constexpr float kRowPartsOfRest = -5.f;  // as kRowParts, and there are shared keys, too
 
-// Rows of a 16-row matrix tile: what rows_kernel takes at a time, once (two CTAs an SM) or
-// twice (one: it has more in registers).
+// Rows of a 16-row matrix tile: what rows_kernel takes at a time, once or twice.
 constexpr int kFewRows = 16;
-inline __host__ __device__ int rows_ctas(int few_rows, int sms) { return few_rows <= kFewRows ? 2 * sms : sms; }
-// Keys of a stage of rows_kernel: 16 KB of K and V.
-inline constexpr int rows_keys(int d) { return d == 128 ? 32 : 64; }
+// Its CTAs an SM.
+inline __host__ __device__ constexpr int rows_ctas(int few_rows) { return few_rows <= kFewRows ? 2 : 1; }
+// Keys of a stage: 16 KB of K and V.
+inline __host__ __device__ constexpr int rows_keys(int d) { return d == 128 ? 32 : 64; }
 
 cudaError_t launch_shared_plan(const PagedLaunch& a, cudaStream_t stream);
 cudaError_t launch_shared_rows(const PagedLaunch& a, cudaStream_t stream);

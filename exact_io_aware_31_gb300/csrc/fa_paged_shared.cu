@@ -31,83 +31,96 @@ namespace {
 
 using namespace paged;
 
-constexpr size_t kGroupBytes = 8 + 5 * 4;  // of the plan's shared memory
-constexpr int kMaxCtas = 255;  // (what a row's mark has room for)
-// Least cost of a CTA's share of paged_kernel where other CTAs have the rest (a tenth of a
-// microsecond, as all costs): what a CTA takes until its first tile and behind its last.
-constexpr int kLeastShare = 60;
-// Fewest keys of a part of an entry with few rows.
-constexpr int kLeastPart = 256;
+constexpr size_t kGroupBytes = 8 + 6 * 4;  // of the plan's shared memory
+constexpr int kMaxCtas = 178;  // (their parts' places are below 2^13, as a row's mark has room for)
+static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
+// What a CTA of paged_kernel takes until its first tile and behind its last (a tenth of a
+// microsecond, as all costs): its share of the work is so much less than the others'.
+constexpr int kTileStart = 120;
+// Fewest keys of a part of an entry with few rows, and what parts' keys are multiples of.
+constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
 
 // ------------------------------------------------------------------ the lists --
-// Sums over the block of four values a thread: those in front of it; *total grows by all.
+// Sums over the block of two values a thread: those in front of it; *total grows by all.
 struct Sums {
-  long long cost, keys;
-  int entries, pieces;
+  long long a, b;
 };
 
 template <int THREADS>
-__device__ __forceinline__ Sums scan4(const Sums& v, Sums* warps, Sums* total) {
+__device__ __forceinline__ Sums scan2(long long a, long long b, Sums* warps, Sums* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
-  Sums s = v;
+  Sums s = {a, b};
 #pragma unroll
   for (int off = 1; off < 32; off *= 2) {
-    const long long cost = __shfl_up_sync(0xffffffffu, s.cost, off), keys = __shfl_up_sync(0xffffffffu, s.keys, off);
-    const int entries = __shfl_up_sync(0xffffffffu, s.entries, off);
-    const int pieces = __shfl_up_sync(0xffffffffu, s.pieces, off);
-    if (lane >= off) s.cost += cost, s.keys += keys, s.entries += entries, s.pieces += pieces;
+    const long long x = __shfl_up_sync(0xffffffffu, s.a, off), y = __shfl_up_sync(0xffffffffu, s.b, off);
+    if (lane >= off) s.a += x, s.b += y;
   }
   __syncthreads();  // the previous use of `warps` has been read
   if (lane == 31) warps[w] = s;
   __syncthreads();
-  s.cost += total->cost - v.cost;
-  s.keys += total->keys - v.keys;
-  s.entries += total->entries - v.entries;
-  s.pieces += total->pieces - v.pieces;
+  s.a += total->a - a;
+  s.b += total->b - b;
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
     const Sums x = warps[i];
-    if (i < w) s.cost += x.cost, s.keys += x.keys, s.entries += x.entries, s.pieces += x.pieces;
-    total->cost += x.cost, total->keys += x.keys, total->entries += x.entries, total->pieces += x.pieces;
+    if (i < w) s.a += x.a, s.b += x.b;
+    total->a += x.a, total->b += x.b;
   }
   return s;
 }
 
+// Keys of the parts of an entry with few rows that has `before` of all of those entries'
+// `keys` (times their heads) in front of it: an eighth of a CTA's share, and half of that for
+// the last fifth of the keys, which end when there is nothing else left to take.  With two row
+// tiles parts are twice as long, as there are half as many CTAs and places.
+__device__ __forceinline__ int part_keys(long long before, long long keys, int few_rows, int sms) {
+  const int tiles = few_rows / kFewRows;
+  long long n = keys / (kPartsASm * sms) >> (5 * before > 4 * keys ? 1 : 0);
+  n = (n * tiles + kPartStep - 1) / kPartStep * kPartStep;
+  return n < kLeastPart * tiles ? kLeastPart * tiles : n > 0x3fffff00 ? 0x3fffff00 : (int)n;
+}
+
 // One block.  Cuts each group's shared keys to whole pages that all of its sequences with
 // new tokens have in front of those, and drops them where computing them once costs no
-// less.  Entries of few rows are split where there are too few of them for all CTAs.
+// less.  Thread by thread the entries are the groups' shared keys, then the sequences; with
+// no more entries than threads each is looked at once.
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ unsigned long long plan_smem[];
-  const int S = p.S, NG = p.num_groups, tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const int S = p.S, NG = p.num_groups, N = NG + S, tid = threadIdx.x, lane = tid & 31;
   unsigned long long* apart = plan_smem;            // [NG] cost of a key tile for each of its sequences by itself
   int* start = reinterpret_cast<int*>(apart + NG);  // [NG + 1]
   int* front = start + NG + 1;                      // [NG] keys in front of the new tokens, the fewest
   int* first = front + NG;                          // [NG] first sequence with new tokens
-  int* members = first + NG;                        // [NG] how many there are
+  int* row = first + NG;                            // [NG] its first row
+  int* members = row + NG;                          // [NG] how many there are
   int* keys = members + NG;                         // [NG] shared keys
   __shared__ Sums warps[THREADS / 32];
+  __shared__ unsigned long long all_cost;  // of the entries with few rows, a key head
   const Shape sh = {2 * p.tile_tokens, p.tile_tokens, p.copy_tokens, p.causal};
   const int cap = p.max_pages << p.page_log2, few = p.few_rows / p.G;
+  const bool once = N <= THREADS;
   bool bad = false;
   auto sequence = [&](int s, bool& b) {
     return make_seq(__ldg(p.cu_seqlens + s), __ldg(p.cu_seqlens + s + 1), __ldg(p.kv_lens + s), p.T, cap, b);
   };
-  // The first of each thread's sequences and groups, asked for at once.
+  // Everything that the first of each thread's entries needs is asked for at once.
   Seq mine = {0, 0, 0};
-  if (tid < S) mine = sequence(tid, bad);
-  auto sequence_again = [&](int s) {
-    bool unused = false;
-    return s == tid ? mine : sequence(s, unused);
-  };
-  const int want0 = tid < NG ? __ldg(p.prefix_lens + tid) : 0;
+  if (tid >= NG && tid < N) mine = sequence(tid - NG, bad);
+  const int row0 = imin(imax(__ldg(p.cu_seqlens), 0), p.T), row1 = imin(imax(__ldg(p.cu_seqlens + S), 0), p.T);
+  int want = 0, last_row = 0;
   for (int g = tid; g <= NG && NG > 0; g += THREADS) {
     const int at = __ldg(p.groups + g);
     start[g] = imin(imax(at, 0), S);
     bad = bad || start[g] != at || (g > 0 && at < __ldg(p.groups + g - 1));
-    if (g < NG) front[g] = first[g] = 0x7fffffff, members[g] = 0, apart[g] = 0;
+    if (g < NG) front[g] = first[g] = row[g] = 0x7fffffff, members[g] = 0, apart[g] = 0;
   }
+  if (tid < NG) {
+    want = __ldg(p.prefix_lens + tid);
+    last_row = __ldg(p.cu_seqlens + imin(imax(__ldg(p.groups + tid + 1), 0), S));
+  }
+  if (tid == 0) all_cost = 0;
   __syncthreads();
   // A sequence's group: the last one that begins at it or in front (-1: none).
   auto group_of = [&](int s) {
@@ -121,19 +134,25 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     }
     return lo - 1 < NG ? lo - 1 : -1;
   };
+  // Cost of a key head of an entry.
+  auto cost_of_entry = [&](const SharedSeq& q) {
+    return q.qn <= few ? cost_of<D>(1, q.kv, kShortCopies) : cost_of_seq<D>(q, sh);
+  };
+  int my_group = -1;  // of the sequence that `mine` is
   if (NG > 0) {
-    for (int s0 = 0; s0 < S; s0 += THREADS) {
-      const int s = s0 + tid;
-      int g = -1, f = 0x7fffffff, cost = 0;
-      if (s < S) {
-        const Seq q = sequence_again(s);
-        if (s0 > 0) sequence(s, bad);
+    for (int i0 = 0; i0 < N; i0 += THREADS) {
+      const int i = i0 + tid, s = i - NG;
+      int g = -1, f = 0x7fffffff, q0 = 0, cost = 0;
+      if (i >= NG && i < N) {
+        const Seq q = i0 == 0 ? mine : sequence(s, bad);
         if (q.qn > 0 && (g = group_of(s)) >= 0) {
           f = imax(0, p.causal ? q.kv - q.qn : q.kv);
+          q0 = q.q0;
           const int full = q.qn / sh.ut, rest = q.qn - full * sh.ut;
           cost = full * tile_cost<D>(sh.form(sh.ut)) + (rest > 0 ? tile_cost<D>(sh.form(rest)) : 0);
         }
       }
+      if (i0 == 0) my_group = g;
       // most warps hold sequences of one group alone
       const unsigned in = __ballot_sync(0xffffffffu, g >= 0);
       if (in == 0) continue;
@@ -141,41 +160,39 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
       if (__all_sync(0xffffffffu, g < 0 || g == g0)) {
         const int least = __reduce_min_sync(0xffffffffu, f);
         const int sum = __reduce_add_sync(0xffffffffu, cost);
-        if (lane == 0) {
+        if (lane == __ffs(in) - 1) {
           atomicMin(&front[g0], least);
-          atomicMin(&first[g0], s0 + warp * 32 + __ffs(in) - 1);
+          atomicMin(&first[g0], s);
+          atomicMin(&row[g0], q0);
           atomicAdd(&members[g0], __popc(in));
           atomicAdd(&apart[g0], (unsigned long long)sum);
         }
       } else if (g >= 0) {
         atomicMin(&front[g], f);
         atomicMin(&first[g], s);
+        atomicMin(&row[g], q0);
         atomicAdd(&members[g], 1);
         atomicAdd(&apart[g], (unsigned long long)cost);
       }
     }
     __syncthreads();
   }
-  // The group's entry, `n` keys of its first sequence.
+  // A group's entry: `n` keys of its first sequence, all rows from that one's on.
   auto prefix_of = [&](int g, int n) {
     SharedSeq q;
-    const int end = imin(imax(__ldg(p.cu_seqlens + start[g + 1]), 0), p.T);
-    q.q0 = imin(imax(__ldg(p.cu_seqlens + first[g]), 0), p.T);
-    q.qn = imax(0, end - q.q0);
+    const int end = g == tid ? last_row : __ldg(p.cu_seqlens + start[g + 1]);
+    q.q0 = row[g];
+    q.qn = imax(0, imin(imax(end, 0), p.T) - q.q0);
     q.kv = n;
     q.row = first[g];
     q.page0 = 0;
     q.kind = kPrefix;
     return q;
   };
-  // Cost of a key head of an entry.
-  auto cost_of_entry = [&](const SharedSeq& q) {
-    return q.qn <= few ? cost_of<D>(1, q.kv, kShortCopies) : cost_of_seq<D>(q, sh);
-  };
   for (int g = tid; g < NG; g += THREADS) {
-    const int want = g == tid ? want0 : __ldg(p.prefix_lens + g);
-    bad = bad || want < 0 || want > cap;
-    int n = imin(imax(want, 0), front[g]) >> p.page_log2 << p.page_log2;
+    const int x = g == tid ? want : __ldg(p.prefix_lens + g);
+    bad = bad || x < 0 || x > cap;
+    int n = imin(imax(x, 0), front[g]) >> p.page_log2 << p.page_log2;
     if (members[g] < 2) n = 0;
     if (n > 0) {
       const SharedSeq q = prefix_of(g, n);
@@ -183,20 +200,19 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     }
     keys[g] = n;
   }
-  __syncthreads();
-  // Entry i: the groups' shared keys, then the sequences.
+  if (NG > 0) __syncthreads();
   auto entry = [&](int i) {
     SharedSeq q;
     q.q0 = q.qn = q.kv = q.row = q.page0 = q.kind = 0;
     if (i < NG) {
       if (keys[i] > 0) q = prefix_of(i, keys[i]);
-    } else if (i < NG + S) {
-      const int s = i - NG;
-      static_cast<Seq&>(q) = sequence_again(s);
+    } else if (i < N) {
+      bool unused = false;
+      static_cast<Seq&>(q) = i == tid ? mine : sequence(i - NG, unused);
       if (q.qn > 0) {
-        const int g = NG > 0 ? group_of(s) : -1;
+        const int g = i == tid ? my_group : NG > 0 ? group_of(i - NG) : -1;
         const int n = g >= 0 ? keys[g] : 0;
-        q.row = s;
+        q.row = i - NG;
         q.page0 = n >> p.page_log2;
         q.kv -= n;
         q.kind = n > 0 ? kRest : kAlone;
@@ -204,96 +220,120 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     }
     return q;
   };
-  // Of the entries with few rows: all keys, and what a part of them is to hold.
-  Sums total = {0, 0, 0, 0};
-  long long rows_cost = 0;
-  for (int i0 = 0; i0 < NG + S; i0 += THREADS) {
-    const SharedSeq q = entry(i0 + tid);
+  // Costs and keys in front of each entry, of those with many and with few rows.
+  SharedSeq q;
+  Sums front_of = {0, 0}, sum = {0, 0};
+  for (int i0 = 0; i0 < N; i0 += THREADS) {
+    q = entry(i0 + tid);
     const bool few_rows = q.qn > 0 && q.qn <= few;
-    const Sums v = {few_rows ? cost_of_entry(q) : 0, few_rows ? q.kv : 0, 0, 0};
-    scan4<THREADS>(v, warps, &total);
+    const long long cost = q.qn > 0 ? cost_of_entry(q) : 0;
+    front_of = scan2<THREADS>(few_rows ? 0 : cost, few_rows ? q.kv : 0, warps, &sum);
+    long long few_cost = few_rows ? cost : 0;
+#pragma unroll
+    for (int off = 16; off > 0; off /= 2) few_cost += __shfl_xor_sync(0xffffffffu, few_cost, off);
+    if (lane == 0 && few_cost > 0) atomicAdd(&all_cost, (unsigned long long)few_cost);
+    __syncthreads();
   }
-  rows_cost = total.cost * p.Hk;
-  const long long share = total.keys * p.Hk / (kPartsASm * p.sms);
-  const int part = imax(kLeastPart, (int)imin(0x3fffff00, (int)(share > 0x3fffff00 ? 0x3fffff00 : share) + 127) / 128 * 128);
+  const long long rows_cost = (long long)all_cost * p.Hk, all_keys = sum.b * p.Hk;
   const SharedLists at = shared_lists(S, NG, p.sms);
   uint8_t* base = reinterpret_cast<uint8_t*>(p.plan);
   long long* costs = reinterpret_cast<long long*>(base + at.cost);
   SharedEntry* list = reinterpret_cast<SharedEntry*>(base + at.list);
   SharedPiece* pieces = reinterpret_cast<SharedPiece*>(base + at.pieces);
-  // The lists.  `keys` of the sums counts the parts of split entries here.
-  total = {0, 0, 0, 0};
-  for (int i0 = 0; i0 < NG + S; i0 += THREADS) {
-    const SharedSeq q = entry(i0 + tid);
+  Sums again = {0, 0}, total = {0, 0};  // total.a: entries << 32 | pieces, total.b: places
+  for (int i0 = 0; i0 < N; i0 += THREADS) {
+    if (!once) {
+      q = entry(i0 + tid);
+      const bool few_rows = q.qn > 0 && q.qn <= few;
+      front_of = scan2<THREADS>(q.qn > 0 && !few_rows ? cost_of_entry(q) : 0, few_rows ? q.kv : 0, warps, &again);
+    }
     const bool few_rows = q.qn > 0 && q.qn <= few, many_rows = q.qn > few;
-    const int parts = few_rows ? imax(1, (q.kv + part - 1) / part) : 0;
-    const Sums v = {many_rows ? cost_of_entry(q) * p.Hk : 0, parts > 1 ? parts : 0, many_rows, parts};
-    const Sums before = scan4<THREADS>(v, warps, &total);
+    int part = 1, parts = 0;
+    if (few_rows) {
+      part = part_keys(front_of.b * p.Hk, all_keys, p.few_rows, p.sms);
+      parts = imax(1, (q.kv + part - 1) / part);
+    }
+    const Sums before = scan2<THREADS>((long long)many_rows << 32 | parts, parts > 1 ? parts : 0, warps, &total);
     if (many_rows) {
-      costs[before.entries] = before.cost;
-      list[before.entries].seq = make_int4(q.q0, q.qn, q.kv, q.row);
-      list[before.entries].how = make_int4(q.page0, q.kind, 0, 0);
+      const int e = (int)(before.a >> 32);
+      costs[e] = front_of.a * p.Hk;
+      list[e].seq = make_int4(q.q0, q.qn, q.kv, q.row);
+      list[e].how = make_int4(q.page0, q.kind, 0, 0);
     }
     for (int k = 0; k < parts; ++k) {
-      SharedPiece& e = pieces[before.pieces + k];
+      SharedPiece& e = pieces[(int)(before.a & 0xffffffff) + k];
       e.seq = make_int4(q.q0, q.qn, q.kv, q.row);
       e.how = make_int4(q.page0, q.kind, k * part, k + 1 < parts ? (k + 1) * part : q.kv);
-      e.part = make_int4(parts > 1 ? ((int)before.keys + k) * p.Hk : -1, parts, k, 0);
+      e.part = make_int4(parts > 1 ? ((int)before.b + k) * p.Hk : -1, parts, k, 0);
     }
   }
   if (tid == 0) {
-    costs[total.entries] = total.cost;
-    int ctas = ctas_for<D>(total.cost, p.sms);
+    const int entries = (int)(total.a >> 32);
+    const long long cost = sum.a * p.Hk;
+    costs[entries] = cost;
+    int ctas = ctas_for<D>(cost, p.sms);
     if (rows_cost > 0 && ctas > 1) {
-      const long long even = (total.cost + rows_cost) / p.sms, least = 128ll * kLeastShare;
+      // as many as end when the others do
+      const long long even = (cost + rows_cost) / p.sms - 128 * kTileStart, least = 128 * kTileStart;
       const long long each = even > least ? even : least;
-      const long long most = (total.cost + each - 1) / each;
+      const long long most = (cost + each - 1) / each;
       ctas = most < ctas ? (int)most : ctas;
     }
-    const int row0 = imin(imax(__ldg(p.cu_seqlens), 0), p.T);
-    const int row1 = imin(imax(__ldg(p.cu_seqlens + S), 0), p.T);
     int4* head = reinterpret_cast<int4*>(p.plan);
-    head[0] = make_int4(total.entries, total.pieces, ctas, 2 * rows_ctas(p.few_rows, p.sms));
+    head[0] = make_int4(entries, (int)(total.a & 0xffffffff), ctas, 0);
     head[1] = make_int4(row0, row1, 0, 0);
   }
   if (bad) record_index(p.status);
 }
 
 // ------------------------------------------------------------------ the merge --
-// D / 8 lanes a row of the output (a token's query head).  SPLIT warps share a row's
-// parts: all eight of a block where rows are few and a group's keys may be cut into
-// many parts, one where rows are many.  Parts are added in a fixed order: those of
-// the sequence's own keys, then those of the shared ones.
+// D / 8 lanes a row of the output (a token's query head).  Bound by latency: a row's mark,
+// the end of a unit that was cut, its parts, one after the other; so every warp takes rows
+// of its own, looks at 32 marks at a time, asks for four parts at once, and all rows of a
+// step are under way at the same time.  Where rows are so few that the warps outnumber them, the eight of a block share a
+// row's parts (a group's keys, cut into a part a CTA).  Parts are added in a fixed order:
+// those of the sequence's own keys, then those of the shared ones.
 template <int D, int SPLIT>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const PagedParams p) {
-  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kRowsABlock = kRowsAWarp * 8 / SPLIT;
-  __shared__ short ends[kMaxCtas + 1];  // the CTA that ends the unit that CTA c began
+__global__ void __launch_bounds__(256, 3) shared_merge_kernel(const PagedParams p) {
+  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kAtOnce = 4;
   __shared__ float4 sum[SPLIT > 1 ? 8 : 1][32][2];
   __shared__ float2 stat[SPLIT > 1 ? 8 : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l8 = lane % kLanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int ctas = __ldcg(&p.plan->ctas);
-  const int4 plan = __ldcg(reinterpret_cast<const int4*>(p.plan) + 1);
-  const int Hq = p.Hk * p.G;
-  const size_t rows = (size_t)(plan.y - plan.x) * Hq, row0 = (size_t)plan.x * Hq;
+  const int4 head0 = __ldcg(reinterpret_cast<const int4*>(p.plan));
+  const int4 head1 = __ldcg(reinterpret_cast<const int4*>(p.plan) + 1);
+  const int ctas = head0.z, Hq = p.Hk * p.G;
+  const size_t rows = (size_t)(head1.y - head1.x) * Hq, row0 = (size_t)head1.x * Hq;
   // (the last one: a CTA gave up, and what the workspace says is not this call's)
-  if (plan.y <= plan.x || (size_t)blockIdx.x * kRowsABlock >= rows || plan.z) return;
-  if ((int)threadIdx.x < ctas) ends[threadIdx.x] = (short)__ldcg(p.hdr + (size_t)threadIdx.x * kPagedHdr + 4);
-  __syncthreads();
-  {
-    const int c = threadIdx.x;
-    int last = c + 1;
-    while (last < ctas - 1 && ends[last] == 1) ++last;
-    __syncthreads();
-    if (c < ctas) ends[c] = (short)imin(last, ctas - 1);
-    __syncthreads();
-  }
+  if (head1.y <= head1.x || head1.z) return;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   const size_t slots = (size_t)p.sms * (2 * kPagedRows), all = (size_t)p.T * Hq;
-  const int places = shared_parts(p.sms);
-  for (size_t n0 = (size_t)blockIdx.x * kRowsABlock; n0 < rows; n0 += (size_t)gridDim.x * kRowsABlock) {
-    const size_t n = n0 + (SPLIT > 1 ? 0 : warp * kRowsAWarp) + lane / kLanes;
-    const size_t row = row0 + (n < rows ? n : rows - 1);
+  const int few_rows = imax(p.few_rows, kFewRows), places = shared_parts(p.sms) * kPartRows / few_rows;
+  // Rows of a warp (or, split, of a block): the next `chunk`, of which `todo` are not done.
+  const int chunk = SPLIT > 1 || rows <= (size_t)gridDim.x * (8 * kRowsAWarp) ? kRowsAWarp : 32;
+  const size_t first = ((size_t)blockIdx.x * (SPLIT > 1 ? 1 : 8) + (SPLIT > 1 ? 0 : warp)) * chunk;
+  const size_t stride = (size_t)gridDim.x * (SPLIT > 1 ? 1 : 8) * chunk;
+  size_t n0 = first;
+  unsigned todo = 0;
+  bool fresh = true;
+  for (;;) {
+    if (fresh) {
+      if (n0 >= rows) break;
+      const bool mine = lane < chunk && n0 + lane < rows;
+      todo = __ballot_sync(0xffffffffu, mine && __ldcg(&ml[slots + all + row0 + n0 + lane].y) != kRowDone);
+    }
+    // the lane groups' rows: the first ones of those left (a group without one goes along)
+    int at_row = -1;
+#pragma unroll
+    for (int k = 0; k < kRowsAWarp; ++k) {
+      if (lane / kLanes == k) at_row = __ffs(todo) - 1;
+      todo &= todo - 1;
+    }
+    const bool has = at_row >= 0;
+    const size_t row = row0 + n0 + (has ? at_row : 0);
+    fresh = todo == 0;
+    if (fresh) n0 += stride;
+    if (!__any_sync(0xffffffffu, has)) continue;
     // Where the parts are: `count` of a unit cut from CTA c on, of an entry's parts from place
     // c on, or one in the row's own place.  (What is said is cut to what there is room for.)
     enum { kHere, kCut, kPlaces };
@@ -305,60 +345,76 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const PagedParams p) 
       Parts u = {kHere, 0, 0, 1};
       if (x.y == kRowCut || x.y == kRowCutOfRest) {
         u.how = kCut;
-        u.c = imin(imax(said / kPagedRows, 0), imax(ctas, 1) - 1);
+        u.c = imin(imax(said / kPagedRows, 0), p.sms - 1);
         u.at = said & (kPagedRows - 1);
-        u.count = ctas > 0 ? imax(1, ends[u.c] - u.c + 1) : 1;
       } else if (x.y == kRowParts || x.y == kRowPartsOfRest) {
         u.how = kPlaces;
-        u.at = said & (kPartRows - 1);
+        u.at = said & (few_rows - 1);
         u.count = said >> 5 & 8191;
         u.c = imax(said >> 18, 0);
       }
       return u;
     };
-    const float2 own = __ldcg(ml + slots + all + row), head = __ldcg(ml + slots + row);
-    const bool done = own.y == kRowDone;
+    const float2 own = __ldcg(ml + slots + all + row), shared = __ldcg(ml + slots + row);
+    const bool done = !has || own.y == kRowDone;
     Parts a = parts_of(own), b = {kHere, 0, 0, 0};
     if (done)
-      a.count = 0;
+      a = {kHere, 0, 0, 0};
     else if (own.y != kRowCut && own.y != kRowParts)
-      b = parts_of(head);
+      b = parts_of(shared);
+    // A cut unit's parts: up to the first CTA behind c whose first slot ends its unit.
+    auto find_end = [&](Parts& u) {
+      bool open = u.how == kCut;
+      for (int at = u.c + 1; __any_sync(0xffffffffu, open); at += kLanes) {
+        const int c = at + l8;
+        const bool goes_on = open && c < ctas - 1 && __ldcg(p.hdr + (size_t)c * kPagedHdr + 4) == 1;
+        const unsigned ends = __ballot_sync(0xffffffffu, open && !goes_on) >> (lane / kLanes * kLanes) & ((1u << (kLanes - 1) << 1) - 1);
+        if (open && ends) {
+          u.count = imin(at + __ffs(ends) - 1, imax(ctas, 1) - 1) - u.c + 1;
+          u.count = imax(u.count, 1);
+          open = false;
+        }
+      }
+    };
+    find_end(a);
+    find_end(b);
     const int count = a.count + b.count;
     auto place = [&](int i) {
       const bool of_b = i >= a.count;
       const Parts& u = of_b ? b : a;
       const int k = of_b ? i - a.count : i;
       if (u.how == kHere) return slots + (of_b ? 0 : all) + row;
-      if (u.how == kPlaces) return slots + 2 * all + (size_t)imin(u.c + k * p.Hk, places - 1) * kPartRows + u.at;
+      if (u.how == kPlaces) return slots + 2 * all + (size_t)imin(u.c + k * p.Hk, places - 1) * few_rows + u.at;
       return ((size_t)imin(u.c + k, p.sms - 1) * 2 + (k == 0 ? 1 : 0)) * kPagedRows + u.at;
     };
     float m = -INFINITY, l = 0.f, acc[8] = {};
-    float4 v0 = {}, v1 = {};
-    float2 x = {-INFINITY, 0.f};
-    auto load = [&](int i) {
-      const size_t at = place(i);
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + at * D) + 2 * l8;
-      v0 = __ldcg(src), v1 = __ldcg(src + 1), x = __ldcg(ml + at);
-    };
     auto add = [&](float w, const float4& u, const float4& v) {
       acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]), acc[2] = fmaf(w, u.z, acc[2]);
       acc[3] = fmaf(w, u.w, acc[3]), acc[4] = fmaf(w, v.x, acc[4]), acc[5] = fmaf(w, v.y, acc[5]);
       acc[6] = fmaf(w, v.z, acc[6]), acc[7] = fmaf(w, v.w, acc[7]);
     };
-    const int i0 = SPLIT > 1 ? warp : 0;
-    if (i0 < count) load(i0);
-    for (int i = i0; i < count; i += SPLIT) {
-      const float4 u0 = v0, u1 = v1;
-      const float2 y = x;
-      if (i + SPLIT < count) load(i + SPLIT);
-      if (y.y == 0.f) continue;  // saw no key
-      const float m_new = fmaxf(m, y.x);
-      const float old = m == -INFINITY ? 0.f : ex2(m - m_new), w = ex2(y.x - m_new);
-      l = fmaf(w, y.y, l * old);
+    for (int i0 = SPLIT > 1 ? warp : 0; i0 < count; i0 += kAtOnce * SPLIT) {
+      float4 v[kAtOnce][2];
+      float2 x[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] *= old;
-      add(w, u0, u1);
-      m = m_new;
+      for (int k = 0; k < kAtOnce; ++k) {
+        x[k] = make_float2(-INFINITY, 0.f);
+        if (i0 + k * SPLIT >= count) continue;
+        const size_t at = place(i0 + k * SPLIT);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + at * D) + 2 * l8;
+        v[k][0] = __ldcg(src), v[k][1] = __ldcg(src + 1), x[k] = __ldcg(ml + at);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (x[k].y == 0.f) continue;  // saw no key
+        const float m_new = fmaxf(m, x[k].x);
+        const float old = m == -INFINITY ? 0.f : ex2(m - m_new), w = ex2(x[k].x - m_new);
+        l = fmaf(w, x[k].y, l * old);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= old;
+        add(w, v[k][0], v[k][1]);
+        m = m_new;
+      }
     }
     if constexpr (SPLIT > 1) {
       sum[warp][lane][0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -379,7 +435,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const PagedParams p) 
         }
       }
     }
-    if ((SPLIT == 1 || warp == 0) && n < rows && !done) {
+    if ((SPLIT == 1 || warp == 0) && !done) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[l8] =
           make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
@@ -395,9 +451,9 @@ cudaError_t launch_merge_t(const PagedLaunch& a, cudaStream_t stream) {
   if (a.grid > kMaxCtas) return cudaErrorInvalidConfiguration;
   const size_t rows = (size_t)a.p.T * a.p.Hk * a.p.G;
   constexpr int kRowsAWarp = 32 / (D / 8);
-  const bool few = rows <= 8192;
+  const bool few = rows <= (size_t)a.grid * 3 * kRowsAWarp;  // (as many blocks as there is room for)
   const size_t a_block = few ? kRowsAWarp : kRowsAWarp * 8;
-  const size_t blocks = (rows + a_block - 1) / a_block, most = (size_t)a.grid * 32;
+  const size_t blocks = (rows + a_block - 1) / a_block, most = (size_t)a.grid * 8;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -425,7 +481,7 @@ cudaError_t launch_plan_t(const PagedLaunch& a, cudaStream_t stream) {
 cudaError_t launch_shared_plan(const PagedLaunch& a, cudaStream_t stream) {
   // (its sums over the block take longer with more threads)
   if (a.p.S + a.p.num_groups <= 256) return a.d == 64 ? launch_plan_t<64, 256>(a, stream) : launch_plan_t<128, 256>(a, stream);
-  return a.d == 64 ? launch_plan_t<64, 1024>(a, stream) : launch_plan_t<128, 1024>(a, stream);
+  return a.d == 64 ? launch_plan_t<64, 512>(a, stream) : launch_plan_t<128, 512>(a, stream);
 }
 
 cudaError_t launch_shared_merge(const PagedLaunch& a, cudaStream_t stream) {

@@ -9,7 +9,6 @@
 #include <cstdint>
 
 #include "../../include/fa.h"
-#include "fa_common.cuh"
 #include "fa_host.h"
 #include "fa_norm_rope.cuh"
 #include "fa_paged.cuh"
@@ -339,14 +338,29 @@ PagedWorkspace shared_workspace(int sms, int T, int S, int num_groups, int Hq, i
 }
 
 // A pool [pages, Hk, page_size, d] of any strides: boxes of 64 columns by the
-// rows of a page, at most `rows` (a key tile's 128; 128-byte swizzle).
+// rows of a page, at most a key tile's 128 (128-byte swizzle).
 int make_pool_map(CUtensorMap* m, const void* base, int pages, int Hk, int page_size, int d, long long sp,
-                  long long sh, long long sr, int rows = kTileRows) {
+                  long long sh, long long sr) {
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)Hk, (cuuint64_t)pages};
   cuuint64_t strides[3] = {(cuuint64_t)sr * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)(page_size < rows ? page_size : rows), 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)(page_size < 128 ? page_size : 128), 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// The same for rows_kernel: boxes of `rows` rows with all of their columns, a block of 64
+// columns behind the other.
+int make_rows_map(CUtensorMap* m, const void* base, int pages, int Hk, int page_size, int d, long long sp,
+                  long long sh, long long sr, int rows) {
+  cuuint64_t dims[5] = {64, (cuuint64_t)page_size, (cuuint64_t)d / 64, (cuuint64_t)Hk, (cuuint64_t)pages};
+  cuuint64_t strides[4] = {(cuuint64_t)sr * 2, 128, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)(page_size < rows ? page_size : rows), (cuuint32_t)d / 64, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? FA_OK
@@ -457,13 +471,16 @@ int fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, 
     p.num_groups = groups->n;
     p.plan = reinterpret_cast<SharedPlan*>(ws + w.plan);
     p.sms = dev.sms;
+    p.hk_inverse = 0xffffffffu / (unsigned)Hk;
     // Rows that rows_kernel takes of a key head: a single token's group at least, and what a
     // step of max_q tokens has where that is no more than its larger form's.
     p.few_rows = G > 2 * kFewRows ? 0 : G > kFewRows || (max_q <= 2 * kFewRows / G && max_q * G > kFewRows) ? 2 * kFewRows : kFewRows;
+    a.q = q;
+    a.q_stride_t = q_stride_t;
+    a.q_stride_h = q_stride_h;
     if (p.few_rows > 0 &&
-        (make_ragged_map(&a.tm_qr, q, T, Hk, G, d, p.few_rows / G, q_stride_t, q_stride_h) ||
-         make_pool_map(&a.tm_kr, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0], rows_keys(d)) ||
-         make_pool_map(&a.tm_vr, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1], rows_keys(d))))
+        (make_rows_map(&a.tm_kr, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0], rows_keys(d)) ||
+         make_rows_map(&a.tm_vr, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1], rows_keys(d))))
       return FA_ERR_CUDA;
   }
   if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||

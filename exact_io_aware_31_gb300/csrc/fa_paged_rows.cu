@@ -288,10 +288,9 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       // This warp's stages: place, place + kWarps, .. of the unit; `takers` warps have some.
       const int place = (warp + C::kWarps - u.base % C::kWarps) % C::kWarps;
       const int takers = imax(1, imin(u.stages, C::kWarps));
-      // Rows that fit into a room are joined by the last warp to bring its part; more of them
-      // (blocking) by all, as many columns at a time as fit.
-      const int rows_log2 = valid <= 4 ? 2 : valid <= 8 ? 3 : valid <= 16 ? 4 : 5;
-      const bool fits = (D << rows_log2) <= C::kJoinFloats;
+      // Rows that fit into a room are joined by the last warp to bring its part; more of them by
+      // all, out of the buffers of their last stages, which the producer gets back then.
+      const bool fits = valid * D <= C::kJoinFloats, hold = !fits && takers > 1;
       if (place >= takers && (fits || takers == 1)) {  // nothing to do but to keep count
         if (takers > 1) {
           const uint32_t use = rooms++;
@@ -315,8 +314,9 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
                                                                 (size_t)(row - tok * p.G) * q_stride_h) + c;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          qa[i / 2][k][i & 1] = row < valid ? __ldg(src + 8 * k) : 0u;
-          qa[i / 2][k][2 + (i & 1)] = row < valid ? __ldg(src + 8 * k + 4) : 0u;
+          const bool there = row < valid && place < takers;
+          qa[i / 2][k][i & 1] = there ? __ldg(src + 8 * k) : 0u;
+          qa[i / 2][k][2 + (i & 1)] = there ? __ldg(src + 8 * k + 4) : 0u;
         }
         lim[i] = causal ? imin(past + tok, u.kv - 1) : u.kv - 1;
         m[i] = -INFINITY;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
           }
         if (used < C::kKeys) fence_proxy_async_smem();  // the next copy comes behind the zeros
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (lane == 0 && !(hold && i + C::kWarps >= u.stages)) mbar_arrive(&empty[st]);
       }
       if (!ok) break;
 #pragma unroll
@@ -477,42 +477,37 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
         __syncwarp();
         continue;
       }
-      // Through a room: this warp's (m, l) and `cols` columns of its rows.  (Every warp takes part in
-      // every use of a room, if only by its arrival, so that none is a use ahead or behind.)
-      const int cols = imin(D, C::kJoinFloats >> rows_log2);
-      const float2* room_ml = nullptr;
-      const float* room = nullptr;
-      uint32_t use = 0;
-      auto bring = [&](int c0) {
-        use = rooms++;
-        if (!wait_short(&room_free[use & 1], ((use >> 1) & 1) ^ 1, status)) return false;
-        float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl) + (use & 1) * (C::kWarps * C::kRows);
-        float* to = reinterpret_cast<float*>(sm + C::kOffJoin) + (use & 1) * (C::kWarps * C::kJoinFloats);
-        room_ml = ml;
-        room = to;
-        if (place >= takers) return true;
+      // This warp's (m, l) and rows.  (Every warp takes part in every use of a room, if only by
+      // its arrival, so that none is a use ahead or behind.)
+      const uint32_t use = rooms++, r = use & 1;
+      if (!(ok = wait_short(&room_free[r], ((use >> 1) & 1) ^ 1, status))) break;
+      float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl) + r * (C::kWarps * C::kRows);
+      auto rows_of = [&](int w) {  // of the w-th taker
+        return hold ? reinterpret_cast<float*>(
+                          sm + ((u.base + w + (u.stages - 1 - w) / C::kWarps * C::kWarps) % C::kStages) * C::kStageBytes)
+                    : reinterpret_cast<float*>(sm + C::kOffJoin) + (r * C::kWarps + w) * C::kJoinFloats;
+      };
+      if (place < takers) {
+        float* to = rows_of(place);
 #pragma unroll
         for (int i2 = 0; i2 < 2 * MT; ++i2) {
           const int row = g + 8 * i2;
           if (row >= valid) continue;
           if (c == 0) ml[place * C::kRows + row] = make_float2(m[i2], l[i2]);
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const int col = 8 * n + 2 * c - c0;
-            if (col < 0 || col >= cols) continue;
-            *reinterpret_cast<float2*>(to + place * C::kJoinFloats + row * cols + (col ^ (8 * (row & 1) & (cols - 1)))) =
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(to + row * D + ((8 * n + 2 * c) ^ (8 * (row & 3)))) =
                 make_float2(o[i2 / 2][n][2 * (i2 & 1)], o[i2 / 2][n][2 * (i2 & 1) + 1]);
-          }
         }
-        return true;
-      };
-      // Four columns of a row from the room, joined in the order of the unit's stages.
-      auto join = [&](int row, int col4, int c0) {
+      }
+      // Four columns of a row, joined in the order of the unit's stages.
+      auto join = [&](int x) {
+        const int row = x / (D / 4), col = x % (D / 4) * 4;
         float2 part[C::kWarps];
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
-          part[w] = w < takers ? room_ml[w * C::kRows + row] : make_float2(-INFINITY, 0.f);
+          part[w] = w < takers ? ml[w * C::kRows + row] : make_float2(-INFINITY, 0.f);
           top = fmaxf(top, part[w].x);
         }
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -520,13 +515,11 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
         for (int w = 0; w < C::kWarps; ++w) {
           if (part[w].y == 0.f) continue;  // saw no key (a row of NaN has a maximum of -inf, too)
           const float wt = ex2(part[w].x - top);
-          const float4 x = *reinterpret_cast<const float4*>(room + w * C::kJoinFloats + row * cols +
-                                                            ((4 * col4) ^ (8 * (row & 1) & (cols - 1))));
+          const float4 v = *reinterpret_cast<const float4*>(rows_of(w) + row * D + (col ^ (8 * (row & 3))));
           sum = fmaf(wt, part[w].y, sum);
-          y.x = fmaf(wt, x.x, y.x), y.y = fmaf(wt, x.y, y.y), y.z = fmaf(wt, x.z, y.z), y.w = fmaf(wt, x.w, y.w);
+          y.x = fmaf(wt, v.x, y.x), y.y = fmaf(wt, v.y, y.y), y.z = fmaf(wt, v.z, y.z), y.w = fmaf(wt, v.w, y.w);
         }
         const size_t at = out_row(row);
-        const int col = c0 + 4 * col4;
         if (direct) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + col) =
@@ -536,40 +529,35 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
         }
         if (col == 0) put_ml(row, at, top, sum);
       };
-      if (fits) {
-        if (!(ok = bring(0))) break;
+      // Counts the warps that came here in this use.
+      auto came = [&] {
         __threadfence_block();
         __syncwarp();
-        int before = 0;
-        if (lane == 0) {
-#ifdef FA_TEST_HOOKS
-          if (warp != 0 || *reinterpret_cast<volatile int*>(&g_fa_test_rows) != 1)
-#endif
-            before = atomicAdd(&arrived[use & 1], 1);
-        }
+        int before = lane == 0 ? atomicAdd(&arrived[r], 1) : 0;
         before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == takers - 1) {  // the last one
-          __threadfence_block();
-          for (int x = lane; x < valid * (D / 4); x += 32) join(x / (D / 4), x % (D / 4), 0);
-          __syncwarp();
-          if (lane == 0) arrived[use & 1] = 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&room_free[use & 1]);
-      } else {
-        for (int c0 = 0; c0 < D; c0 += cols) {
-          if (!(ok = bring(c0))) break;
+        __threadfence_block();
+        return before + 1;
+      };
 #ifdef FA_TEST_HOOKS
-          if (warp != 0 || *reinterpret_cast<volatile int*>(&g_fa_test_rows) != 1)
+      if (warp == 0 && *reinterpret_cast<volatile int*>(&g_fa_test_rows) == 1) continue;
 #endif
-            mbar_arrive(&room_full[use & 1]);
-          if (!(ok = wait_short(&room_full[use & 1], fulls >> (use & 1) & 1, status))) break;
-          fulls ^= 1u << (use & 1);
-          for (int x = threadIdx.x; x < valid * (cols / 4); x += 32 * C::kWarps) join(x / (cols / 4), x % (cols / 4), c0);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&room_free[use & 1]);
+      if (hold) {
+        mbar_arrive(&room_full[r]);
+        if (!(ok = wait_short(&room_full[r], fulls >> r & 1, status))) break;
+        fulls ^= 1u << r;
+        for (int x = threadIdx.x; x < valid * (D / 4); x += 32 * C::kWarps) join(x);
+        fence_proxy_async_smem();  // the next copies come behind these accesses
+        if (came() == C::kWarps) {
+          if (lane < takers)
+            mbar_arrive(&empty[(u.base + lane + (u.stages - 1 - lane) / C::kWarps * C::kWarps) % C::kStages]);
+          if (lane == 0) arrived[r] = 0;
         }
+      } else if (came() == takers) {
+        for (int x = lane; x < valid * (D / 4); x += 32) join(x);
+        if (lane == 0) arrived[r] = 0;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&room_free[r]);
       if (__any_sync(0xffffffffu, aborted(abort_flag))) ok = false;
     }
     if (!ok) *abort_flag = 1;

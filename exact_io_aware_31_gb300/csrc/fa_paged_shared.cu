@@ -34,9 +34,15 @@ using namespace paged;
 constexpr size_t kGroupBytes = 8 + 6 * 4;  // of the plan's shared memory
 constexpr int kMaxCtas = 178;  // (their parts' places are below 2^13, as a row's mark has room for)
 static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
-// What a CTA of paged_kernel takes until its first tile and behind its last (a tenth of a
-// microsecond, as all costs): its share of the work is so much less than the others'.
-constexpr int kTileStart = 120;
+// What paged_kernel takes until its first tile and behind its last, and rows_kernel (a tenth of
+// a microsecond, as all costs).
+constexpr int kTileStart = 120, kRowsStart = 60;
+// Cost of a unit of rows_kernel: its share of an SM's copies for 128 keys, and its beginning and
+// end (more where all warps join its rows).
+template <int D>
+__device__ __forceinline__ long long rows_cost(int keys, int rows) {
+  return (long long)(D == 128 ? 14 : 7) * (keys + 32) + 128 * (rows > kFewRows ? 30 : rows * D > 512 ? 12 : 6);
+}
 // Fewest keys of a part of an entry with few rows, and what parts' keys are multiples of.
 constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
 
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   int* members = row + NG;                          // [NG] how many there are
   int* keys = members + NG;                         // [NG] shared keys
   __shared__ Sums warps[THREADS / 32];
-  __shared__ unsigned long long all_cost;  // of the entries with few rows, a key head
+  __shared__ unsigned long long all_cost, best;  // of the entries with few rows, a key head; see below
   const Shape sh = {2 * p.tile_tokens, p.tile_tokens, p.copy_tokens, p.causal};
   const int cap = p.max_pages << p.page_log2, few = p.few_rows / p.G;
   const bool once = N <= THREADS;
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     want = __ldg(p.prefix_lens + tid);
     last_row = __ldg(p.cu_seqlens + imin(imax(__ldg(p.groups + tid + 1), 0), S));
   }
-  if (tid == 0) all_cost = 0;
+  if (tid == 0) all_cost = 0, best = ~0ull;
   __syncthreads();
   // A sequence's group: the last one that begins at it or in front (-1: none).
   auto group_of = [&](int s) {
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   };
   // Cost of a key head of an entry.
   auto cost_of_entry = [&](const SharedSeq& q) {
-    return q.qn <= few ? cost_of<D>(1, q.kv, kShortCopies) : cost_of_seq<D>(q, sh);
+    return q.qn <= few ? rows_cost<D>(q.kv, q.qn * p.G) : cost_of_seq<D>(q, sh);
   };
   int my_group = -1;  // of the sequence that `mine` is
   if (NG > 0) {
@@ -234,7 +240,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     if (lane == 0 && few_cost > 0) atomicAdd(&all_cost, (unsigned long long)few_cost);
     __syncthreads();
   }
-  const long long rows_cost = (long long)all_cost * p.Hk, all_keys = sum.b * p.Hk;
+  const long long few_cost_all = (long long)all_cost * p.Hk, many_cost_all = sum.a * p.Hk, all_keys = sum.b * p.Hk;
+  // The CTAs that paged_kernel's entries are given to: all that they can be given to, or, with
+  // others beside them, as many as let both kernels end at the same time.
+  const int most = ctas_for<D>(many_cost_all, p.sms);
+  if (few_cost_all > 0 && tid > 0 && tid <= most && tid < p.sms) {
+    const long long tiles = many_cost_all / tid + 128 * kTileStart, rows = few_cost_all / (p.sms - tid) + 128 * kRowsStart;
+    atomicMin(&best, (unsigned long long)(tiles > rows ? tiles : rows) << 8 | tid);
+  }
   const SharedLists at = shared_lists(S, NG, p.sms);
   uint8_t* base = reinterpret_cast<uint8_t*>(p.plan);
   long long* costs = reinterpret_cast<long long*>(base + at.cost);
@@ -269,16 +282,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   }
   if (tid == 0) {
     const int entries = (int)(total.a >> 32);
-    const long long cost = sum.a * p.Hk;
-    costs[entries] = cost;
-    int ctas = ctas_for<D>(cost, p.sms);
-    if (rows_cost > 0 && ctas > 1) {
-      // as many as end when the others do
-      const long long even = (cost + rows_cost) / p.sms - 128 * kTileStart, least = 128 * kTileStart;
-      const long long each = even > least ? even : least;
-      const long long most = (cost + each - 1) / each;
-      ctas = most < ctas ? (int)most : ctas;
-    }
+    costs[entries] = many_cost_all;
+    const int ctas = few_cost_all > 0 && most > 0 ? (int)(best & 255) : most;
     int4* head = reinterpret_cast<int4*>(p.plan);
     head[0] = make_int4(entries, (int)(total.a & 0xffffffff), ctas, 0);
     head[1] = make_int4(row0, row1, 0, 0);

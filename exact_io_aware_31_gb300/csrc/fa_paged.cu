@@ -118,7 +118,7 @@ struct Work {
   const int* cu;
   const int* lens;
   int S, Hk, T, cap;
-  __device__ __forceinline__ explicit Work(const PagedParams& p)
+  __device__ __forceinline__ explicit Work(const PagedParams& p, int = 0)
       : cu(p.cu_seqlens), lens(p.kv_lens), S(p.S), Hk(p.Hk), T(p.T), cap(p.max_pages << p.page_log2) {}
   __device__ __forceinline__ Seq seq(int s, bool& bad) const {
     return make_seq(__ldg(cu + s), __ldg(cu + s + 1), __ldg(lens + s), T, cap, bad);
@@ -134,10 +134,10 @@ template <>
 struct Work<true> {
   const SharedEntry* list;
   int S, Hk;
-  __device__ __forceinline__ explicit Work(const PagedParams& p)
+  __device__ __forceinline__ Work(const PagedParams& p, int entries)
       : list(reinterpret_cast<const SharedEntry*>(reinterpret_cast<const uint8_t*>(p.plan) +
                                                   shared_lists(p.S, p.num_groups, p.sms).list)),
-        S(__ldcg(&p.plan->entries)),
+        S(entries),
         Hk(p.Hk) {}
   __device__ __forceinline__ SharedSeq seq(int s) const {
     const int4 a = __ldcg(&list[s].seq), b = __ldcg(&list[s].how);
@@ -266,17 +266,19 @@ __device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<Seq>* plan
 
 // The same where the entries' costs have been added up before.
 template <int D, int THREADS>
-__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<SharedSeq>* plan) {
-  const Work<true> work(p);
+__device__ void make_plan(const PagedParams& p, const Shape& sh, Plan<SharedSeq>* plan, int entries, int ctas) {
+  const Work<true> work(p, entries);
   const long long* cost = reinterpret_cast<const long long*>(p.plan + 1);
   const long long total = __ldcg(cost + work.S);
-  const int ctas = __ldcg(&p.plan->ctas);
+  long long before0 = 0, behind0 = 0;  // asked for at the same time
+  if ((int)threadIdx.x < work.S) before0 = __ldcg(cost + threadIdx.x), behind0 = __ldcg(cost + threadIdx.x + 1);
   const long long share = ctas > 0 ? div_long(total, ctas) : 0;
   const long long x[2] = {border(total, share, blockIdx.x, ctas), border(total, share, blockIdx.x + 1, ctas)};
   if (threadIdx.x < 2) plan->at[threadIdx.x] = {work.S, 0, 0, 0};  // a border at the end
   __syncthreads();
   for (int s = threadIdx.x; s < work.S; s += THREADS) {
-    const long long before = __ldcg(cost + s), behind = __ldcg(cost + s + 1);
+    const long long before = s == (int)threadIdx.x ? before0 : __ldcg(cost + s);
+    const long long behind = s == (int)threadIdx.x ? behind0 : __ldcg(cost + s + 1);
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       const long long at = e ? x[1] : x[0];
@@ -360,13 +362,6 @@ __global__ void __launch_bounds__(384, 1)
   const float c2 = fabsf(p.c2);
   int* status = p.status;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  // Where keys are shared the launch in front wrote the list of entries, and the one
-  // behind (rows_kernel) may begin once that is there; CTAs without work make room for it.
-  if constexpr (SHARED) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if ((int)blockIdx.x >= __ldcg(&p.plan->ctas)) return;
-  }
   bool start_ok = smem_base_ok(smem_raw, status);
 #ifdef FA_TEST_HOOKS
   if (*reinterpret_cast<volatile int*>(&g_fa_test_paged) == 2) {
@@ -376,7 +371,10 @@ __global__ void __launch_bounds__(384, 1)
 #endif
   if (!start_ok) {  // nothing for the merge kernel, whatever the workspace holds
     if (threadIdx.x < kPagedHdr) p.hdr[(size_t)blockIdx.x * kPagedHdr + threadIdx.x] = 0;
-    if (SHARED && threadIdx.x == 0) p.plan->failed = 1;
+    if constexpr (SHARED) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (threadIdx.x == 0) p.plan->failed = 1;
+    }
     return;
   }
   uint8_t* sm = smem_raw;
@@ -422,6 +420,15 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
+  // Where keys are shared the launch in front wrote the list of entries, and the one
+  // behind (rows_kernel) may begin once that is there; CTAs without work make room for it.
+  int4 head = make_int4(0, 0, 0, 0);
+  if constexpr (SHARED) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    head = __ldcg(reinterpret_cast<const int4*>(p.plan));
+    if ((int)blockIdx.x >= head.z) return;
+  }
   if (warp == 9) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
@@ -435,13 +442,16 @@ __global__ void __launch_bounds__(384, 1)
   // Short chunks: the plan behind the barrier (64 sequences of 8 tokens against up to
   // 1024 keys, d = 64: 47.3 -> 45.4 us).  The other way round with the other forms,
   // whose softmax loops come out slower so (2 x 2048 tokens: 458 -> 463 us).
-  if constexpr (!SHORT) make_plan<D, C::kThreads>(p, sh, plan);
+  if constexpr (SHARED)
+    make_plan<D, C::kThreads>(p, sh, plan, head.x, head.z);
+  else if constexpr (!SHORT)
+    make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_before();
   __syncthreads();
   if constexpr (SHORT) make_plan<D, C::kThreads>(p, sh, plan);
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const Work<SHARED> work(p);
+  const Work<SHARED> work(p, head.x);
   auto form_of = [&](const Segment& g) { return SHORT ? kFourCopies : sh.form(g.ntok); };
   // The roles' walk through the run: `step` goes to the next segment, the first one
   // included.  With short chunks warp 11 walks for all and the others read what it
@@ -1382,7 +1392,10 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess) return e;
+    // (no launch where no entry can have more rows than rows_kernel takes)
+    if (a.p.T * (long long)a.p.G > a.p.few_rows &&
+        (e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess)
+      return e;
     if (a.p.few_rows > 0 && (e = launch_shared_rows(a, stream)) != cudaSuccess) return e;
     return launch_shared_merge(a, stream);
   }

@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
   }
 #endif
   if (!start_ok) {
-    if (threadIdx.x == 0) p.plan->failed = 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) p.plan->failed = 1;
     return;
   }
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBar);  // [stages] K and V are there
@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
     tma_prefetch_map(&tm_v);
   }
   __syncthreads();
+  // The lists are there: the launch in front waited for them before it let this one begin, or,
+  // where there is none between, is the one that makes them.
+  if (p.T * (long long)p.G <= p.few_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == C::kWarps) {
     // ---------------------------------------------------------------- producer --

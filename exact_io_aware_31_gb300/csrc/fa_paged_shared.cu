@@ -31,17 +31,17 @@ namespace {
 
 using namespace paged;
 
-constexpr size_t kGroupBytes = 8 + 6 * 4;  // of the plan's shared memory
+constexpr size_t kGroupBytes = 8 + 7 * 4;  // of the plan's shared memory
 constexpr int kMaxCtas = 178;  // (their parts' places are below 2^13, as a row's mark has room for)
 static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
 // What paged_kernel takes until its first tile and behind its last, and rows_kernel (a tenth of
 // a microsecond, as all costs).
-constexpr int kTileStart = 120, kRowsStart = 60;
+constexpr int kTileStart = 150, kRowsStart = 60;
 // Cost of a unit of rows_kernel: its share of an SM's copies for 128 keys, and its beginning and
 // end (more where all warps join its rows).
 template <int D>
 __device__ __forceinline__ long long rows_cost(int keys, int rows) {
-  return (long long)(D == 128 ? 14 : 7) * (keys + 32) + 128 * (rows > kFewRows ? 30 : rows * D > 512 ? 12 : 6);
+  return (long long)(D == 128 ? 14 : 7) * (keys + 32) + 128 * (rows > kFewRows ? 60 : rows * D > 512 ? 12 : 6);
 }
 // Fewest keys of a part of an entry with few rows, and what parts' keys are multiples of.
 constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
@@ -100,10 +100,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   int* front = start + NG + 1;                      // [NG] keys in front of the new tokens, the fewest
   int* first = front + NG;                          // [NG] first sequence with new tokens
   int* row = first + NG;                            // [NG] its first row
-  int* members = row + NG;                          // [NG] how many there are
+  int* row_end = row + NG;                          // [NG] behind the last one's rows
+  int* members = row_end + NG;                      // [NG] how many there are
   int* keys = members + NG;                         // [NG] shared keys
   __shared__ Sums warps[THREADS / 32];
-  __shared__ unsigned long long all_cost, best;  // of the entries with few rows, a key head; see below
+  __shared__ unsigned long long all_cost, all_units, best;  // of a key head, with few and with many rows; see below
   const Shape sh = {2 * p.tile_tokens, p.tile_tokens, p.copy_tokens, p.causal};
   const int cap = p.max_pages << p.page_log2, few = p.few_rows / p.G;
   const bool once = N <= THREADS;
@@ -115,18 +116,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   Seq mine = {0, 0, 0};
   if (tid >= NG && tid < N) mine = sequence(tid - NG, bad);
   const int row0 = imin(imax(__ldg(p.cu_seqlens), 0), p.T), row1 = imin(imax(__ldg(p.cu_seqlens + S), 0), p.T);
-  int want = 0, last_row = 0;
+  const int want = tid < NG ? __ldg(p.prefix_lens + tid) : 0;
   for (int g = tid; g <= NG && NG > 0; g += THREADS) {
     const int at = __ldg(p.groups + g);
     start[g] = imin(imax(at, 0), S);
     bad = bad || start[g] != at || (g > 0 && at < __ldg(p.groups + g - 1));
-    if (g < NG) front[g] = first[g] = row[g] = 0x7fffffff, members[g] = 0, apart[g] = 0;
+    if (g < NG) front[g] = first[g] = row[g] = 0x7fffffff, row_end[g] = members[g] = 0, apart[g] = 0;
   }
-  if (tid < NG) {
-    want = __ldg(p.prefix_lens + tid);
-    last_row = __ldg(p.cu_seqlens + imin(imax(__ldg(p.groups + tid + 1), 0), S));
-  }
-  if (tid == 0) all_cost = 0, best = ~0ull;
+  if (tid == 0) all_cost = all_units = 0, best = ~0ull;
   __syncthreads();
   // A sequence's group: the last one that begins at it or in front (-1: none).
   auto group_of = [&](int s) {
@@ -148,12 +145,12 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   if (NG > 0) {
     for (int i0 = 0; i0 < N; i0 += THREADS) {
       const int i = i0 + tid, s = i - NG;
-      int g = -1, f = 0x7fffffff, q0 = 0, cost = 0;
+      int g = -1, f = 0x7fffffff, q0 = 0, q1 = 0, cost = 0;
       if (i >= NG && i < N) {
         const Seq q = i0 == 0 ? mine : sequence(s, bad);
         if (q.qn > 0 && (g = group_of(s)) >= 0) {
           f = imax(0, p.causal ? q.kv - q.qn : q.kv);
-          q0 = q.q0;
+          q0 = q.q0, q1 = q.q0 + q.qn;
           const int full = q.qn / sh.ut, rest = q.qn - full * sh.ut;
           cost = full * tile_cost<D>(sh.form(sh.ut)) + (rest > 0 ? tile_cost<D>(sh.form(rest)) : 0);
         }
@@ -164,12 +161,13 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
       if (in == 0) continue;
       const int g0 = __shfl_sync(0xffffffffu, g, __ffs(in) - 1);
       if (__all_sync(0xffffffffu, g < 0 || g == g0)) {
-        const int least = __reduce_min_sync(0xffffffffu, f);
+        const int least = __reduce_min_sync(0xffffffffu, f), end = __reduce_max_sync(0xffffffffu, q1);
         const int sum = __reduce_add_sync(0xffffffffu, cost);
         if (lane == __ffs(in) - 1) {
           atomicMin(&front[g0], least);
           atomicMin(&first[g0], s);
           atomicMin(&row[g0], q0);
+          atomicMax(&row_end[g0], end);
           atomicAdd(&members[g0], __popc(in));
           atomicAdd(&apart[g0], (unsigned long long)sum);
         }
@@ -177,18 +175,18 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
         atomicMin(&front[g], f);
         atomicMin(&first[g], s);
         atomicMin(&row[g], q0);
+        atomicMax(&row_end[g], q1);
         atomicAdd(&members[g], 1);
         atomicAdd(&apart[g], (unsigned long long)cost);
       }
     }
     __syncthreads();
   }
-  // A group's entry: `n` keys of its first sequence, all rows from that one's on.
+  // A group's entry: `n` keys of its first sequence, all rows from that one's to the last one's.
   auto prefix_of = [&](int g, int n) {
     SharedSeq q;
-    const int end = g == tid ? last_row : __ldg(p.cu_seqlens + start[g + 1]);
     q.q0 = row[g];
-    q.qn = imax(0, imin(imax(end, 0), p.T) - q.q0);
+    q.qn = row_end[g] - row[g];
     q.kv = n;
     q.row = first[g];
     q.page0 = 0;
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     if (members[g] < 2) n = 0;
     if (n > 0) {
       const SharedSeq q = prefix_of(g, n);
-      if (q.qn == 0 || cost_of_entry(q) >= (long long)apart[g] * n) n = 0;
+      if (cost_of_entry(q) >= (long long)apart[g] * n) n = 0;
     }
     keys[g] = n;
   }
@@ -235,9 +233,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     const long long cost = q.qn > 0 ? cost_of_entry(q) : 0;
     front_of = scan2<THREADS>(few_rows ? 0 : cost, few_rows ? q.kv : 0, warps, &sum);
     long long few_cost = few_rows ? cost : 0;
+    const unsigned units = __reduce_add_sync(0xffffffffu, few_rows ? 0u : (unsigned)blocks_of(q, sh.ut));
 #pragma unroll
     for (int off = 16; off > 0; off /= 2) few_cost += __shfl_xor_sync(0xffffffffu, few_cost, off);
     if (lane == 0 && few_cost > 0) atomicAdd(&all_cost, (unsigned long long)few_cost);
+    if (lane == 0 && units > 0) atomicAdd(&all_units, (unsigned long long)units);
     __syncthreads();
   }
   const long long few_cost_all = (long long)all_cost * p.Hk, many_cost_all = sum.a * p.Hk, all_keys = sum.b * p.Hk;
@@ -245,7 +245,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   // others beside them, as many as let both kernels end at the same time.
   const int most = ctas_for<D>(many_cost_all, p.sms);
   if (few_cost_all > 0 && tid > 0 && tid <= most && tid < p.sms) {
-    const long long tiles = many_cost_all / tid + 128 * kTileStart, rows = few_cost_all / (p.sms - tid) + 128 * kRowsStart;
+    // (rows_kernel is bound by device memory, of which an SM can use almost twice its share
+    // where it has two CTAs; paged_kernel's tiles take longer beside it)
+    const long long tiles = many_cost_all * 9 / 8 / tid + 128 * kTileStart;
+    const long long mine = (p.few_rows > kFewRows ? few_cost_all : few_cost_all * 3 / 5) / (p.sms - tid);
+    const long long rows = (mine > few_cost_all / p.sms ? mine : few_cost_all / p.sms) + 128 * kRowsStart;
     atomicMin(&best, (unsigned long long)(tiles > rows ? tiles : rows) << 8 | tid);
   }
   const SharedLists at = shared_lists(S, NG, p.sms);
@@ -283,7 +287,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   if (tid == 0) {
     const int entries = (int)(total.a >> 32);
     costs[entries] = many_cost_all;
-    const int ctas = few_cost_all > 0 && most > 0 ? (int)(best & 255) : most;
+    // (a multiple of the units: units of one cost are then cut into the same parts, and no CTA
+    // has the end of one and the beginning of the next, which take it 6 us each)
+    int ctas = few_cost_all > 0 && most > 0 ? (int)(best & 255) : most;
+    const unsigned long long units = all_units * p.Hk;
+    if (units > 0 && units < (unsigned long long)ctas) ctas -= ctas % (int)units;
     int4* head = reinterpret_cast<int4*>(p.plan);
     head[0] = make_int4(entries, (int)(total.a & 0xffffffff), ctas, 0);
     head[1] = make_int4(row0, row1, 0, 0);
@@ -294,38 +302,37 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
 // ------------------------------------------------------------------ the merge --
 // D / 8 lanes a row of the output (a token's query head).  Bound by latency: a row's mark,
 // the end of a unit that was cut, its parts, one after the other; so every warp takes rows
-// of its own, looks at 32 marks at a time, asks for four parts at once, and all rows of a
+// of its own, looks at 32 marks at a time, asks for eight parts at once, and all rows of a
 // step are under way at the same time.  Where rows are so few that the warps outnumber them, the eight of a block share a
 // row's parts (a group's keys, cut into a part a CTA).  Parts are added in a fixed order:
 // those of the sequence's own keys, then those of the shared ones.
 template <int D, int SPLIT>
-__global__ void __launch_bounds__(256, 3) shared_merge_kernel(const PagedParams p) {
-  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kAtOnce = 4;
+__global__ void __launch_bounds__(256, 2) shared_merge_kernel(const PagedParams p) {
+  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kAtOnce = 8;
   __shared__ float4 sum[SPLIT > 1 ? 8 : 1][32][2];
   __shared__ float2 stat[SPLIT > 1 ? 8 : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l8 = lane % kLanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 head0 = __ldcg(reinterpret_cast<const int4*>(p.plan));
   const int4 head1 = __ldcg(reinterpret_cast<const int4*>(p.plan) + 1);
-  const int ctas = head0.z, Hq = p.Hk * p.G;
-  const size_t rows = (size_t)(head1.y - head1.x) * Hq, row0 = (size_t)head1.x * Hq;
-  // (the last one: a CTA gave up, and what the workspace says is not this call's)
-  if (head1.y <= head1.x || head1.z) return;
+  const int Hq = p.Hk * p.G;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   const size_t slots = (size_t)p.sms * (2 * kPagedRows), all = (size_t)p.T * Hq;
   const int few_rows = imax(p.few_rows, kFewRows), places = shared_parts(p.sms) * kPartRows / few_rows;
-  // Rows of a warp (or, split, of a block): the next `chunk`, of which `todo` are not done.
-  const int chunk = SPLIT > 1 || rows <= (size_t)gridDim.x * (8 * kRowsAWarp) ? kRowsAWarp : 32;
-  const size_t first = ((size_t)blockIdx.x * (SPLIT > 1 ? 1 : 8) + (SPLIT > 1 ? 0 : warp)) * chunk;
+  // Rows of a warp (or, split, of a block): the next `chunk`.  With 32 of them the marks say
+  // which ones are not done.
+  const bool many = SPLIT == 1 && all > (size_t)gridDim.x * (8 * kRowsAWarp);
+  const int chunk = many ? 32 : kRowsAWarp;
   const size_t stride = (size_t)gridDim.x * (SPLIT > 1 ? 1 : 8) * chunk;
-  size_t n0 = first;
+  size_t n0 = ((size_t)blockIdx.x * (SPLIT > 1 ? 1 : 8) + (SPLIT > 1 ? 0 : warp)) * chunk;
   unsigned todo = 0;
   bool fresh = true;
   for (;;) {
     if (fresh) {
-      if (n0 >= rows) break;
-      const bool mine = lane < chunk && n0 + lane < rows;
-      todo = __ballot_sync(0xffffffffu, mine && __ldcg(&ml[slots + all + row0 + n0 + lane].y) != kRowDone);
+      if (n0 >= all) break;
+      todo = (1u << (chunk - 1) << 1) - 1;
+      if (many)
+        todo = __ballot_sync(0xffffffffu, n0 + lane < all && __ldcg(&ml[slots + all + n0 + lane].y) != kRowDone);
     }
     // the lane groups' rows: the first ones of those left (a group without one goes along)
     int at_row = -1;
@@ -334,11 +341,17 @@ __global__ void __launch_bounds__(256, 3) shared_merge_kernel(const PagedParams 
       if (lane / kLanes == k) at_row = __ffs(todo) - 1;
       todo &= todo - 1;
     }
-    const bool has = at_row >= 0;
-    const size_t row = row0 + n0 + (has ? at_row : 0);
+    const bool has = at_row >= 0 && n0 + at_row < all;
+    const size_t row = n0 + (has ? at_row : 0);
     fresh = todo == 0;
     if (fresh) n0 += stride;
-    if (!__any_sync(0xffffffffu, has)) continue;
+    const float2 own = __ldcg(ml + slots + all + row), shared = __ldcg(ml + slots + row);
+    // (behind the loads: asked for at the same time as the first of them.  The last one: a CTA
+    // gave up, and what the workspace says is not this call's)
+    const int ctas = head0.z;
+    if (head1.y <= head1.x || head1.z) return;
+    const bool done = !has || row < (size_t)head1.x * Hq || row >= (size_t)head1.y * Hq || own.y == kRowDone;
+    if (SPLIT > 1 ? __syncthreads_and(done) : __all_sync(0xffffffffu, done)) continue;
     // Where the parts are: `count` of a unit cut from CTA c on, of an entry's parts from place
     // c on, or one in the row's own place.  (What is said is cut to what there is room for.)
     enum { kHere, kCut, kPlaces };
@@ -360,29 +373,26 @@ __global__ void __launch_bounds__(256, 3) shared_merge_kernel(const PagedParams 
       }
       return u;
     };
-    const float2 own = __ldcg(ml + slots + all + row), shared = __ldcg(ml + slots + row);
-    const bool done = !has || own.y == kRowDone;
     Parts a = parts_of(own), b = {kHere, 0, 0, 0};
     if (done)
       a = {kHere, 0, 0, 0};
     else if (own.y != kRowCut && own.y != kRowParts)
       b = parts_of(shared);
     // A cut unit's parts: up to the first CTA behind c whose first slot ends its unit.
-    auto find_end = [&](Parts& u) {
-      bool open = u.how == kCut;
-      for (int at = u.c + 1; __any_sync(0xffffffffu, open); at += kLanes) {
-        const int c = at + l8;
-        const bool goes_on = open && c < ctas - 1 && __ldcg(p.hdr + (size_t)c * kPagedHdr + 4) == 1;
-        const unsigned ends = __ballot_sync(0xffffffffu, open && !goes_on) >> (lane / kLanes * kLanes) & ((1u << (kLanes - 1) << 1) - 1);
-        if (open && ends) {
-          u.count = imin(at + __ffs(ends) - 1, imax(ctas, 1) - 1) - u.c + 1;
-          u.count = imax(u.count, 1);
-          open = false;
-        }
-      }
-    };
-    find_end(a);
-    find_end(b);
+    bool open_a = a.how == kCut, open_b = b.how == kCut;
+    for (int k = 1; __any_sync(0xffffffffu, open_a || open_b); k += kLanes) {
+      const int ca = a.c + k + l8, cb = b.c + k + l8;
+      const bool on_a = open_a && ca < ctas - 1 && __ldcg(p.hdr + (size_t)ca * kPagedHdr + 4) == 1;
+      const bool on_b = open_b && cb < ctas - 1 && __ldcg(p.hdr + (size_t)cb * kPagedHdr + 4) == 1;
+      auto end = [&](Parts& u, bool& open, bool on) {
+        const unsigned ends = __ballot_sync(0xffffffffu, open && !on) >> (lane / kLanes * kLanes) & ((1u << (kLanes - 1) << 1) - 1);
+        if (!open || !ends) return;
+        u.count = imax(imin(u.c + k + __ffs(ends) - 1, imax(ctas, 1) - 1) - u.c + 1, 1);
+        open = false;
+      };
+      end(a, open_a, on_a);
+      end(b, open_b, on_b);
+    }
     const int count = a.count + b.count;
     auto place = [&](int i) {
       const bool of_b = i >= a.count;
@@ -456,7 +466,7 @@ cudaError_t launch_merge_t(const PagedLaunch& a, cudaStream_t stream) {
   if (a.grid > kMaxCtas) return cudaErrorInvalidConfiguration;
   const size_t rows = (size_t)a.p.T * a.p.Hk * a.p.G;
   constexpr int kRowsAWarp = 32 / (D / 8);
-  const bool few = rows <= (size_t)a.grid * 3 * kRowsAWarp;  // (as many blocks as there is room for)
+  const bool few = rows <= (size_t)a.grid * 2 * kRowsAWarp;  // (as many blocks as there is room for)
   const size_t a_block = few ? kRowsAWarp : kRowsAWarp * 8;
   const size_t blocks = (rows + a_block - 1) / a_block, most = (size_t)a.grid * 8;
   cudaLaunchAttribute attr[1];

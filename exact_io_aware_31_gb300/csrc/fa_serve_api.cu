@@ -483,6 +483,8 @@ int fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, 
          make_rows_map(&a.tm_vr, v_pages, num_pages, Hk, page_size, d, sp[1], sh[1], sr[1], rows_keys(d))))
       return FA_ERR_CUDA;
   }
+  const bool tiles = !groups || (long long)T * G > p.few_rows;  // any unit of paged_kernel
+  if (!tiles) return cuda_status(launch_paged(a, stream));
   if (make_ragged_map(&a.tm_q, q, T, Hk, G, d, p.tile_tokens, q_stride_t, q_stride_h) ||
       make_ragged_map(&a.tm_q4, q, T, Hk, G, d, p.copy_tokens > 0 ? p.copy_tokens : 1, q_stride_t, q_stride_h) ||
       make_pool_map(&a.tm_k, k_pages, num_pages, Hk, page_size, d, sp[0], sh[0], sr[0]) ||

@@ -25,11 +25,10 @@ struct SharedEntry {
 };
 // Of an entry with few rows, or a part of its keys.
 struct SharedPiece {
-  int4 seq;   // as SharedEntry
-  int4 how;   // first entry of the page table, kind, keys [z, w) of the entry
-  int4 part;  // place of its partial rows (-1: not split), parts of the entry, which one
+  int4 seq;   // first token and kind, keys, row of the page table, first entry there
+  int4 part;  // keys [x, y) of the entry, place of its partial rows (-1: not split), parts, which one, tokens
 };
-static_assert(sizeof(SharedPlan) == 32 && sizeof(SharedEntry) == 32 && sizeof(SharedPiece) == 48, "16-byte reads");
+static_assert(sizeof(SharedPlan) == 32 && sizeof(SharedEntry) == 32 && sizeof(SharedPiece) == 32, "16-byte reads");
 
 // Partial rows of rows_kernel's entries in parts: of kMaxParts (16 rows) or half as many (32
 // rows) an SM.  An entry of n keys has at most 2 n / (L + 1) parts of L keys, if it has two;

@@ -184,9 +184,6 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
     // A unit's number is asked for two units ahead, its piece one, its first pages while the
     // stages of the one in front are copied.  (No further: what a CTA has taken no other one
     // does.)
-    struct Piece {
-      int4 seq, how, part;
-    };
     auto split = [&](unsigned i, int& hk) {  // i = piece * Hk + hk
       unsigned x = __umulhi(i, p.hk_inverse), rest = i - x * Hk;
       while (rest >= Hk) rest -= Hk, ++x;  // (once or twice at most: the inverse is rounded down)
@@ -194,43 +191,44 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       return x;
     };
     auto fetch = [&](unsigned i, int& hk) {
-      Piece e = {};
+      SharedPiece e = {};
       if (i < total) {
         const SharedPiece* from = list + split(i, hk);
-        e.seq = __ldcg(&from->seq), e.how = __ldcg(&from->how), e.part = __ldcg(&from->part);
+        e.seq = __ldcg(&from->seq), e.part = __ldcg(&from->part);
       }
       return e;
     };
-    auto page_at = [&](const Piece& e, int i) {  // this lane's of stage i
-      const int key = e.how.z + i * C::kKeys + my_box * box_rows;
-      return lane < copies && key < e.how.w
-                 ? __ldg(p.page_table + (size_t)e.seq.w * p.max_pages + e.how.x + (key >> p.page_log2))
+    auto page_at = [&](const SharedPiece& e, int i) {  // this lane's of stage i
+      const int key = e.part.x + i * C::kKeys + my_box * box_rows;
+      return lane < copies && key < e.part.y
+                 ? __ldg(p.page_table + (size_t)e.seq.z * p.max_pages + e.seq.w + (key >> p.page_log2))
                  : 0;
     };
     // (All from the counter: CTAs that wait for paged_kernel's SMs find nothing left.)
     auto take = [&] { return lane == 0 ? atomicAdd(&p.plan->next, 1u) : 0u; };
     unsigned at = __shfl_sync(0xffffffffu, take(), 0), after = take();
     int hk = 0, hk1 = 0;
-    Piece e = fetch(at, hk);
+    SharedPiece e = fetch(at, hk);
     int page = page_at(e, 0), page1 = 0;
     unsigned next = __shfl_sync(0xffffffffu, after, 0);
     for (;; ++count) {
       const int slot = count % C::kItems;
       const bool end = at >= total;
       if (!(ok = wait_short(&item_empty[slot], ((count / C::kItems) & 1) ^ 1, status))) break;
-      const int k0 = e.how.z, k1 = e.how.w;
+      const int k0 = e.part.x, k1 = e.part.y;
       const int stages = end ? 0 : (k1 - k0 + C::kKeys - 1) / C::kKeys;
       if (lane == 0) {
         int4* to = reinterpret_cast<int4*>(sm + C::kOffItem + slot * 64);
-        to[0] = make_int4(e.seq.x, e.seq.y, e.seq.z, e.how.y);
-        to[1] = make_int4(k0, stages, hk, e.part.x);
-        to[2] = make_int4(e.part.y, e.part.z, (int)it, end);
+        const unsigned said = e.part.w;
+        to[0] = make_int4((int)((unsigned)e.seq.x >> 2), (int)(said & 31) + 1, e.seq.y, e.seq.x & 3);
+        to[1] = make_int4(k0, stages, hk, e.part.z);
+        to[2] = make_int4((int)(said >> 18), (int)(said >> 5 & 8191), (int)it, end);
         mbar_arrive(&item_full[slot]);
       }
       __syncwarp();
       if (end) break;
       after = take();
-      const Piece e1 = fetch(next, hk1);
+      const SharedPiece e1 = fetch(next, hk1);
       for (int i = 0; i < stages; ++i, ++it) {
         const int key = k0 + i * C::kKeys, st = it % C::kStages;
         const int live = imin(boxes, (k1 - key + box_rows - 1) / box_rows);  // boxes with keys

@@ -38,52 +38,82 @@ static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
 // a microsecond, as all costs).
 constexpr int kTileStart = 150, kRowsStart = 60;
 // Cost of a unit of rows_kernel: its share of an SM's copies for 128 keys, and its beginning and
-// end (more where all warps join its rows).
+// end (more where all warps join its rows).  Like all that only decides how work is divided, in
+// fp32: the block's time is that of its arithmetic, one step after the other.
 template <int D>
-__device__ __forceinline__ long long rows_cost(int keys, int rows) {
-  return (long long)(D == 128 ? 14 : 7) * (keys + 32) + 128 * (rows > kFewRows ? 60 : rows * D > 512 ? 12 : 6);
+__device__ __forceinline__ float rows_cost(int keys, int rows) {
+  return (D == 128 ? 14.f : 7.f) * (keys + 32) + 128.f * (rows > kFewRows ? 60 : rows * D > 512 ? 12 : 6);
 }
-// Fewest keys of a part of an entry with few rows, and what parts' keys are multiples of.
+// Parts of an SM and fewest keys of one (an entry with few rows), and what their keys are multiples of.
 constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
-
-// ------------------------------------------------------------------ the lists --
-// Sums over the block of two values a thread: those in front of it; *total grows by all.
-struct Sums {
-  long long a, b;
-};
-
-template <int THREADS>
-__device__ __forceinline__ Sums scan2(long long a, long long b, Sums* warps, Sums* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
-  Sums s = {a, b};
-#pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const long long x = __shfl_up_sync(0xffffffffu, s.a, off), y = __shfl_up_sync(0xffffffffu, s.b, off);
-    if (lane >= off) s.a += x, s.b += y;
-  }
-  __syncthreads();  // the previous use of `warps` has been read
-  if (lane == 31) warps[w] = s;
-  __syncthreads();
-  s.a += total->a - a;
-  s.b += total->b - b;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) {
-    const Sums x = warps[i];
-    if (i < w) s.a += x.a, s.b += x.b;
-    total->a += x.a, total->b += x.b;
-  }
-  return s;
-}
 
 // Keys of the parts of an entry with few rows that has `before` of all of those entries'
 // `keys` (times their heads) in front of it: an eighth of a CTA's share, and half of that for
 // the last fifth of the keys, which end when there is nothing else left to take.  With two row
 // tiles parts are twice as long, as there are half as many CTAs and places.
-__device__ __forceinline__ int part_keys(long long before, long long keys, int few_rows, int sms) {
+__device__ __forceinline__ int part_keys(float before, float keys, int few_rows, int sms) {
   const int tiles = few_rows / kFewRows;
-  long long n = keys / (kPartsASm * sms) >> (5 * before > 4 * keys ? 1 : 0);
-  n = (n * tiles + kPartStep - 1) / kPartStep * kPartStep;
-  return n < kLeastPart * tiles ? kLeastPart * tiles : n > 0x3fffff00 ? 0x3fffff00 : (int)n;
+  const float share = keys / (kPartsASm * sms) * (5.f * before > 4.f * keys ? 0.5f : 1.f) * tiles;
+  const int n = (int)fminf(share, 1e9f) / kPartStep * kPartStep + kPartStep;
+  return imax(n, kLeastPart * tiles);
+}
+
+// ------------------------------------------------------------------ the lists --
+// Sums of a thread's values over those in front of it; *total grows by all.
+struct Sums {
+  long long cost;  // of the entries with many rows
+  float keys;      // of those with few
+  float few;       // their cost
+};
+struct Counts {
+  int entries, pieces, places, unused;
+};
+__device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
+  return {x.cost + y.cost, x.keys + y.keys, x.few + y.few};
+}
+__device__ __forceinline__ Counts operator+(const Counts& x, const Counts& y) {
+  return {x.entries + y.entries, x.pieces + y.pieces, x.places + y.places, 0};
+}
+__device__ __forceinline__ Sums shfl_up(const Sums& x, int off) {
+  return {__shfl_up_sync(0xffffffffu, x.cost, off), __shfl_up_sync(0xffffffffu, x.keys, off),
+          __shfl_up_sync(0xffffffffu, x.few, off)};
+}
+__device__ __forceinline__ Counts shfl_up(const Counts& x, int off) {
+  return {__shfl_up_sync(0xffffffffu, x.entries, off), __shfl_up_sync(0xffffffffu, x.pieces, off),
+          __shfl_up_sync(0xffffffffu, x.places, off), 0};
+}
+
+template <int THREADS, class T>
+__device__ __forceinline__ T scan(const T& v, T* warps, T* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
+  T s = v;
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const T x = shfl_up(s, off);
+    if (lane >= off) s = s + x;
+  }
+  T before = shfl_up(s, 1);
+  if (lane == 0) before = T{};
+  __syncthreads();  // the previous use of `warps` has been read
+  if (lane == 31) warps[w] = s;
+  __syncthreads();
+  T front = *total;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const T x = warps[i];
+    if (i == w) before = front + before;
+    front = front + x;
+  }
+  *total = front;
+  return before;
+}
+
+// A piece in 32 bytes: tokens lie below 2^30 and are at most 32, parts are fewer than 2^13.
+__device__ __forceinline__ SharedPiece pack_piece(const SharedSeq& q, int k0, int k1, int slot, int parts, int which) {
+  SharedPiece e;
+  e.seq = make_int4((int)((unsigned)q.q0 << 2 | q.kind), q.kv, q.row, q.page0);
+  e.part = make_int4(k0, k1, slot, parts << 18 | which << 5 | (q.qn - 1));
+  return e;
 }
 
 // One block.  Cuts each group's shared keys to whole pages that all of its sequences with
@@ -104,7 +134,9 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   int* members = row_end + NG;                      // [NG] how many there are
   int* keys = members + NG;                         // [NG] shared keys
   __shared__ Sums warps[THREADS / 32];
-  __shared__ unsigned long long all_cost, all_units, best;  // of a key head, with few and with many rows; see below
+  __shared__ Counts warp_counts[THREADS / 32];
+  __shared__ unsigned all_units;        // of a key head, with many rows
+  __shared__ unsigned long long best;   // see below
   const Shape sh = {2 * p.tile_tokens, p.tile_tokens, p.copy_tokens, p.causal};
   const int cap = p.max_pages << p.page_log2, few = p.few_rows / p.G;
   const bool once = N <= THREADS;
@@ -123,7 +155,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     bad = bad || start[g] != at || (g > 0 && at < __ldg(p.groups + g - 1));
     if (g < NG) front[g] = first[g] = row[g] = 0x7fffffff, row_end[g] = members[g] = 0, apart[g] = 0;
   }
-  if (tid == 0) all_cost = all_units = 0, best = ~0ull;
+  if (tid == 0) all_units = 0, best = ~0ull;
   __syncthreads();
   // A sequence's group: the last one that begins at it or in front (-1: none).
   auto group_of = [&](int s) {
@@ -136,10 +168,6 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
         hi = mid;
     }
     return lo - 1 < NG ? lo - 1 : -1;
-  };
-  // Cost of a key head of an entry.
-  auto cost_of_entry = [&](const SharedSeq& q) {
-    return q.qn <= few ? rows_cost<D>(q.kv, q.qn * p.G) : cost_of_seq<D>(q, sh);
   };
   int my_group = -1;  // of the sequence that `mine` is
   if (NG > 0) {
@@ -200,7 +228,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     if (members[g] < 2) n = 0;
     if (n > 0) {
       const SharedSeq q = prefix_of(g, n);
-      if (cost_of_entry(q) >= (long long)apart[g] * n) n = 0;
+      const float cost = q.qn <= few ? rows_cost<D>(n, q.qn * p.G) : (float)cost_of_seq<D>(q, sh);
+      if (cost >= (float)apart[g] * n) n = 0;
     }
     keys[g] = n;
   }
@@ -224,76 +253,71 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     }
     return q;
   };
-  // Costs and keys in front of each entry, of those with many and with few rows.
+  // Costs and keys in front of each entry.
   SharedSeq q;
-  Sums front_of = {0, 0}, sum = {0, 0};
+  Sums front_of = {0, 0.f, 0.f}, sum = {0, 0.f, 0.f};
+  auto values = [&] {
+    const bool few_rows = q.qn > 0 && q.qn <= few;
+    const Sums v = {q.qn > few ? cost_of_seq<D>(q, sh) : 0, few_rows ? (float)q.kv : 0.f,
+                    few_rows ? rows_cost<D>(q.kv, q.qn * p.G) : 0.f};
+    return v;
+  };
   for (int i0 = 0; i0 < N; i0 += THREADS) {
     q = entry(i0 + tid);
-    const bool few_rows = q.qn > 0 && q.qn <= few;
-    const long long cost = q.qn > 0 ? cost_of_entry(q) : 0;
-    front_of = scan2<THREADS>(few_rows ? 0 : cost, few_rows ? q.kv : 0, warps, &sum);
-    long long few_cost = few_rows ? cost : 0;
-    const unsigned units = __reduce_add_sync(0xffffffffu, few_rows ? 0u : (unsigned)blocks_of(q, sh.ut));
-#pragma unroll
-    for (int off = 16; off > 0; off /= 2) few_cost += __shfl_xor_sync(0xffffffffu, few_cost, off);
-    if (lane == 0 && few_cost > 0) atomicAdd(&all_cost, (unsigned long long)few_cost);
-    if (lane == 0 && units > 0) atomicAdd(&all_units, (unsigned long long)units);
-    __syncthreads();
+    const unsigned units = __reduce_add_sync(0xffffffffu, q.qn > few ? (unsigned)blocks_of(q, sh.ut) : 0u);
+    if (lane == 0 && units > 0) atomicAdd(&all_units, units);
+    front_of = scan<THREADS>(values(), warps, &sum);
   }
-  const long long few_cost_all = (long long)all_cost * p.Hk, many_cost_all = sum.a * p.Hk, all_keys = sum.b * p.Hk;
+  const float few_all = sum.few * p.Hk, all_keys = sum.keys * p.Hk;
+  const long long many_all = sum.cost * p.Hk;
   // The CTAs that paged_kernel's entries are given to: all that they can be given to, or, with
   // others beside them, as many as let both kernels end at the same time.
-  const int most = ctas_for<D>(many_cost_all, p.sms);
-  if (few_cost_all > 0 && tid > 0 && tid <= most && tid < p.sms) {
+  const int most = ctas_for<D>(many_all, p.sms);
+  if (few_all > 0.f && tid > 0 && tid <= most && tid < p.sms) {
     // (rows_kernel is bound by device memory, of which an SM can use almost twice its share
     // where it has two CTAs; paged_kernel's tiles take longer beside it)
-    const long long tiles = many_cost_all * 9 / 8 / tid + 128 * kTileStart;
-    const long long mine = (p.few_rows > kFewRows ? few_cost_all : few_cost_all * 3 / 5) / (p.sms - tid);
-    const long long rows = (mine > few_cost_all / p.sms ? mine : few_cost_all / p.sms) + 128 * kRowsStart;
-    atomicMin(&best, (unsigned long long)(tiles > rows ? tiles : rows) << 8 | tid);
+    const float tiles = 1.4f * many_all / tid + 128 * kTileStart;
+    const float mine = few_all * (p.few_rows > kFewRows ? 1.f : 0.6f) / (p.sms - tid);
+    const float rows = fmaxf(mine, few_all / p.sms) + 128 * kRowsStart;
+    atomicMin(&best, (unsigned long long)__float_as_uint(fmaxf(tiles, rows)) << 8 | tid);  // (positive: in order as bits)
   }
   const SharedLists at = shared_lists(S, NG, p.sms);
   uint8_t* base = reinterpret_cast<uint8_t*>(p.plan);
   long long* costs = reinterpret_cast<long long*>(base + at.cost);
   SharedEntry* list = reinterpret_cast<SharedEntry*>(base + at.list);
   SharedPiece* pieces = reinterpret_cast<SharedPiece*>(base + at.pieces);
-  Sums again = {0, 0}, total = {0, 0};  // total.a: entries << 32 | pieces, total.b: places
+  Sums again = {0, 0.f, 0.f};
+  Counts total = {0, 0, 0, 0};
   for (int i0 = 0; i0 < N; i0 += THREADS) {
     if (!once) {
       q = entry(i0 + tid);
-      const bool few_rows = q.qn > 0 && q.qn <= few;
-      front_of = scan2<THREADS>(q.qn > 0 && !few_rows ? cost_of_entry(q) : 0, few_rows ? q.kv : 0, warps, &again);
+      front_of = scan<THREADS>(values(), warps, &again);
     }
     const bool few_rows = q.qn > 0 && q.qn <= few, many_rows = q.qn > few;
     int part = 1, parts = 0;
     if (few_rows) {
-      part = part_keys(front_of.b * p.Hk, all_keys, p.few_rows, p.sms);
+      part = part_keys(front_of.keys * p.Hk, all_keys, p.few_rows, p.sms);
       parts = imax(1, (q.kv + part - 1) / part);
     }
-    const Sums before = scan2<THREADS>((long long)many_rows << 32 | parts, parts > 1 ? parts : 0, warps, &total);
+    const Counts before = scan<THREADS>(Counts{many_rows, parts, parts > 1 ? parts : 0, 0}, warp_counts, &total);
     if (many_rows) {
-      const int e = (int)(before.a >> 32);
-      costs[e] = front_of.a * p.Hk;
-      list[e].seq = make_int4(q.q0, q.qn, q.kv, q.row);
-      list[e].how = make_int4(q.page0, q.kind, 0, 0);
+      costs[before.entries] = front_of.cost * p.Hk;
+      list[before.entries].seq = make_int4(q.q0, q.qn, q.kv, q.row);
+      list[before.entries].how = make_int4(q.page0, q.kind, 0, 0);
     }
-    for (int k = 0; k < parts; ++k) {
-      SharedPiece& e = pieces[(int)(before.a & 0xffffffff) + k];
-      e.seq = make_int4(q.q0, q.qn, q.kv, q.row);
-      e.how = make_int4(q.page0, q.kind, k * part, k + 1 < parts ? (k + 1) * part : q.kv);
-      e.part = make_int4(parts > 1 ? ((int)before.b + k) * p.Hk : -1, parts, k, 0);
-    }
+    for (int k = 0; k < parts; ++k)
+      pieces[before.pieces + k] = pack_piece(q, k * part, k + 1 < parts ? (k + 1) * part : q.kv,
+                                             parts > 1 ? (before.places + k) * p.Hk : -1, parts, k);
   }
   if (tid == 0) {
-    const int entries = (int)(total.a >> 32);
-    costs[entries] = many_cost_all;
+    costs[total.entries] = many_all;
     // (a multiple of the units: units of one cost are then cut into the same parts, and no CTA
     // has the end of one and the beginning of the next, which take it 6 us each)
-    int ctas = few_cost_all > 0 && most > 0 ? (int)(best & 255) : most;
-    const unsigned long long units = all_units * p.Hk;
+    int ctas = few_all > 0.f && most > 0 ? (int)(best & 255) : most;
+    const unsigned long long units = (unsigned long long)all_units * p.Hk;
     if (units > 0 && units < (unsigned long long)ctas) ctas -= ctas % (int)units;
     int4* head = reinterpret_cast<int4*>(p.plan);
-    head[0] = make_int4(entries, (int)(total.a & 0xffffffff), ctas, 0);
+    head[0] = make_int4(total.entries, total.pieces, ctas, 0);
     head[1] = make_int4(row0, row1, 0, 0);
   }
   if (bad) record_index(p.status);
@@ -302,13 +326,15 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
 // ------------------------------------------------------------------ the merge --
 // D / 8 lanes a row of the output (a token's query head).  Bound by latency: a row's mark,
 // the end of a unit that was cut, its parts, one after the other; so every warp takes rows
-// of its own, looks at 32 marks at a time, asks for eight parts at once, and all rows of a
-// step are under way at the same time.  Where rows are so few that the warps outnumber them, the eight of a block share a
+// of its own, asks for eight parts at once, and all rows of a step are under way at the same
+// time.  Where rows are many (MANY) most are done and the others have few parts: a warp looks at
+// 32 marks at a time, and there are twice as many warps.  Where rows are so few that the warps outnumber them, the eight of a block share a
 // row's parts (a group's keys, cut into a part a CTA).  Parts are added in a fixed order:
 // those of the sequence's own keys, then those of the shared ones.
-template <int D, int SPLIT>
-__global__ void __launch_bounds__(256, 2) shared_merge_kernel(const PagedParams p) {
-  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kAtOnce = 8;
+template <int D, int SPLIT, bool MANY>
+__global__ void __launch_bounds__(256, MANY ? 4 : 2) shared_merge_kernel(const PagedParams p) {
+  constexpr int kLanes = D / 8, kRowsAWarp = 32 / kLanes, kAtOnce = MANY ? 2 : 8;
+  static_assert(SPLIT == 1 || !MANY, "no such form");
   __shared__ float4 sum[SPLIT > 1 ? 8 : 1][32][2];
   __shared__ float2 stat[SPLIT > 1 ? 8 : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, l8 = lane % kLanes;
@@ -319,10 +345,8 @@ __global__ void __launch_bounds__(256, 2) shared_merge_kernel(const PagedParams 
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   const size_t slots = (size_t)p.sms * (2 * kPagedRows), all = (size_t)p.T * Hq;
   const int few_rows = imax(p.few_rows, kFewRows), places = shared_parts(p.sms) * kPartRows / few_rows;
-  // Rows of a warp (or, split, of a block): the next `chunk`.  With 32 of them the marks say
-  // which ones are not done.
-  const bool many = SPLIT == 1 && all > (size_t)gridDim.x * (8 * kRowsAWarp);
-  const int chunk = many ? 32 : kRowsAWarp;
+  // Rows of a warp (or, split, of a block): the next `chunk`.
+  constexpr int chunk = MANY ? 32 : kRowsAWarp;
   const size_t stride = (size_t)gridDim.x * (SPLIT > 1 ? 1 : 8) * chunk;
   size_t n0 = ((size_t)blockIdx.x * (SPLIT > 1 ? 1 : 8) + (SPLIT > 1 ? 0 : warp)) * chunk;
   unsigned todo = 0;
@@ -331,7 +355,7 @@ __global__ void __launch_bounds__(256, 2) shared_merge_kernel(const PagedParams 
     if (fresh) {
       if (n0 >= all) break;
       todo = (1u << (chunk - 1) << 1) - 1;
-      if (many)
+      if (MANY)
         todo = __ballot_sync(0xffffffffu, n0 + lane < all && __ldcg(&ml[slots + all + n0 + lane].y) != kRowDone);
     }
     // the lane groups' rows: the first ones of those left (a group without one goes along)
@@ -466,9 +490,10 @@ cudaError_t launch_merge_t(const PagedLaunch& a, cudaStream_t stream) {
   if (a.grid > kMaxCtas) return cudaErrorInvalidConfiguration;
   const size_t rows = (size_t)a.p.T * a.p.Hk * a.p.G;
   constexpr int kRowsAWarp = 32 / (D / 8);
-  const bool few = rows <= (size_t)a.grid * 2 * kRowsAWarp;  // (as many blocks as there is room for)
-  const size_t a_block = few ? kRowsAWarp : kRowsAWarp * 8;
-  const size_t blocks = (rows + a_block - 1) / a_block, most = (size_t)a.grid * 8;
+  const bool few = rows <= (size_t)a.grid * 2 * kRowsAWarp;        // (as many blocks as there is room for)
+  const bool many = rows > (size_t)a.grid * 2 * 8 * kRowsAWarp * 4;  // (four times the rows that there is room for)
+  const size_t a_block = few ? kRowsAWarp : many ? 32 * 8 : kRowsAWarp * 8;
+  const size_t blocks = (rows + a_block - 1) / a_block, most = (size_t)a.grid * 32;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -478,7 +503,10 @@ cudaError_t launch_merge_t(const PagedLaunch& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few ? shared_merge_kernel<D, 8> : shared_merge_kernel<D, 1>, a.p);
+  return cudaLaunchKernelEx(&cfg, few    ? shared_merge_kernel<D, 8, false>
+                                  : many ? shared_merge_kernel<D, 1, true>
+                                         : shared_merge_kernel<D, 1, false>,
+                            a.p);
 }
 
 template <int D, int THREADS>

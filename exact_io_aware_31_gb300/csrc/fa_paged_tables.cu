@@ -175,31 +175,42 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
       const int n = seq.cu[s + 1] - seq.cu[s], x0 = ((int)i - seq.piece[s]) * kPiece;
       const int held = (int)((seq.old[s] + (1ll << lg) - 1) >> lg);
       const int used = (int)((seq.old[s] + (long long)n + (1ll << lg) - 1) >> lg);
+      int page[kPiece / 32];  // all asked for before the first is written
+#pragma unroll
+      for (int k = 0; k < kPiece / 32; ++k) {
+        const int x = x0 + 32 * k + lane;
+        page[k] = x < used ? page_of(s, r, x) : 0;
+      }
 #pragma unroll
       for (int k = 0; k < kPiece / 32; ++k) {
         const int x = x0 + 32 * k + lane;
         if (x >= used) continue;
-        const int page = page_of(s, r, x);
-        p.page_table[(size_t)s * p.max_pages + x] = page;
-        if (x >= held) p.request_table[(size_t)r * p.max_pages + x] = page;
+        p.page_table[(size_t)s * p.max_pages + x] = page[k];
+        if (x >= held) p.request_table[(size_t)r * p.max_pages + x] = page[k];
       }
     } else {
+      int pos[kTokens / 32];
+      long long slot[kTokens / 32];
+#pragma unroll
+      for (int k = 0; k < kTokens / 32; ++k) {
+        const long long t = (i - pieces) * kTokens + 32 * k + lane;
+        pos[k] = 0;
+        slot[k] = -1;
+        if (t < end) {
+          const int s = find(seq.cu, S, (int)t), r = seq.request[s];
+          pos[k] = -1;
+          if (r >= 0) {
+            pos[k] = seq.old[s] + ((int)t - seq.cu[s]);
+            slot[k] = ((long long)page_of(s, r, pos[k] >> lg) << lg) + (pos[k] & ((1 << lg) - 1));
+          }
+        }
+      }
 #pragma unroll
       for (int k = 0; k < kTokens / 32; ++k) {
         const long long t = (i - pieces) * kTokens + 32 * k + lane;
         if (t >= T) continue;
-        int pos = 0;
-        long long slot = -1;
-        if (t < end) {
-          const int s = find(seq.cu, S, (int)t), r = seq.request[s];
-          pos = -1;
-          if (r >= 0) {
-            pos = seq.old[s] + ((int)t - seq.cu[s]);
-            slot = ((long long)page_of(s, r, pos >> lg) << lg) + (pos & ((1 << lg) - 1));
-          }
-        }
-        if (p.positions) p.positions[t] = pos;
-        if (p.slots) p.slots[t] = slot;
+        if (p.positions) p.positions[t] = pos[k];
+        if (p.slots) p.slots[t] = slot[k];
       }
     }
   }
@@ -267,13 +278,18 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const TablesParams
   for (int i = blockIdx.x * kWarps + tid / 32; i < seq.piece[S]; i += gridDim.x * kWarps) {
     const int s = find(seq.piece, S, i), r = seq.request[s], x0 = (i - seq.piece[s]) * kPiece;
     const int n = (s + 1 < S ? seq.before[s + 1] : total) - seq.before[s];
+    int page[kPiece / 32];  // all asked for before the first is written
+#pragma unroll
+    for (int k = 0; k < kPiece / 32; ++k) {
+      const int x = x0 + 32 * k + lane;
+      page[k] = x < n ? __ldg(p.request_table + (size_t)r * p.max_pages + seq.cu[s] + x) : 0;
+    }
 #pragma unroll
     for (int k = 0; k < kPiece / 32; ++k) {
       const int x = x0 + 32 * k + lane;
       if (x >= n) continue;
-      const int page = __ldg(p.request_table + (size_t)r * p.max_pages + seq.cu[s] + x);
-      bad = bad || page < 0 || page >= p.num_pages;
-      stack[count + total - 1 - (seq.before[s] + x)] = page;
+      bad = bad || page[k] < 0 || page[k] >= p.num_pages;
+      stack[count + total - 1 - (seq.before[s] + x)] = page[k];
     }
   }
   if (bad) record_index(p.status);

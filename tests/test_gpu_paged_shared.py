@@ -39,6 +39,9 @@ SHAPES = {
     "long chunks": ([(300, [(260, 260), (130, 140)])], 2, 1),
     "heads of one key head": ([(2000, [(1, 4)] * 7)], 64, 1),
     "tile a token": ([(600, [(1, 4)] * 3)], 128, 1),
+    "16 rows": ([(1300, [(1, 200 + 90 * i) for i in range(7)]), (0, [(1, 1), (1, 700)])], 32, 2),
+    "20 heads a key head": ([(800, [(1, 500), (1, 31), (1, 33)])], 20, 1),
+    "32 heads a key head": ([(600, [(1, 450), (1, 7)] * 3)], 64, 2),
     "long": ([(9000, [(1, 20)] * 5)], 2, 1),                                                # cut into many parts
     "long, two tiles": ([(12000, [(1, 20 + i) for i in range(70)])], 4, 1),
 }
@@ -86,6 +89,28 @@ def test_against_the_oracle(shape, form):
     o, lse = call(x, scale=0.11, causal=causal)
     assert status() == fa.FA_OK
     check(o, lse, ref)
+
+
+@pytest.mark.parametrize("hint", [1, 2, 5, 10 ** 6])
+@pytest.mark.parametrize("shape", ["groups", "odd group", "16 rows", "empty", "loners"])
+def test_hints(shape, hint):
+    """The hint moves entries from one kernel to the other; all give the same attention."""
+    x = batch(*SHAPES[shape], 128, 32, False)
+    o, lse = call(x, scale=0.11, max_q=hint)
+    assert status() == fa.FA_OK
+    check(o, lse, reference(*x[:5], 0.11, True))
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(32, 8, 128), (16, 16, 64), (16, 1, 128), (24, 1, 64)])
+def test_more_units_than_ctas(Hq, Hk, d):
+    """Every CTA takes several units, of one stage to a dozen, from the counter; the longest entries come in parts."""
+    lens = [1 + 37 * i % 401 for i in range(180)]
+    x = batch([(256, [(1, n) for n in lens[:90]]), (0, [(1, n) for n in lens[90:]] + [(1, 5000)])], Hq, Hk, d, 16, True)
+    want = call(x, scale=0.2, max_q=1)
+    assert status() == fa.FA_OK
+    check(*want, reference(*x[:5], 0.2, True))
+    for _ in range(3):                     # whichever CTA takes which unit
+        assert all(torch.equal(a, b) for a, b in zip(call(x, scale=0.2, max_q=1), want))
 
 
 @pytest.mark.parametrize("scale", [-0.1, 0.0])

@@ -23,6 +23,7 @@ Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`d
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -467,6 +468,12 @@ def _room_for(size, device, d):
     return need
 
 
+@functools.lru_cache(maxsize=4096)
+def _shared_room(T, S, groups, Hq, d, device):
+    """Workspace bytes of :func:`paged_forward_shared` on the current device, asked for once for each batch shape."""
+    return load_library().fa_fwd_paged_shared_workspace_size(T, S, groups, Hq, d)
+
+
 def _room(workspace, device):
     """Address and bytes of a workspace (None: no room)."""
     if workspace is None:
@@ -780,8 +787,7 @@ def paged_forward_shared(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, g
     else:
         _flat(lse, "lse", (T, Hq), torch.float32, dev)
     if workspace is None:
-        need = load_library().fa_fwd_paged_shared_workspace_size(T, S, n, Hq, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(_shared_room(T, S, n, Hq, d, dev), dtype=torch.uint8, device=q.device)
     ws, wbytes = _room(workspace, dev)
     st = load_library().fa_fwd_paged_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), *meta, *shared, T, S, n, Hq, Hk, d, num_pages, page_size,

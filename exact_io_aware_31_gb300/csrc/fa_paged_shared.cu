@@ -512,9 +512,11 @@ cudaError_t launch_merge_t(const PagedLaunch& a, cudaStream_t stream) {
 template <int D, int THREADS>
 cudaError_t launch_plan_t(const PagedLaunch& a, cudaStream_t stream) {
   const size_t bytes = (size_t)a.p.num_groups * kGroupBytes + sizeof(int);
-  const cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(kMaxGroups * kGroupBytes + sizeof(int)));
-  if (e != cudaSuccess) return e;
+  if (bytes > 32768) {  // (more than a kernel may have without asking, with what it has besides)
+    const cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(kMaxGroups * kGroupBytes + sizeof(int)));
+    if (e != cudaSuccess) return e;
+  }
   shared_plan_kernel<D, THREADS><<<1, THREADS, bytes, stream>>>(a.p);
   return cudaGetLastError();
 }

@@ -6,6 +6,8 @@
 
 #include <cstddef>
 
+#include "fa_paged_plan.cuh"
+
 namespace fa {
 
 // The plan of a batch whose sequences share keys, in the workspace: what the work is, one
@@ -30,14 +32,9 @@ struct SharedPiece {
 };
 static_assert(sizeof(SharedPlan) == 32 && sizeof(SharedEntry) == 32 && sizeof(SharedPiece) == 32, "16-byte reads");
 
-// Partial rows of rows_kernel's entries in parts: of kMaxParts (16 rows) or half as many (32
-// rows) an SM.  An entry of n keys has at most 2 n / (L + 1) parts of L keys, if it has two;
-// with part_keys()' lengths and W keys times heads for 8 workers an SM these are, a worker,
-// 3 / W for each of the first W / 2, 6 / W for the next 3 W / 10 and 12 / W for the others at most:
-// 5.7 in all.
-constexpr int kMaxParts = 46;
-constexpr int kPartRows = 16;
-inline __host__ __device__ int shared_parts(int sms) { return kMaxParts * sms; }
+using paged::kMaxParts;
+using paged::kPartRows;
+using paged::shared_parts;
 
 // Where the lists lie behind the head: costs in front of the entries, entries, pieces.
 struct SharedLists {

@@ -239,5 +239,29 @@ __host__ __device__ inline int tile0_count(const Q& q, const Segment& g, const S
 // The key tile that holds a sequence's last key (0 if it has none).
 __host__ __device__ inline int last_tile(int kv) { return kv > 0 ? (kv - 1) >> 7 : 0; }
 
+// Parts of an SM and fewest keys of one (an entry with few rows of a batch whose sequences
+// share keys), and what their keys are multiples of.
+constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
+
+// Keys of the parts of such an entry that has `before` of all of those entries' `keys` (times
+// their heads) in front of it: an eighth of a CTA's share, and half of that for the last fifth
+// of the keys, which end when there is nothing else left to take.  With two row tiles (`tiles`)
+// parts are twice as long, as there are half as many CTAs and places.
+__host__ __device__ inline int part_keys(float before, float keys, int tiles, int sms) {
+  const float share = keys / (kPartsASm * sms) * (5.f * before > 4.f * keys ? 0.5f : 1.f) * tiles;
+  // (a share beyond all keys that there can be, 2^30, leaves every entry whole)
+  const int n = (share < 1073741824.f ? (int)share : 1 << 30) / kPartStep * kPartStep + kPartStep;
+  return imax(n, kLeastPart * tiles);
+}
+__host__ __device__ inline int parts_of_keys(int keys, int part) { return imax(0, keys - 1) / part + 1; }
+
+// Parts that there is room for, of kPartRows rows (or half as many of twice the rows).  An entry
+// of n keys in several parts of L has fewer than 2 n / L; with W keys times heads in all and
+// part_keys()' lengths these are fewer than 2 * 16 * 0.8 an SM for those that begin in the first
+// four fifths, and 2 * 32 * 0.2 for the others: 38.4.
+constexpr int kMaxParts = 46;
+constexpr int kPartRows = 16;
+inline __host__ __device__ int shared_parts(int sms) { return kMaxParts * sms; }
+
 }  // namespace paged
 }  // namespace fa

@@ -44,19 +44,6 @@ template <int D>
 __device__ __forceinline__ float rows_cost(int keys, int rows) {
   return (D == 128 ? 14.f : 7.f) * (keys + 32) + 128.f * (rows > kFewRows ? 60 : rows * D > 512 ? 12 : 6);
 }
-// Parts of an SM and fewest keys of one (an entry with few rows), and what their keys are multiples of.
-constexpr int kPartsASm = 16, kLeastPart = 256, kPartStep = 64;
-
-// Keys of the parts of an entry with few rows that has `before` of all of those entries'
-// `keys` (times their heads) in front of it: an eighth of a CTA's share, and half of that for
-// the last fifth of the keys, which end when there is nothing else left to take.  With two row
-// tiles parts are twice as long, as there are half as many CTAs and places.
-__device__ __forceinline__ int part_keys(float before, float keys, int few_rows, int sms) {
-  const int tiles = few_rows / kFewRows;
-  const float share = keys / (kPartsASm * sms) * (5.f * before > 4.f * keys ? 0.5f : 1.f) * tiles;
-  const int n = (int)fminf(share, 1e9f) / kPartStep * kPartStep + kPartStep;
-  return imax(n, kLeastPart * tiles);
-}
 
 // ------------------------------------------------------------------ the lists --
 // Sums of a thread's values over those in front of it; *total grows by all.
@@ -296,8 +283,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     const bool few_rows = q.qn > 0 && q.qn <= few, many_rows = q.qn > few;
     int part = 1, parts = 0;
     if (few_rows) {
-      part = part_keys(front_of.keys * p.Hk, all_keys, p.few_rows, p.sms);
-      parts = imax(1, (q.kv + part - 1) / part);
+      part = part_keys(front_of.keys * p.Hk, all_keys, p.few_rows / kFewRows, p.sms);
+      parts = parts_of_keys(q.kv, part);
     }
     const Counts before = scan<THREADS>(Counts{many_rows, parts, parts > 1 ? parts : 0, 0}, warp_counts, &total);
     if (many_rows) {

@@ -672,7 +672,8 @@ def paged_extend(requests, new_lens, request_lens, request_table, pool, page_siz
     requests' state and brought up to date.  Returns ``(cu_seqlens [S + 1], kv_lens [S], page_table [S, max_pages],
     positions [tokens], slots [tokens] int64)`` for the other calls; ``out`` gives tensors to write to (any of the
     last two may be None: not wanted), as a captured step does.  Of ``page_table`` only entries in use are written.
-    A sequence that finds no room has ``kv_lens`` 0 and leaves its request as it was."""
+    A sequence that finds no room has ``kv_lens`` 0 and leaves its request as it was.  Pages that requests share are
+    full ones."""
     where = _elsewhere(requests, stream)
     if where is not None:
         with where:
@@ -705,7 +706,8 @@ def paged_release(requests, request_lens, request_table, pool, page_size, keep_l
                   stream=None):
     """The requests ``requests [S]`` (negative: none) give pages back to the pool and keep their first ``keep_lens
     [S]`` keys (None: none).  ``kept_pages [R]`` counts the pages at the front of each request that it shares and
-    does not own (None: it owns all)."""
+    does not own (None: it owns all); a request that keeps fewer keys than those hold has its count brought down by
+    the caller."""
     where = _elsewhere(requests, stream)
     if where is not None:
         with where:

@@ -35,6 +35,8 @@
 //               own query buffer, which is dead by then.
 // SHORT kernels hold only the last form: the host takes them where it was told
 // that chunks are short; a longer chunk is then a row of small units.
+// SHARED kernels take their units from a list (fa_paged_shared.cu), on as many of the
+// CTAs as the list says, and leave whole rows' partial outputs to another merge.
 //
 // Rounding: scores, maxima, sums and O are fp32.  P is rounded to bf16 once, as the
 // MMA takes it (its sum takes the fp32 values), for single tokens, too, which run the

@@ -2,8 +2,10 @@
 // share keys (fa_paged_shared.cu) that have at most 16 (or 32) query rows a key head:
 // single tokens, mostly, behind their group's shared keys.
 //
-// Bound: the read of K and V (4 d bytes a key for 4 d G FLOP).  The units are short, a
-// few hundred keys, so what matters is that loads never wait for the end of one.  The
+// Bound: the read of K and V (4 d bytes a key for 4 d G FLOP; 64 single tokens of 8192 keys,
+// 32 + 8 heads, d = 128, pages of 128: 320 us for 2.15 GB, 6.7 TB/s, the rate of a copy;
+// pages of 16: 330).  The units are short, a few hundred keys, so what matters is that loads
+// never wait for the end of one.  The
 // 128-row tiles of paged_kernel take 2 us from a unit's last key tile to the next one's
 // first scores (tensor memory, barriers between the roles, eight partial rows merged by
 // the whole CTA); here a unit's end costs the loads nothing:
@@ -14,13 +16,15 @@
 //     results stay in registers (mma.sync: 16 rows are an eighth of tcgen05's smallest
 //     tile, and the way through tensor memory and back is most of a short unit's time;
 //     the MMAs here are busy a fifth of the time that the loads take), a running maximum
-//     and sum of its own, P from the registers of S, O += P V
+//     and sum of its own, P from the registers of S, O += P V.  More rows than a tile or two
+//     are paged_kernel's: 64 would keep these MMAs busy three quarters of the time
 //   the stages of the next unit go on where those of the last one ended, so that units of
 //     a stage or two run side by side; the warp that is the last to put its partial rows
 //     into shared memory joins them, while the others are at the next unit
 //
 // Units are (piece, key head) pairs in the order of a list; CTAs take them from a
-// counter.  Which CTA computes a unit has no part in its result: its stages go to the
+// counter, as paged_kernel's CTAs leave their SMs to this kernel one after the other.  Which
+// CTA computes a unit has no part in its result: its stages go to the
 // warps in the order of the unit, and are joined in that order, too.
 //
 // Rounding as in paged_kernel: scores, maxima, sums and O in fp32, P to bf16 once for the
@@ -94,9 +98,8 @@ __device__ __forceinline__ void mma_rows(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A warp's bounded wait.  The time is looked at every 64 tests only: reading the timer takes
-// as long as most of these waits (64 single tokens of 330 keys, 32 + 8 heads, d = 128: FIGURE us with
-// it in front of the second test).
+// A warp's bounded wait.  The time is looked at every 64 tests only (in front of the second
+// test it took 38.1 us instead of 37.9: 64 single tokens of 330 keys, 32 + 8 heads, d = 128).
 __device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, int* status) {
   const uint32_t a = smem_addr(bar);
   uint32_t t0 = 0;

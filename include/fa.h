@@ -359,7 +359,11 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  *  pool[2 .. 2 + pool[0]) their numbers, the next one to be taken last.  The
  *  caller sets all of it up (every page free: pool[0] = num_pages, pool[1] = 0)
  *  and may change it between calls.  Calls on the same requests or the same
- *  pool must not overlap.
+ *  pool must not overlap, and the outputs are arrays of their own.
+ *  Requests may share pages, written by the caller into the front of their rows
+ *  of request_table with the lengths to match: full pages only (the next token
+ *  of a request goes to the page that its length ends in), counted in
+ *  kept_pages when they are released.
  *
  * fa_paged_extend: room for the new tokens of a step, and the step's tables for
  * fa_paged_append and the attention over the cache.  One launch.
@@ -394,7 +398,9 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  *   keep_lens  in   [S] int32: keys that each keeps (a step whose tokens are not
  *                   all accepted keeps those in front), or NULL: none
  *   kept_pages in   [R] int32, or NULL: pages at the front of each request that are
- *                   not its own (a shared prompt's) and stay out of the pool
+ *                   not its own (a shared prompt's) and stay out of the pool.
+ *                   A request that keeps fewer keys than these hold has its count
+ *                   brought down by the caller before it is extended again
  *   request_lens    in, out  becomes keep_lens
  *   request_table   in   [R, max_pages]
  *   pool            in, out  the pages behind those kept, so that fa_paged_extend of
@@ -481,13 +487,13 @@ size_t fa_fwd_paged_workspace_size(int d);
  *   others    as in fa_fwd_paged, which see
  *   workspace fa_fwd_paged_shared_workspace_size(T, S, num_groups, Hq, d) bytes,
  *             256-byte aligned, under fa_fwd_paged's rules: two fp32 rows for each
- *             row of the output, and the work's list
+ *             row of the output, the rows of entries in parts, the work's list
  *
  * Any prefix_lens[g] that is true is right: what is computed once is cut to the
  * keys that every sequence of the group has in front of its new tokens (with
- * causal = 0: has), and to whole tiles of 128 keys and whole pages, and is
- * nothing where that costs no less (a group of few rows, long chunks that fill
- * the tensor cores by themselves); the other keys are each sequence's own.
+ * causal = 0: has), and to whole pages, and is nothing where that costs no less
+ * (a group of one, long chunks that fill the tensor cores by themselves); the
+ * other keys are each sequence's own.
  * groups and prefix_lens live on the device as the lengths do, so that one
  * captured graph serves every step of the same T, S and num_groups.  Values of
  * groups outside of 0 .. S or decreasing, and prefix_lens outside of
@@ -495,8 +501,11 @@ size_t fa_fwd_paged_workspace_size(int d);
  * FA_ERR_DEVICE_INDEX; rows of sequences that two groups then hold are not
  * specified.
  *
- * Three launches.  Results are the same bits on every run.  In the last bits a
- * row depends on the other sequences of its group.  num_groups <= 4096
+ * Four launches (three where T * Hq / Hk is at most 16 or 32).  Results are the
+ * same bits on every run.  In the last bits a row depends on the other sequences
+ * of its group, and on the lengths of the whole batch (which say how keys are cut
+ * into parts).  max_q says as well which of two forms steps of a few tokens take:
+ * what it is told wrongly costs time alone.  num_groups <= 4096
  * (FA_ERR_UNSUPPORTED above); 0 with groups and prefix_lens NULL is allowed.
  */
 int fa_fwd_paged_shared(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,

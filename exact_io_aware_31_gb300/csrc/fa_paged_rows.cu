@@ -18,6 +18,10 @@
 //     the MMAs here are busy a fifth of the time that the loads take), a running maximum
 //     and sum of its own, P from the registers of S, O += P V.  More rows than a tile or two
 //     are paged_kernel's: 64 would keep these MMAs busy three quarters of the time
+//   where a unit has up to 32 rows a second team of five warps takes the other 16: it reads
+//     the same stages, a warp of each team a stage (one warp for both tiles took 1.9 us a
+//     stage, and five warps 1.9 us to join a unit: 51 sequences of 5 tokens, 20 + 4 heads,
+//     in 4 groups 46.5 us, 40.6 with two teams)
 //   the stages of the next unit go on where those of the last one ended, so that units of
 //     a stage or two run side by side; the warp that is the last to put its partial rows
 //     into shared memory joins them, while the others are at the next unit
@@ -59,19 +63,21 @@ struct RowsCfg {
   static constexpr int kStageBytes = 2 * kKvBytes;
   static constexpr int kStages = MT == 1 ? 5 : 10;
   static constexpr int kCtas = rows_ctas(kRows);      // an SM
-  // Warps that compute.  The stages are a multiple of them, so that a stage's buffer has
-  // one reader: a warp that came for a buffer's next contents while another one still waited
-  // for these would take the one's for the other's (a wait knows odd from even).
-  static constexpr int kWarps = 5;
-  static_assert(kStages % kWarps == 0, "one reader a buffer");
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  // Warps that compute.  The stages are a multiple of a team's, so that a stage's buffer has
+  // one reader in each: a warp that came for a buffer's next contents while another one still
+  // waited for these would take the one's for the other's (a wait knows odd from even).  Two
+  // that both read all of its contents cannot come apart so far.
+  static constexpr int kWarps = 5;                    // of a team, which has 16 rows
+  static constexpr int kAll = MT * kWarps;
+  static_assert(kStages % kWarps == 0, "one reader a buffer and team");
+  static constexpr int kThreads = 32 * (kAll + 1);
   static constexpr int kJoinFloats = 512;             // room of a warp for partial rows
   static constexpr int kItems = 8;                    // units that the producer may be ahead
   static constexpr int kOffJoin = kStages * kStageBytes;                  // [2][warps][kJoinFloats]
   static constexpr int kOffMl = kOffJoin + 2 * kWarps * kJoinFloats * 4;  // [2][warps][rows] (m, l)
   static constexpr int kOffItem = kOffMl + 2 * kWarps * kRows * 8;        // [kItems] 64 bytes
   static constexpr int kOffBar = kOffItem + kItems * 64;
-  static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 * 2;
+  static constexpr int kNumBars = 2 * kStages + 2 * kItems + 2 * 2 + kWarps;
   static constexpr int kOffArrived = kOffBar + 8 * kNumBars;  // [2] warps whose rows are in the room
   static constexpr int kOffAbort = kOffArrived + 8;
   static constexpr int kSmemBytes = kOffAbort + 8;
@@ -146,23 +152,28 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
     return;
   }
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBar);  // [stages] K and V are there
-  uint64_t* empty = full + C::kStages;                            // the warp that took it is done
+  uint64_t* empty = full + C::kStages;                            // the warps that took it are done
   uint64_t* item_full = empty + C::kStages;                       // [items]
   uint64_t* item_empty = item_full + C::kItems;
   uint64_t* room_free = item_empty + C::kItems;                   // [2] its rows have been joined
   uint64_t* room_full = room_free + 2;                            // [2] (many rows) every warp's part is there
+  uint64_t* last_read = room_full + 2;                            // [warps] (many rows) all teams' are done with their last stage
   int* arrived = reinterpret_cast<int*>(sm + C::kOffArrived);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == 0) {
     for (int i = lane; i < C::kNumBars; i += 32) {
       uint64_t* bar = full + i;
-      mbar_init(bar, bar >= room_full ? 32 * C::kWarps : bar >= item_empty ? C::kWarps : 1);
+      mbar_init(bar, bar >= last_read                      ? MT
+                     : bar >= room_full                    ? 32 * C::kAll
+                     : bar >= item_empty                   ? C::kAll
+                     : bar >= empty && bar < item_full     ? MT
+                                                           : 1);
     }
     if (lane == 0) *abort_flag = 0, arrived[0] = arrived[1] = 0;
     fence_mbar_init();
   }
-  if (warp == C::kWarps && lane == 0) {
+  if (warp == C::kAll && lane == 0) {
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
   }
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
   // where there is none between, is the one that makes them.
   if (p.T * (long long)p.G <= p.few_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == C::kWarps) {
+  if (warp == C::kAll) {
     // ---------------------------------------------------------------- producer --
     const SharedPiece* list = reinterpret_cast<const SharedPiece*>(reinterpret_cast<const uint8_t*>(p.plan) +
                                                                    shared_lists(p.S, p.num_groups, p.sms).pieces);
@@ -275,7 +286,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
     const uint32_t half = imin(1 << p.page_log2, C::kKeys) * 128;
     const uint32_t keys16 = D == 64 ? 2048 : half == 2048 ? 4096 : 2048;
     const int g = lane / 4, c = lane % 4;  // rows g and g + 8, columns 2 c and 2 c + 1 of a result's tile
-    uint32_t rooms = 0, fulls = 0;  // uses of the rooms; bit r: parity of room_full[r]
+    const int team = MT > 1 ? warp / C::kWarps : 0, mine = warp - team * C::kWarps, row0 = kFewRows * team;
+    uint32_t rooms = 0, fulls = 0, reads = 0;  // uses of the rooms, of last_read; bit r: parity of room_full[r]
     bool ok = true;
     const size_t all = (size_t)p.T * p.Hk * p.G;
     const size_t rows0 = (size_t)p.sms * (2 * kPagedRows);
@@ -290,7 +302,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       if (u.end) break;
       const int valid = u.qn * p.G;  // rows
       // This warp's stages: place, place + kWarps, .. of the unit; `takers` warps have some.
-      const int place = (warp + C::kWarps - u.base % C::kWarps) % C::kWarps;
+      const int place = (mine + C::kWarps - u.base % C::kWarps) % C::kWarps;
       const int takers = imax(1, imin(u.stages, C::kWarps));
       // Rows that fit into a room are joined by the last warp to bring its part; more of them by
       // all, out of the buffers of their last stages, which the producer gets back then.
@@ -306,34 +318,38 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       const bool causal = p.causal && u.kind != kPrefix;
       const int past = u.kv - u.qn;
       const int lim0 = causal ? imin(past, u.kv - 1) : u.kv - 1;  // last key that all rows see
-      int lim[2 * MT];
-      float m[2 * MT], l[2 * MT], o[MT][D / 8][4];
+      const bool idle = row0 >= valid;  // this team has no rows: it keeps count
+      int lim[2];
+      float m[2], l[2], o[D / 8][4];
       // The queries, in the layout of an MMA's first operand; rows that are no token's are zero.
-      uint32_t qa[MT][D / 16][4];
+      uint32_t qa[D / 16][4];
       const __nv_bfloat16* q_head = queries + (size_t)u.hk * p.G * q_stride_h;
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        const int row = g + 8 * i, tok = (row * p.g_inverse) >> 16;
+      for (int i = 0; i < 2; ++i) {
+        const int row = row0 + g + 8 * i, tok = (row * p.g_inverse) >> 16;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(q_head + (size_t)(u.q0 + tok) * q_stride_t +
                                                                 (size_t)(row - tok * p.G) * q_stride_h) + c;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const bool there = row < valid && place < takers;
-          qa[i / 2][k][i & 1] = there ? __ldg(src + 8 * k) : 0u;
-          qa[i / 2][k][2 + (i & 1)] = there ? __ldg(src + 8 * k + 4) : 0u;
+          qa[k][i] = there ? __ldg(src + 8 * k) : 0u;
+          qa[k][2 + i] = there ? __ldg(src + 8 * k + 4) : 0u;
         }
         lim[i] = causal ? imin(past + tok, u.kv - 1) : u.kv - 1;
         m[i] = -INFINITY;
         l[i] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
       for (int i = place; i < u.stages; i += C::kWarps) {
         const uint32_t it = (uint32_t)u.base + i;
         const int st = it % C::kStages;
         if (!(ok = wait_short(&full[st], (it / C::kStages) & 1, status))) break;
+        if (MT > 1 && idle) {
+          __syncwarp();
+          if (lane == 0 && !(hold && i + C::kWarps >= u.stages)) mbar_arrive(&empty[st]);
+          continue;
+        }
         const uint32_t k_s = stage0 + st * C::kStageBytes, v_s = k_s + C::kKvBytes;
         const int key0 = u.k0 + i * C::kKeys, used = u.kv - key0;  // keys of the stage that the entry has
         if (used < C::kKeys) {
@@ -346,11 +362,9 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
           __syncwarp();
         }
         // S = Q K^T: 8 keys a tile
-        float s[MT][C::kKeys / 8][4];
+        float s[C::kKeys / 8][4];
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int n = 0; n < C::kKeys / 8; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
+        for (int n = 0; n < C::kKeys / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2)  // 32 columns
 #pragma unroll
@@ -358,25 +372,22 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
             uint32_t kf[4];
             const int row = lane & 7, chunk = 4 * (k2 & 1) + (lane >> 3);
             ldsm4(k_s + (k2 >> 1) * half + (n >> 1) * keys16 + ((n & 1) * 8 + row) * 128 + ((chunk ^ row) << 4), kf);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              mma_rows(s[j][n], qa[j][2 * k2], kf[0], kf[1]);
-              mma_rows(s[j][n], qa[j][2 * k2 + 1], kf[2], kf[3]);
-            }
+            mma_rows(s[n], qa[2 * k2], kf[0], kf[1]);
+            mma_rows(s[n], qa[2 * k2 + 1], kf[2], kf[3]);
           }
         // in log2 units; -inf where masked
-        float mx[2 * MT];
+        float mx[2];
         bool need = false;
         const bool masked = key0 + C::kKeys - 1 > lim0;
 #pragma unroll
-        for (int i2 = 0; i2 < 2 * MT; ++i2) {
+        for (int i2 = 0; i2 < 2; ++i2) {
           float t = -INFINITY;
           const int last = lim[i2] - key0 - 2 * c;
 #pragma unroll
           for (int n = 0; n < C::kKeys / 8; ++n) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float& y = s[i2 / 2][n][2 * (i2 & 1) + x];
+              float& y = s[n][2 * i2 + x];
               y *= c2;
               if (masked) y = 8 * n + x > last ? -INFINITY : y;
               t = fmaxf(t, y);
@@ -389,26 +400,26 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
         // A row's maximum moves by what the row itself holds, whatever makes the warp come here.
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-          for (int i2 = 0; i2 < 2 * MT; ++i2) {
+          for (int i2 = 0; i2 < 2; ++i2) {
             const bool moves = mx[i2] > m[i2] + kRescaleThreshold;
             const float alpha = !moves ? 1.f : m[i2] == -INFINITY ? 0.f : ex2(m[i2] - mx[i2]);
             m[i2] = moves ? mx[i2] : m[i2];
             l[i2] *= alpha;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) o[i2 / 2][n][2 * (i2 & 1)] *= alpha, o[i2 / 2][n][2 * (i2 & 1) + 1] *= alpha;
+            for (int n = 0; n < D / 8; ++n) o[n][2 * i2] *= alpha, o[n][2 * i2 + 1] *= alpha;
           }
         }
         // P = 2^(s - m) (0 where masked), summed before its rounding; O += P V: 16 keys at a time
-        uint32_t pa[MT][C::kKeys / 16][4];
+        uint32_t pa[C::kKeys / 16][4];
 #pragma unroll
-        for (int i2 = 0; i2 < 2 * MT; ++i2) {
+        for (int i2 = 0; i2 < 2; ++i2) {
           const float ref = m[i2] == -INFINITY ? 0.f : m[i2];
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < C::kKeys / 8; ++n) {
-            const float p0 = ex2(s[i2 / 2][n][2 * (i2 & 1)] - ref), p1 = ex2(s[i2 / 2][n][2 * (i2 & 1) + 1] - ref);
+            const float p0 = ex2(s[n][2 * i2] - ref), p1 = ex2(s[n][2 * i2 + 1] - ref);
             sum += p0 + p1;
-            pa[i2 / 2][n / 2][2 * (n & 1) + (i2 & 1)] = pack_bf16x2(p0, p1);
+            pa[n / 2][2 * (n & 1) + i2] = pack_bf16x2(p0, p1);
           }
           l[i2] += sum;
         }
@@ -419,11 +430,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
             uint32_t vf[4];
             const int row = lane & 15, chunk = 2 * (n2 & 3) + (lane >> 4);
             ldsm4t(v_s + (n2 >> 2) * half + k * keys16 + row * 128 + ((chunk ^ (row & 7)) << 4), vf);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              mma_rows(o[j][2 * n2], pa[j][k], vf[0], vf[1]);
-              mma_rows(o[j][2 * n2 + 1], pa[j][k], vf[2], vf[3]);
-            }
+            mma_rows(o[2 * n2], pa[k], vf[0], vf[1]);
+            mma_rows(o[2 * n2 + 1], pa[k], vf[2], vf[3]);
           }
         if (used < C::kKeys) fence_proxy_async_smem();  // the next copy comes behind the zeros
         __syncwarp();
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       }
       if (!ok) break;
 #pragma unroll
-      for (int i2 = 0; i2 < 2 * MT; ++i2) {
+      for (int i2 = 0; i2 < 2; ++i2) {
         l[i2] += __shfl_xor_sync(0xffffffffu, l[i2], 1);
         l[i2] += __shfl_xor_sync(0xffffffffu, l[i2], 2);
       }
@@ -460,8 +468,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       };
       if (takers == 1) {  // nothing to join
 #pragma unroll
-        for (int i2 = 0; i2 < 2 * MT; ++i2) {
-          const int row = g + 8 * i2;
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int row = row0 + g + 8 * i2;
           if (row >= valid) continue;
           const size_t at = out_row(row);
           if (c == 0) put_ml(row, at, m[i2], l[i2]);
@@ -470,16 +478,21 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
             uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at * D) + c;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
-              out[4 * n] = pack_bf16x2(o[i2 / 2][n][2 * (i2 & 1)] * inv, o[i2 / 2][n][2 * (i2 & 1) + 1] * inv);
+              out[4 * n] = pack_bf16x2(o[n][2 * i2] * inv, o[n][2 * i2 + 1] * inv);
           } else {
             float2* out = reinterpret_cast<float2*>(p.part_o + part_row(row, at) * D) + c;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
-              out[4 * n] = make_float2(o[i2 / 2][n][2 * (i2 & 1)], o[i2 / 2][n][2 * (i2 & 1) + 1]);
+              out[4 * n] = make_float2(o[n][2 * i2], o[n][2 * i2 + 1]);
           }
         }
         __syncwarp();
         continue;
+      }
+      // The buffers of the last stages are written to next: all teams have read them.
+      if (MT > 1 && hold && place < takers) {
+        if (lane == 0) mbar_arrive(&last_read[mine]);
+        if (!(ok = wait_short(&last_read[mine], reads++ & 1, status))) break;
       }
       // This warp's (m, l) and rows.  (Every warp takes part in every use of a room, if only by
       // its arrival, so that none is a use ahead or behind.)
@@ -494,14 +507,14 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
       if (place < takers) {
         float* to = rows_of(place);
 #pragma unroll
-        for (int i2 = 0; i2 < 2 * MT; ++i2) {
-          const int row = g + 8 * i2;
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const int row = row0 + g + 8 * i2;
           if (row >= valid) continue;
           if (c == 0) ml[place * C::kRows + row] = make_float2(m[i2], l[i2]);
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
             *reinterpret_cast<float2*>(to + row * D + ((8 * n + 2 * c) ^ (8 * (row & 3)))) =
-                make_float2(o[i2 / 2][n][2 * (i2 & 1)], o[i2 / 2][n][2 * (i2 & 1) + 1]);
+                make_float2(o[n][2 * i2], o[n][2 * i2 + 1]);
         }
       }
       // Four columns of a row, joined in the order of the unit's stages.
@@ -549,14 +562,15 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::kThreads, RowsCfg<D, MT>::kCta
         mbar_arrive(&room_full[r]);
         if (!(ok = wait_short(&room_full[r], fulls >> r & 1, status))) break;
         fulls ^= 1u << r;
-        for (int x = threadIdx.x; x < valid * (D / 4); x += 32 * C::kWarps) join(x);
+        for (int x = threadIdx.x; x < valid * (D / 4); x += 32 * C::kAll) join(x);
         fence_proxy_async_smem();  // the next copies come behind these accesses
-        if (came() == C::kWarps) {
+        if (came() == C::kAll) {
           if (lane < takers)
-            mbar_arrive(&empty[(u.base + lane + (u.stages - 1 - lane) / C::kWarps * C::kWarps) % C::kStages]);
+            for (int j = 0; j < MT; ++j)
+              mbar_arrive(&empty[(u.base + lane + (u.stages - 1 - lane) / C::kWarps * C::kWarps) % C::kStages]);
           if (lane == 0) arrived[r] = 0;
         }
-      } else if (came() == takers) {
+      } else if (!idle && came() == takers) {
         for (int x = lane; x < valid * (D / 4); x += 32) join(x);
         if (lane == 0) arrived[r] = 0;
       }

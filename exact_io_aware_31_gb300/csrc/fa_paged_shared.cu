@@ -49,7 +49,7 @@ constexpr int kTileStart = 150, kRowsStart = 60;
 // fp32: the block's time is that of its arithmetic, one step after the other.
 template <int D>
 __device__ __forceinline__ float rows_cost(int keys, int rows) {
-  return (D == 128 ? 14.f : 7.f) * (keys + 32) + 128.f * (rows > kFewRows ? 60 : rows * D > 512 ? 12 : 6);
+  return (D == 128 ? 14.f : 7.f) * (keys + 32) + 128.f * (rows > kFewRows ? 40 : rows * D > 512 ? 12 : 6);
 }
 
 // ------------------------------------------------------------------ the lists --

@@ -1380,7 +1380,9 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
     return cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs == C::kLaunchRegs;
   }();
   if (!regs_ok) return cudaErrorInvalidKernelImage;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  // (no launch where no entry can have more rows than rows_kernel takes)
+  const bool any = !SHARED || a.p.T * (long long)a.p.G > a.p.few_rows;
+  cudaError_t e = any ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) : cudaSuccess;
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1394,10 +1396,7 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // (no launch where no entry can have more rows than rows_kernel takes)
-    if (a.p.T * (long long)a.p.G > a.p.few_rows &&
-        (e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess)
-      return e;
+    if (any && (e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_q4, a.tm_k, a.tm_v, a.p)) != cudaSuccess) return e;
     if (a.p.few_rows > 0 && (e = launch_shared_rows(a, stream)) != cudaSuccess) return e;
     return launch_shared_merge(a, stream);
   }

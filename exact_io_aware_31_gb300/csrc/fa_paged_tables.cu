@@ -308,8 +308,10 @@ template <class K>
 cudaError_t launch(K kern, const TablesParams& p, int sms, long long items, cudaStream_t stream) {
   const size_t bytes = (5 * (size_t)p.S + 2 + p.R) * sizeof(int);
   constexpr size_t kMost = (5 * (size_t)kMaxSequences + 2 + kMaxRequests) * sizeof(int);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
-  if (e != cudaSuccess) return e;
+  if (bytes > 32768) {  // (more than a kernel may have without asking, with what it has besides)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    if (e != cudaSuccess) return e;
+  }
   const long long blocks = (items + kWarps - 1) / kWarps;
   kern<<<(unsigned)(blocks < 1 ? 1 : blocks < sms ? blocks : sms), kThreads, bytes, stream>>>(p);
   return cudaGetLastError();

@@ -113,6 +113,24 @@ def test_more_units_than_ctas(Hq, Hk, d):
         assert all(torch.equal(a, b) for a, b in zip(call(x, scale=0.2, max_q=1), want))
 
 
+@pytest.mark.parametrize("Hq,Hk,d,most", [(20, 4, 128, 5), (20, 4, 64, 5), (8, 2, 128, 8), (8, 2, 64, 8), (16, 1, 128, 2),
+                                          (17, 1, 64, 1)])
+def test_units_of_one_and_of_two_row_tiles(Hq, Hk, d, most):
+    """Entries of 1 to 32 rows side by side, more than CTAs, whose second tile has rows or none; NaN in one token's
+    query reaches no other one's rows."""
+    seqs = [(1 + i % most, most + 53 * i % 611) for i in range(190)]
+    x = batch([(256, seqs[:80]), (0, seqs[80:] + [(most, 4000)])], Hq, Hk, d, 32, False)
+    want = call(x, scale=0.2, max_q=most)
+    assert status() == fa.FA_OK
+    check(*want, reference(*x[:5], 0.2, True))
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(call(x, scale=0.2, max_q=most), want))
+    x[0][int(x[3][100])] = float("nan")    # the first token of sequence 100
+    o, lse = call(x, scale=0.2, max_q=most)
+    bad = torch.isnan(o.float()).any(-1).any(-1)
+    assert bad.nonzero().flatten().tolist() == [int(x[3][100])]
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0])
 @pytest.mark.parametrize("shape", ["samples", "chunks"])
 def test_scales(shape, scale):

@@ -781,21 +781,27 @@ def paged_forward_shared(q, k_pages, v_pages, page_table, cu_seqlens, kv_lens, g
     shared = _flat(groups, "groups", (n + 1,), i32, dev), _flat(prefix_lens, "prefix_lens", (n,), i32, dev)
     sq = _rows(q, "q", (T, Hq, d), bf16, dev)
     if out is None:
-        out = torch.empty(T, Hq, d, dtype=bf16, device=q.device)
+        out = torch.empty_like(q) if sq == (Hq * d, d) else torch.empty(T, Hq, d, dtype=bf16, device=q.device)
     else:
         _flat(out, "out", (T, Hq, d), bf16, dev)
     if lse is None:
         lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
     else:
         _flat(lse, "lse", (T, Hq), torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(_shared_room(T, S, n, Hq, d, dev), dtype=torch.uint8, device=q.device)
+    on = torch._C._cuda_getCurrentRawStream(dev)
     ws, wbytes = _room(workspace, dev)
-    st = load_library().fa_fwd_paged_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
-                                            lse.data_ptr(), *meta, *shared, T, S, n, Hq, Hk, d, num_pages, page_size,
-                                            max_pages, *sq, *steps, d ** -0.5 if scale is None else scale,
-                                            1 if causal else 0, max_q, ws, wbytes,
-                                            torch._C._cuda_getCurrentRawStream(dev))
+    own = None  # a workspace of this call alone: the allocator's bytes, without a tensor around them (2 us)
+    if workspace is None and (wbytes := _shared_room(T, S, n, Hq, d, dev)):
+        ws = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(wbytes, on)
+    try:
+        st = load_library().fa_fwd_paged_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(),
+                                                lse.data_ptr(), *meta, *shared, T, S, n, Hq, Hk, d, num_pages,
+                                                page_size, max_pages, *sq, *steps,
+                                                d ** -0.5 if scale is None else scale, 1 if causal else 0, max_q, ws,
+                                                wbytes, on)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged_shared")
     return out, lse

@@ -63,6 +63,7 @@
 #include <type_traits>
 
 #include "fa_common.cuh"
+#include "fa_context.h"
 #include "fa_paged.cuh"
 #include "fa_paged_plan.cuh"
 #include "sm103_ptx.cuh"
@@ -1382,7 +1383,8 @@ cudaError_t launch_paged_t(const PagedLaunch& a, cudaStream_t stream) {
   if (!regs_ok) return cudaErrorInvalidKernelImage;
   // (no launch where no entry can have more rows than rows_kernel takes)
   const bool any = !SHARED || a.p.T * (long long)a.p.G > a.p.few_rows;
-  cudaError_t e = any ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) : cudaSuccess;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = any ? allow_shared(reinterpret_cast<const void*>(kern), C::kSmemBytes, allowed) : cudaSuccess;
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include "fa_common.cuh"
+#include "fa_context.h"
 #include "fa_paged.cuh"
 #include "fa_paged_plan.cuh"
 #include "sm103_ptx.cuh"
@@ -599,7 +600,8 @@ template <int D, int MT>
 cudaError_t launch_rows_t(const PagedLaunch& a, cudaStream_t stream) {
   using C = RowsCfg<D, MT>;
   auto kern = rows_kernel<D, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kern), C::kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -656,8 +656,11 @@ def _tables_args(requests, request_lens, request_table, pool, device):
     """Checks of the tensors that hold the requests: their addresses, ``(S, R, num_pages, max_pages)``."""
     import torch
     i32 = torch.int32
-    S, (R, max_pages), room = (_shape(requests, "requests", 1)[0], _shape(request_table, "request_table", 2),
-                               _shape(pool, "pool", 1)[0])
+    try:
+        (S,), (R, max_pages), (room,) = requests.shape, request_table.shape, pool.shape
+    except (AttributeError, TypeError, ValueError):  # one of them has not these dimensions
+        S, (R, max_pages), room = (_shape(requests, "requests", 1)[0], _shape(request_table, "request_table", 2),
+                                   _shape(pool, "pool", 1)[0])
     if room < 3:
         raise ValueError("pool must hold at least one page")
     return (_flat(requests, "requests", (S,), i32, device), _flat(request_lens, "request_lens", (R,), i32, device),

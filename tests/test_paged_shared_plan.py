@@ -58,8 +58,11 @@ int main() {
     for (int k : keys) all += (float)k;
     long long places = 0;
     for (int k : keys) {
-      const int part = part_keys(before * heads, all * heads, tiles, sms), parts = parts_of_keys(k, part);
-      if (part % kPartStep || part < kLeastPart || parts < 1) return printf("part %d, %d of them\n", part, parts), 1;
+      const int most_keys = part_keys(before * heads, all * heads, tiles, sms);
+      int part = most_keys;
+      const int parts = parts_of_keys(k, part);
+      if (most_keys < kLeastPart || part % kPartStep || part < kPartStep || parts < 1 || part > most_keys * 3ll / 2 + 64)
+        return printf("part %d of %d, %d of them\n", part, most_keys, parts), 1;
       if ((long long)parts * part < k || (parts - 1ll) * part >= (k > 0 ? k : 1))
         return printf("%d parts of %d keys for %d\n", parts, part, k), 1;
       if (parts > 1) places += (long long)parts * heads;

@@ -42,9 +42,9 @@ using namespace paged;
 constexpr size_t kGroupBytes = 8 + 7 * 4;  // of the plan's shared memory
 constexpr int kMaxCtas = 178;  // (their parts' places are below 2^13, as a row's mark has room for)
 static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
-// What paged_kernel takes until its first tile and behind its last, and rows_kernel (a tenth of
-// a microsecond, as all costs).
-constexpr int kTileStart = 150, kRowsStart = 60;
+// What paged_kernel takes until its first tile and behind its last, what of it between two units,
+// and what rows_kernel takes (a tenth of a microsecond, as all costs).
+constexpr int kTileStart = 150, kTileEnds = 100, kRowsStart = 60;
 // Cost of a unit of rows_kernel: its share of an SM's copies for 128 keys, and its beginning and
 // end (more where all warps join its rows).  Like all that only decides how work is divided, in
 // fp32: the block's time is that of its arithmetic, one step after the other.
@@ -306,11 +306,16 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   }
   if (tid == 0) {
     costs[total.entries] = many_all;
-    // (a multiple of the units: units of one cost are then cut into the same parts, and no CTA
-    // has the end of one and the beginning of the next, which take it 6 us each)
+    // (a multiple of the units where that costs less than it gives: units of one cost are then
+    // cut into the same parts, and no CTA has the end of one and the beginning of the next,
+    // which take it 6 us each.  13 sequences, 5 of them of 196 tokens, behind 20318 keys, 10
+    // heads on 2, d = 64: 122 us on 80 CTAs, the only multiple of 80 units, 79 on 152)
     int ctas = few_all > 0.f && most > 0 ? (int)(best & 255) : most;
     const unsigned long long units = (unsigned long long)all_units * p.Hk;
-    if (units > 0 && units < (unsigned long long)ctas) ctas -= ctas % (int)units;
+    if (units > 0 && units < (unsigned long long)ctas) {
+      const int fewer = ctas - ctas % (int)units;
+      if (1.4f * many_all * (1.f / fewer - 1.f / ctas) <= 128 * kTileEnds) ctas = fewer;
+    }
     int4* head = reinterpret_cast<int4*>(p.plan);
     head[0] = make_int4(total.entries, total.pieces, ctas, 0);
     head[1] = make_int4(row0, row1, 0, 0);

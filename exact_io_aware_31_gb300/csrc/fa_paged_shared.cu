@@ -44,7 +44,7 @@ constexpr int kMaxCtas = 178;  // (their parts' places are below 2^13, as a row'
 static_assert(kMaxCtas * kMaxParts < 1 << 13, "a row's mark");
 // What paged_kernel takes until its first tile and behind its last, what of it between two units,
 // and what rows_kernel takes (a tenth of a microsecond, as all costs).
-constexpr int kTileStart = 150, kTileEnds = 100, kRowsStart = 60;
+constexpr int kTileStart = 150, kTileEnds = 80, kRowsStart = 60;
 // Cost of a unit of rows_kernel: its share of an SM's copies for 128 keys, and its beginning and
 // end (more where all warps join its rows).  Like all that only decides how work is divided, in
 // fp32: the block's time is that of its arithmetic, one step after the other.

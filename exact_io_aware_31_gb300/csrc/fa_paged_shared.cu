@@ -235,8 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     if (i < NG) {
       if (keys[i] > 0) q = prefix_of(i, keys[i]);
     } else if (i < N) {
-      bool unused = false;
-      static_cast<Seq&>(q) = i == tid ? mine : sequence(i - NG, unused);
+      static_cast<Seq&>(q) = i == tid ? mine : sequence(i - NG, bad);  // (without groups the first look at it)
       if (q.qn > 0) {
         const int g = i == tid ? my_group : NG > 0 ? group_of(i - NG) : -1;
         const int n = g >= 0 ? keys[g] : 0;

@@ -172,6 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
     return x < held ? __ldg(p.request_table + (size_t)r * p.max_pages + x)
                     : __ldg(stack + clamp(count - 1 - (seq.before[s] + x - held), 0, p.num_pages - 1));
   };
+  // What the caller's rows hold, and through release() the stack, may be no page: its tokens have
+  // no slot (the caller writes to its own cache by them), and each entry in use is looked at below.
+  auto is_page = [&](int x) { return (unsigned)x < (unsigned)p.num_pages; };
+  bool lost = false;
   const long long items = (long long)pieces + (T + kTokens - 1) / kTokens;
   for (long long i = (long long)blockIdx.x * kWarps + tid / 32; i < items; i += (long long)gridDim.x * kWarps) {
     if (i < pieces) {
@@ -190,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
       for (int k = 0; k < kPiece / 32; ++k) {
         const int x = x0 + 32 * k + lane;
         if (x >= used) continue;
+        lost = lost || !is_page(page[k]);
         p.page_table[(size_t)s * p.max_pages + x] = page[k];
         if (x >= held) p.request_table[(size_t)r * p.max_pages + x] = page[k];
       }
@@ -206,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
           pos[k] = -1;
           if (r >= 0) {
             pos[k] = seq.old[s] + ((int)t - seq.cu[s]);
-            slot[k] = ((long long)page_of(s, r, pos[k] >> lg) << lg) + (pos[k] & ((1 << lg) - 1));
+            const int page = page_of(s, r, pos[k] >> lg);
+            if (is_page(page)) slot[k] = ((long long)page << lg) + (pos[k] & ((1 << lg) - 1));
           }
         }
       }
@@ -224,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
       p.cu_seqlens[s] = seq.cu[s];
       if (s < S) p.kv_lens[s] = seq.request[s] >= 0 ? seq.old[s] + seq.cu[s + 1] - seq.cu[s] : 0;
     }
-    if (bad) record_index(p.status);
+    lost = lost || bad;
   }
+  if (lost) record_index(p.status);
   if (!last_block(p)) return;
   for (int s = tid; s < S; s += kThreads)
     if (seq.request[s] >= 0) p.request_lens[seq.request[s]] = seq.old[s] + seq.cu[s + 1] - seq.cu[s];

@@ -390,7 +390,10 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  * too): its request stays as it was, its kv_lens is 0, so that it attends to
  * nothing and nothing of it is cached, the positions and slots of its rows are
  * -1, and FA_ERR_DEVICE_INDEX is recorded.  The caller sees it in kv_lens and
- * may bring it again.  cu_seqlens counts its rows (cut to T).
+ * may bring it again.  cu_seqlens counts its rows (cut to T).  A page outside of
+ * the pool among the entries in use (of the caller's, or come back with such a
+ * row) records FA_ERR_DEVICE_INDEX at every step that meets it; tokens in it have
+ * the slot -1, and fa_paged_append and the attention take it as they say.
  *
  * fa_paged_release: requests give their pages back.  One launch.
  *
@@ -409,7 +412,8 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  * A request that is not in 0 .. R-1, stands in front already or is to keep what
  * it does not have stays as it is; where more pages come back than the pool has
  * room for (some came back before) nothing is done.  Both, and a page outside of
- * the pool in the table, record FA_ERR_DEVICE_INDEX.
+ * the pool in the table (which comes back as the others do), record
+ * FA_ERR_DEVICE_INDEX.
  *
  * page_size and max_pages are the cache's; num_pages <= 2^30, S <= 4096 and R <=
  * 16384 (FA_ERR_UNSUPPORTED above).  S = 0 does nothing.

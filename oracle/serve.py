@@ -157,6 +157,9 @@ class Tables:
             self.lens[r] += n
             kv[s] = self.lens[r]
             out[s, :need] = self.table[r, :need]
+            lost = [not 0 <= x < self.num_pages for x in out[s, :need]]  # no pages of the pool: no slots in them
+            self.bad |= any(lost)
+            slots[first:row] = np.where(np.array(lost, dtype=bool)[at // self.page], -1, slots[first:row])
         return np.array(cu), np.array(kv), out, positions, slots
 
     def release(self, requests, keep_lens=None, kept_pages=None):

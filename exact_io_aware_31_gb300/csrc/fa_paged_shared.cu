@@ -112,8 +112,8 @@ __device__ __forceinline__ SharedPiece pack_piece(const SharedSeq& q, int k0, in
 }
 
 // One block.  Cuts each group's shared keys to whole pages that all of its sequences with
-// new tokens have in front of those, and drops them where computing them once costs no
-// less.  Thread by thread the entries are the groups' shared keys, then the sequences; with
+// new tokens and keys have in front of those, and drops them where computing them once costs
+// no less.  Thread by thread the entries are the groups' shared keys, then the sequences; with
 // no more entries than threads each is looked at once.
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedParams p) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
   unsigned long long* apart = plan_smem;            // [NG] cost of a key tile for each of its sequences by itself
   int* start = reinterpret_cast<int*>(apart + NG);  // [NG + 1]
   int* front = start + NG + 1;                      // [NG] keys in front of the new tokens, the fewest
-  int* first = front + NG;                          // [NG] first sequence with new tokens
+  int* first = front + NG;                          // [NG] first sequence with new tokens and keys
   int* row = first + NG;                            // [NG] its first row
   int* row_end = row + NG;                          // [NG] behind the last one's rows
   int* members = row_end + NG;                      // [NG] how many there are
@@ -164,6 +164,9 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     }
     return lo - 1 < NG ? lo - 1 : -1;
   };
+  // A sequence without keys (left out of the step, as its pages were not there) sees nothing, and
+  // keeps the others from sharing nothing: its rows are its own entry's.
+  auto in_group = [](const Seq& q) { return q.qn > 0 && q.kv > 0; };
   int my_group = -1;  // of the sequence that `mine` is
   if (NG > 0) {
     for (int i0 = 0; i0 < N; i0 += THREADS) {
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
       int g = -1, f = 0x7fffffff, q0 = 0, q1 = 0, cost = 0;
       if (i >= NG && i < N) {
         const Seq q = i0 == 0 ? mine : sequence(s, bad);
-        if (q.qn > 0 && (g = group_of(s)) >= 0) {
+        if (in_group(q) && (g = group_of(s)) >= 0) {
           f = imax(0, p.causal ? q.kv - q.qn : q.kv);
           q0 = q.q0, q1 = q.q0 + q.qn;
           const int full = q.qn / sh.ut, rest = q.qn - full * sh.ut;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_plan_kernel(const PagedPara
     } else if (i < N) {
       static_cast<Seq&>(q) = i == tid ? mine : sequence(i - NG, bad);  // (without groups the first look at it)
       if (q.qn > 0) {
-        const int g = i == tid ? my_group : NG > 0 ? group_of(i - NG) : -1;
+        const int g = i == tid ? my_group : NG > 0 && in_group(q) ? group_of(i - NG) : -1;
         const int n = g >= 0 ? keys[g] : 0;
         q.row = i - NG;
         q.page0 = n >> p.page_log2;

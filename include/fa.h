@@ -487,7 +487,7 @@ size_t fa_fwd_paged_workspace_size(int d);
  *   prefix_lens in [num_groups] int32, >= 0: the first prefix_lens[g] keys and
  *                  values are the same for all sequences of group g (the same
  *                  pages, or copies).  They are read from the pages of the first
- *                  one that has new tokens
+ *                  one that has new tokens and keys
  *   others    as in fa_fwd_paged, which see
  *   workspace fa_fwd_paged_shared_workspace_size(T, S, num_groups, Hq, d) bytes,
  *             256-byte aligned, under fa_fwd_paged's rules: two fp32 rows for each
@@ -495,7 +495,8 @@ size_t fa_fwd_paged_workspace_size(int d);
  *
  * Any prefix_lens[g] that is true is right: what is computed once is cut to the
  * keys that every sequence of the group has in front of its new tokens (with
- * causal = 0: has), and to whole pages, and is nothing where that costs no less
+ * causal = 0: has; one with kv_lens 0, as fa_paged_extend leaves it out, has no
+ * part in that), and to whole pages, and is nothing where that costs no less
  * (a group of one, long chunks that fill the tensor cores by themselves); the
  * other keys are each sequence's own.  What is counted is the keys' work alone:
  * a small batch, to which sharing saves less than some 10 us, is faster in

@@ -11,7 +11,7 @@ from tests.gpu_util import require_gpu
 from tests.test_gpu_norm_rope import status
 from tests.test_gpu_paged import check, reference
 from tests.test_gpu_paged_shared import batch, call
-from tests.test_gpu_paged_tables import State
+from tests.test_gpu_paged_tables import State, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,55 @@ def test_pages_outside_of_the_pool_among_many():
     s.extend(list(range(700)), [1 + i % 9 for i in range(700)])
     s.extend([650], [1])
     s.extend([r for r in range(700) if r != 650], [20] * 699)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hk,d,dead,seqs", [
+    (8, 2, 64, (3,), [(1, 5 + i) for i in range(9)]),
+    (8, 2, 128, (0, 4, 8), [(1, 5 + i) for i in range(9)]),                            # the first and the last one
+    (4, 1, 64, (0, 1, 30, 31, 32, 69), [(1, 200 - i) for i in range(70)]),             # 280 rows, two units of them
+    (8, 2, 64, (0, 4, 9), [(40, 40), (1, 3), (3, 3), (1, 9), (9, 9), (2, 2)] + [(1, 4)] * 3 + [(150, 150)]),  # chunks
+    (32, 1, 64, (1,), [(1, 40), (1, 2), (1, 30)]),
+    (64, 1, 128, (1,), [(1, 4)] * 7),
+])
+def test_a_sequence_that_was_left_out_keeps_no_group_from_sharing(Hq, Hk, d, dead, seqs, causal):
+    """Tokens of a sequence without keys (its pages were not there) see nothing, and the keys of the others are
+    shared all the same: those of the first that has some count, as each has copies of its own that differ."""
+    q, pages, table, cu, lens, starts, prefix = batch([(1280, seqs), (0, [(1, 70)])], Hq, Hk, d, 16, False)
+    live = [s for s in range(len(seqs)) if s not in dead]
+    for s in dead:
+        lens[s] = 0
+        table[s] = -7
+    apart, at, n = table.clone(), pages[0].shape[0], 1280 // 16
+    extra = [torch.randn(n * (len(live) - 1), *p.shape[1:], device="cuda").bfloat16() for p in pages]
+    for s in live[1:]:
+        apart[s, :n] = torch.arange(at, at + n)
+        at += n
+    pages = [torch.cat([p, e]) for p, e in zip(pages, extra)]
+    o, lse = call((q, pages, apart, cu, lens, starts, prefix), scale=0.11, causal=causal)
+    assert status() == fa.FA_OK
+    check(o, lse, reference(q, pages, table, cu, lens, 0.11, causal))
+
+
+def test_a_pool_that_runs_out_keeps_no_group_from_sharing():
+    """Six requests behind a prompt, pages for five of them: the sixth is left out of the step, the others share."""
+    page, max_pages, n, P = 16, 100, 64, 6 * 100
+    lens, table = ints([0] + [n * page] * 6), torch.full((7, max_pages), -5, dtype=torch.int32, device="cuda")
+    pool = fa.paged_pool(P)
+    free = ints(list(range(P - 1, n + 6 * n - 1, -1)))
+    pool[0] = 5                                   # five pages are left
+    pool[2:7] = free[:5]
+    for r in range(1, 7):                         # each with a copy that differs: the first one's counts
+        table[r, :n] = torch.arange((r - 1) * n, r * n, dtype=torch.int32)
+    g = torch.Generator().manual_seed(3)
+    pages = [torch.randn(P, 2, page, 64, generator=g).bfloat16().cuda() for _ in "kv"]
+    q = torch.randn(6, 8, 64, generator=g).bfloat16().cuda()
+    cu, kv, pt, _, slots = fa.paged_extend(ints([1, 2, 3, 4, 5, 6]), ints([1] * 6), lens, table, pool, page, 6)
+    assert status() == fa.FA_ERR_DEVICE_INDEX
+    assert kv.tolist() == [n * page + 1] * 5 + [0] and slots.tolist()[5] == -1
+    o, lse = fa.paged_forward_shared(q, *pages, pt, cu, kv, ints([0, 6]), ints([n * page]), scale=0.2)
+    assert status() == fa.FA_OK
+    want = pt.cpu()
+    want[:5, :n] = want[0, :n]
+    want[5] = -7
+    check(o, lse, reference(q, pages, want, cu.cpu(), kv.cpu(), 0.2, True))

@@ -675,8 +675,8 @@ def paged_extend(requests, new_lens, request_lens, request_table, pool, page_siz
     requests' state and brought up to date.  Returns ``(cu_seqlens [S + 1], kv_lens [S], page_table [S, max_pages],
     positions [tokens], slots [tokens] int64)`` for the other calls; ``out`` gives tensors to write to (any of the
     last two may be None: not wanted), as a captured step does.  Of ``page_table`` only entries in use are written.
-    A sequence that finds no room has ``kv_lens`` 0 and leaves its request as it was.  Pages that requests share are
-    full ones."""
+    A sequence that finds no room has ``kv_lens`` 0 and leaves its request as it was.  Rows behind the last sequence
+    (all of them in a step without any) have position 0 and slot -1.  Pages that requests share are full ones."""
     where = _elsewhere(requests, stream)
     if where is not None:
         with where:
@@ -702,6 +702,10 @@ def paged_extend(requests, new_lens, request_lens, request_table, pool, page_siz
                                         page_size, max_pages, torch._C._cuda_getCurrentRawStream(dev))
     if st != FA_OK:
         raise FaError(st, "fa_paged_extend")
+    if S == 0:  # (the call did nothing: all rows are behind the last sequence)
+        for t, value in ((cu, 0), (positions, 0), (slots, -1)):
+            if t is not None:
+                t.fill_(value)
     return cu, kv, pages, positions, slots
 
 

@@ -416,7 +416,8 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  * FA_ERR_DEVICE_INDEX.
  *
  * page_size and max_pages are the cache's; num_pages <= 2^30, S <= 4096 and R <=
- * 16384 (FA_ERR_UNSUPPORTED above).  S = 0 does nothing.
+ * 16384 (FA_ERR_UNSUPPORTED above).  S = 0 does nothing, and writes no output
+ * (the Python helper fills in those of a step whose rows belong to no sequence).
  */
 int fa_paged_extend(const int* requests, const int* new_lens, int* request_lens, int* request_table, int* pool,
                     int* cu_seqlens, int* kv_lens, int* page_table, int* positions, long long* slots, int T, int S,

@@ -3,6 +3,7 @@
 Tolerances are those of tests/test_gpu_paged.py (its ``check``); tables are whole numbers and equal the plain form's.
 """
 
+import numpy as np
 import pytest
 import torch
 
@@ -11,7 +12,7 @@ from tests.gpu_util import require_gpu
 from tests.test_gpu_norm_rope import status
 from tests.test_gpu_paged import check, reference
 from tests.test_gpu_paged_shared import batch, call
-from tests.test_gpu_paged_tables import State, ints
+from tests.test_gpu_paged_tables import OLD, State, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +123,28 @@ def test_a_pool_that_runs_out_keeps_no_group_from_sharing():
     want[:5, :n] = want[0, :n]
     want[5] = -7
     check(o, lse, reference(q, pages, want, cu.cpu(), kv.cpu(), 0.2, True))
+
+
+@pytest.mark.parametrize("tokens", [0, 1, 300])
+def test_a_step_without_sequences(tokens):
+    """Its rows are all behind the last sequence."""
+    s = State([20, 0], 4, 16, 9)
+    got = s.extend([], [], tokens=tokens)         # (into tensors that hold the step before's values)
+    assert got[0].tolist() == [0] and (got[3] == 0).all() and (got[4] == -1).all()
+    s.extend([], [], tokens=tokens, wanted=(False, True))
+    s.extend([], [], tokens=tokens, wanted=(True, False))
+    torch.full((4096,), OLD, dtype=torch.int64, device="cuda")   # what the next tensors may be made of
+    cu, kv, table, positions, slots = fa.paged_extend(ints([]), ints([]), s.lens, s.table, s.pool, 16, tokens)
+    assert cu.tolist() == [0] and kv.shape == (0,) and table.shape == (0, 4)
+    assert positions.tolist() == [0] * tokens and slots.tolist() == [-1] * tokens
+    out = (ints([OLD]), ints([]), ints(np.zeros((0, 4))), ints([OLD] * tokens),
+           torch.full((tokens,), OLD, dtype=torch.int64, device="cuda"))
+    none = ints([])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.paged_extend(none, none, s.lens, s.table, s.pool, 16, tokens, out=out, stream=torch.cuda.current_stream())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out[0].tolist() == [0] and (out[3] == 0).all() and (out[4] == -1).all()
+    s.release([])

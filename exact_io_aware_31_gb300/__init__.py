@@ -23,7 +23,6 @@ Tensor helpers: :func:`forward`, :func:`forward_fp8`, :func:`backward`, :func:`d
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 __all__ = [
@@ -468,10 +467,21 @@ def _room_for(size, device, d):
     return need
 
 
-@functools.lru_cache(maxsize=4096)
+_shared_rooms = {}
+
+
 def _shared_room(T, S, groups, Hq, d, device):
-    """Workspace bytes of :func:`paged_forward_shared` on the current device, asked for once for each batch shape."""
-    return load_library().fa_fwd_paged_shared_workspace_size(T, S, groups, Hq, d)
+    """Workspace bytes of :func:`paged_forward_shared` on the current device, asked for once for each batch shape (at
+    most 4096 of them are kept)."""
+    key = T, S, groups, Hq, d, device
+    need = _shared_rooms.get(key)
+    if need is None:
+        need = load_library().fa_fwd_paged_shared_workspace_size(T, S, groups, Hq, d)
+        if need:  # (0: refused by the call itself, or nothing to do)
+            if len(_shared_rooms) >= 4096:
+                _shared_rooms.clear()
+            _shared_rooms[key] = need
+    return need
 
 
 def _room(workspace, device):

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const TablesParams 
   // no slot (the caller writes to its own cache by them), and each entry in use is looked at below.
   auto is_page = [&](int x) { return (unsigned)x < (unsigned)p.num_pages; };
   bool lost = false;
-  const long long items = (long long)pieces + (T + kTokens - 1) / kTokens;
+  const long long items = (long long)pieces + (T + (long long)kTokens - 1) / kTokens;  // (T goes up to 2^31 - 1)
   for (long long i = (long long)blockIdx.x * kWarps + tid / 32; i < items; i += (long long)gridDim.x * kWarps) {
     if (i < pieces) {
       const int s = find(seq.piece, S, (int)i), r = seq.request[s];
@@ -328,7 +328,8 @@ cudaError_t launch(K kern, const TablesParams& p, int sms, long long items, cuda
 
 // A block a sixteen pieces or groups of tokens that there may be.
 cudaError_t launch_paged_extend(const TablesParams& p, int sms, cudaStream_t stream) {
-  const long long items = (long long)p.S * ((p.max_pages + kPiece - 1) / kPiece) + (p.T + kTokens - 1) / kTokens;
+  const long long items =
+      (long long)p.S * ((p.max_pages + kPiece - 1) / kPiece) + (p.T + (long long)kTokens - 1) / kTokens;
   return launch(extend_kernel, p, sms, items, stream);
 }
 

@@ -148,3 +148,15 @@ def test_a_step_without_sequences(tokens):
     torch.cuda.synchronize()
     assert out[0].tolist() == [0] and (out[3] == 0).all() and (out[4] == -1).all()
     s.release([])
+
+
+@pytest.mark.parametrize("tokens", [2 ** 31 - 1, 2 ** 31 - 127, 2 ** 31 - 128])
+def test_the_most_rows(tokens):
+    """A count of rows next to 2^31, maps not wanted: the tables are written."""
+    s = State([20, 0, 64, 33], 8, 16, 24)
+    batch, new = [2, -1, 0, 3], [3, 0, 20, 1]
+    out = (ints([OLD] * 5), ints([OLD] * 4), ints(np.full((4, 8), OLD)), None, None)
+    fa.paged_extend(ints(batch), ints(new), s.lens, s.table, s.pool, 16, tokens, out=out)
+    want = s.plain.extend(batch, new, 24, np.full((4, 8), OLD))
+    assert all(np.array_equal(g.cpu().numpy(), w) for g, w in zip(out[:3], want[:3]))
+    s.same()

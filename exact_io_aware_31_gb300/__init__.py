@@ -696,13 +696,13 @@ def paged_extend(requests, new_lens, request_lens, request_table, pool, page_siz
     dev = requests.get_device()
     req, lens, table, pool_at, S, R, num_pages, max_pages = _tables_args(requests, request_lens, request_table, pool, dev)
     new = _flat(new_lens, "new_lens", (S,), i32, dev)
+    if not 0 <= tokens < 1 << 31:
+        raise ValueError("tokens must be in 0 .. 2^31 - 1")
     if out is None:
         out = (torch.empty(S + 1, dtype=i32, device=requests.device), torch.empty(S, dtype=i32, device=requests.device),
                torch.empty(S, max_pages, dtype=i32, device=requests.device),
                torch.empty(tokens, dtype=i32, device=requests.device),
                torch.empty(tokens, dtype=torch.int64, device=requests.device))
-    if not 0 <= tokens < 1 << 31:
-        raise ValueError("tokens must be in 0 .. 2^31 - 1")
     cu, kv, pages, positions, slots = out
     st = load_library().fa_paged_extend(req, new, lens, table, pool_at, _flat(cu, "cu_seqlens", (S + 1,), i32, dev),
                                         _flat(kv, "kv_lens", (S,), i32, dev),

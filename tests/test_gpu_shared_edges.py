@@ -160,3 +160,13 @@ def test_the_most_rows(tokens):
     want = s.plain.extend(batch, new, 24, np.full((4, 8), OLD))
     assert all(np.array_equal(g.cpu().numpy(), w) for g, w in zip(out[:3], want[:3]))
     s.same()
+
+
+@pytest.mark.parametrize("tokens", [-1, 2 ** 31])
+def test_rows_that_cannot_be_are_refused_before_anything_is_made(tokens):
+    s = State([20], 4, 16, 9)
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    with pytest.raises(ValueError):
+        fa.paged_extend(s.lens, s.lens, s.lens, s.table, s.pool, 16, tokens)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    s.same()

@@ -256,14 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) release_kernel(const TablesParams
       const int want = p.lens ? __ldg(p.lens + s) : 0;
       const bool in = r < p.R && seq.owner[r] == s;
       const int len = in ? *reinterpret_cast<volatile int*>(p.request_lens + r) : 0;
-      if (in && len >= 0 && len <= cap && want >= 0 && want <= len) {
+      const int kept = in && p.kept_pages ? __ldg(p.kept_pages + r) : 0;
+      if (in && len >= 0 && len <= cap && want >= 0 && want <= len && kept >= 0 && kept <= p.max_pages) {
         keep = want;
-        first = (int)((keep + (1ll << lg) - 1) >> lg);
-        if (p.kept_pages) {
-          const int kept = __ldg(p.kept_pages + r);
-          bad = bad || kept < 0 || kept > p.max_pages;
-          first = first > kept ? first : kept;
-        }
+        first = max((int)((keep + (1ll << lg) - 1) >> lg), kept);
         n = (int)((len + (1ll << lg) - 1) >> lg) - first;
         if (n < 0) n = 0;
       } else {

@@ -409,11 +409,11 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
  *   pool            in, out  the pages behind those kept, so that fa_paged_extend of
  *                   the same batch would take them in the same order again
  *
- * A request that is not in 0 .. R-1, stands in front already or is to keep what
- * it does not have stays as it is; where more pages come back than the pool has
- * room for (some came back before) nothing is done.  Both, and a page outside of
- * the pool in the table (which comes back as the others do), record
- * FA_ERR_DEVICE_INDEX.
+ * A request that is not in 0 .. R-1, stands in front already, is to keep what it
+ * does not have or has a count in kept_pages outside of 0 .. max_pages stays as
+ * it is; where more pages come back than the pool has room for (some came back
+ * before) nothing is done.  Both, and a page outside of the pool in the table
+ * (which comes back as the others do), record FA_ERR_DEVICE_INDEX.
  *
  * page_size and max_pages are the cache's; num_pages <= 2^30, S <= 4096 and R <=
  * 16384 (FA_ERR_UNSUPPORTED above).  S = 0 does nothing, and writes no output

@@ -168,7 +168,9 @@ class Tables:
             if r < 0:
                 continue
             keep = 0 if keep_lens is None else keep_lens[s]
-            if r >= len(lens) or r in seen or not 0 <= keep <= lens[r] <= self.table.shape[1] * self.page:
+            most = self.table.shape[1]
+            if (r >= len(lens) or r in seen or not 0 <= keep <= lens[r] <= most * self.page
+                    or kept_pages is not None and not 0 <= kept_pages[r] <= most):
                 self.bad = True
                 seen.add(r)
                 continue

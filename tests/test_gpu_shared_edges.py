@@ -170,3 +170,19 @@ def test_rows_that_cannot_be_are_refused_before_anything_is_made(tokens):
         fa.paged_extend(s.lens, s.lens, s.lens, s.table, s.pool, 16, tokens)
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
     s.same()
+
+
+@pytest.mark.parametrize("kept", [-1, 5, 2 ** 31 - 1, -2 ** 31])
+def test_counts_of_shared_pages_that_cannot_be(kept):
+    """A request whose count is outside of its row stays as it was; the others give their pages back."""
+    s = State([20, 0, 64, 33], 4, 16, 16)
+    s.release([0, 2, 3], [5, 0, 40], [0, 0, kept, 1])          # keeps more than it has, besides
+    s.release([2, 0, 3, 1], [16, 0, 1, 0], [0, kept, kept, 4])
+    s.release([0, 3], None, [kept, 0, 0, 1])
+    s.release([0, 3], None, [4, 0, 0, 0])                       # as many as a row may have: none is its own
+    s.release([0, 1])
+
+
+def test_a_count_of_shared_pages_of_no_sequence_has_no_part():
+    s = State([20, 0, 64, 33], 4, 16, 16)
+    s.release([0, -1], [5, 0], [0, -3, 99, 1])

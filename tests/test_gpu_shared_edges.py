@@ -186,3 +186,59 @@ def test_counts_of_shared_pages_that_cannot_be(kept):
 def test_a_count_of_shared_pages_of_no_sequence_has_no_part():
     s = State([20, 0, 64, 33], 4, 16, 16)
     s.release([0, -1], [5, 0], [0, -3, 99, 1])
+
+
+def test_a_captured_call_keeps_its_workspace():
+    """Calls without a workspace in two captured graphs, replayed among each other's and other memory's use."""
+    xs = [batch([(1280, [(1, 5 + i) for i in range(9)])], 8, 2, 128, 16, False),
+          batch([(1024, [(1, 3)] * 4), (512, [(2, 40), (3, 9), (1, 130)])], 4, 2, 64, 16, False, seed=20)]
+    xs = [tuple([p.cuda() for p in t] if isinstance(t, list) else t.cuda() for t in x) for x in xs]
+    refs = [reference(x[0], x[1], *(t.cpu() for t in x[2:5]), 0.11, True) for x in xs]
+    outs, graphs = [], []
+    for order in ((0, 1, 0), (1, 0, 1)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            made = []
+            for i in order:
+                made.append((i, call(xs[i], scale=0.11)))
+                torch.full((1 << 22,), 3, dtype=torch.uint8, device="cuda")   # takes what was given back
+        graphs.append(graph)
+        outs.append(made)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for made in outs:
+            for _, (o, lse) in made:
+                o.zero_(), lse.zero_()
+        torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(255)     # another pool's memory
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        eager = call(xs[0], scale=0.11)
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.current_stream().wait_stream(side)
+        assert status() == fa.FA_OK
+        for i, (o, lse) in (*outs[0], *outs[1], (0, eager)):
+            check(o, lse, refs[i])
+
+
+def test_partial_rows_past_2_31_floats():
+    """140000 single tokens of 64 heads behind one prompt: places of partial rows, and bytes of the workspace, that 32
+    bits do not hold; sequences from both ends and between are compared."""
+    S, Hq, Hk, d, page, prompt = 140000, 64, 2, 128, 16, 256
+    assert 2 * S * Hq * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    n = prompt // page
+    pages = [rand(S + n, Hk, page, d) for _ in "kv"]
+    q = rand(S, Hq, d)
+    table = torch.cat([torch.arange(n, device="cuda").expand(S, n), n + torch.randperm(S, generator=g, device="cuda")[:, None]],
+                      1).int().contiguous()
+    lens = (prompt + 1 + torch.arange(S, device="cuda") % page).int()
+    cu = torch.arange(S + 1, device="cuda").int()
+    o, lse = fa.paged_forward_shared(q, *pages, table, cu, lens, ints([0, S]), ints([prompt]), scale=0.2, max_q=1)
+    assert status() == fa.FA_OK
+    some = torch.tensor([0, 1, S - 1, S - 2, *range(5, S, S // 40)], device="cuda")
+    used = torch.cat([torch.arange(n, device="cuda"), table[some, n].long()])
+    own = torch.cat([torch.arange(n).expand(len(some), n), n + torch.arange(len(some))[:, None]], 1).int()
+    check(o[some], lse[some], reference(q[some], [p[used] for p in pages], own, torch.arange(len(some) + 1).int(),
+                                        lens[some].cpu(), 0.2, True))

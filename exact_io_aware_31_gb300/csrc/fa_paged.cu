@@ -36,7 +36,8 @@
 // SHORT kernels hold only the last form: the host takes them where it was told
 // that chunks are short; a longer chunk is then a row of small units.
 // SHARED kernels take their units from a list (fa_paged_shared.cu), on as many of the
-// CTAs as the list says, and leave whole rows' partial outputs to another merge.
+// CTAs as the list says, and leave whole rows' partial outputs to another merge.  (Their
+// 168 registers are one too few: a word is stored to local memory, and 24 places read it.)
 //
 // Rounding: scores, maxima, sums and O are fp32.  P is rounded to bf16 once, as the
 // MMA takes it (its sum takes the fp32 values), for single tokens, too, which run the

@@ -265,7 +265,9 @@ __host__ __device__ inline int parts_of_keys(int keys, int& part) {
 // Parts that there is room for, of kPartRows rows (or half as many of twice the rows).  An entry
 // of n keys in several parts of some L has at most 4/3 n / L; with W keys times heads in all and
 // part_keys()' lengths these are at most 4/3 * 16 * 0.8 an SM for those that begin in the first
-// four fifths, and 4/3 * 32 * 0.2 for the others: 25.6.
+// four fifths, and 4/3 * 32 * 0.2 for the others: 25.6.  (There is room for entries cut at every
+// L keys, too, up to 2 n / L parts each, 38.4 an SM, and for sums in fp32 that are off by a
+// fifth: at d = 128 26 MB more of workspace than equal parts and exact sums need.)
 constexpr int kMaxParts = 46;
 constexpr int kPartRows = 16;
 inline __host__ __device__ int shared_parts(int sms) { return kMaxParts * sms; }

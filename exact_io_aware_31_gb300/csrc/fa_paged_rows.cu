@@ -33,6 +33,9 @@
 //
 // Rounding as in paged_kernel: scores, maxima, sums and O in fp32, P to bf16 once for the
 // second product.
+//
+// Registers: 168, what the room for two CTAs (or one of eleven warps) leaves a thread; of it
+// d = 128 with two row tiles spills 20 bytes, with one 4, d = 64 with one 8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

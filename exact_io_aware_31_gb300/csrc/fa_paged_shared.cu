@@ -20,12 +20,12 @@
 //   shared_merge_kernel  the rows that have parts
 //
 // Measured (GB300; in brackets fa_fwd_paged on the same batch): 64 single tokens, 8192
-// shared keys and up to 512 of their own, 32 + 8 heads, d = 128: 46 us (299); 256 behind
+// shared keys and up to 512 of their own, 32 + 8 heads, d = 128: 47 us (299); 256 behind
 // 2 x 2048, up to 1024 of their own: 130 (281), 5.3 TB/s; 128 behind 1021, 16 heads, d = 64:
 // 28 (90); 48 x 5 behind 4 prompts of up to 4093, 20 + 4 heads, d = 128: 41 (49); 4 behind
 // 512: 13 (13.8); 8 x 509 tokens behind 16384: 703 (711), both at the tensor cores' rate.
-// Small batches are a chain: plan 5 us (8 with more than 256 entries), beginnings and ends
-// of units 6 us each, merge 6 us.
+// Small batches are a chain: plan 5 us (9 with more than 256 entries, 13 with 514, 18 with
+// 1026), beginnings and ends of units 6 us each, merge 6 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -509,7 +509,8 @@ size_t fa_fwd_paged_workspace_size(int d);
  * FA_ERR_DEVICE_INDEX; rows of sequences that two groups then hold are not
  * specified.
  *
- * Four launches (three where T * Hq / Hk is at most 16 or 32).  Results are the
+ * Four launches; three where T * Hq / Hk is at most 16 or 32 (all rows are the
+ * kernel's for few rows), or Hq / Hk is above 32 (none are).  Results are the
  * same bits on every run.  In the last bits a row depends on the other sequences
  * of its group, and on the lengths of the whole batch (which say how keys are cut
  * into parts).  max_q says as well which of two forms steps of a few tokens take:

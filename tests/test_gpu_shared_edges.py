@@ -3,6 +3,8 @@
 Tolerances are those of tests/test_gpu_paged.py (its ``check``); tables are whole numbers and equal the plain form's.
 """
 
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -242,3 +244,25 @@ def test_partial_rows_past_2_31_floats():
     own = torch.cat([torch.arange(n).expand(len(some), n), n + torch.arange(len(some))[:, None]], 1).int()
     check(o[some], lse[some], reference(q[some], [p[used] for p in pages], own, torch.arange(len(some) + 1).int(),
                                         lens[some].cpu(), 0.2, True))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_any_mix_of_groups_with_sequences_left_out(seed):
+    rng = random.Random(700 + seed)
+    d, page = rng.choice([64, 128]), rng.choice([16, 32, 128])
+    Hk = rng.choice([1, 2, 3])
+    Hq = Hk * rng.choice([1, 4, 7, 16, 40])
+    groups = []
+    for _ in range(rng.randint(1, 4)):
+        most = rng.choice([1, 1, 5, 60])
+        seqs = [(q, q + rng.randint(0, 150)) for q in (rng.randint(0, most) for _ in range(rng.randint(2, 50)))]
+        groups.append((rng.choice([0, rng.randint(200, 4000)]), seqs))
+    groups.append((0, [(1, 30)]))
+    causal = rng.random() < 0.8
+    x = batch(groups, Hq, Hk, d, page, rng.random() < 0.5, seed=seed)
+    for s in range(len(x[4]) - 1):
+        if rng.random() < 0.25:
+            x[4][s] = 0
+    o, lse = call(x, scale=0.13, causal=causal, max_q=rng.choice([0, 1, 60]))
+    assert status() == fa.FA_OK
+    check(o, lse, reference(*x[:5], 0.13, causal))
